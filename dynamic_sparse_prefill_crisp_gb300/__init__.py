@@ -68,6 +68,20 @@ class LayerViews(ctypes.Structure):
                  "rowbits", "counts", "order")]
 
 
+class KVCache(ctypes.Structure):
+    """A paged 8-bit key/value cache (make_kv_cache); keeps its tensors alive."""
+    _fields_ = [("batch", ctypes.c_int32), ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+class Tokens(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("tok_stride", ctypes.c_int64)]
+
+
 def lib():
     """The loaded libcrisp.so; raises if it has not been built."""
     global _lib
@@ -111,6 +125,14 @@ def load_library(path):
     L.crisp_dense_prefill.argtypes = [P(Shape), vp, vp, vp, vp, vp, sz, st]
     L.crisp_layer_views_get.argtypes = [P(Shape), vp, P(LayerViews)]
     L.crisp_prefill_layer.argtypes = [P(Shape), P(Params), vp, vp, vp, vp, vp, sz, st]
+    i32 = ctypes.c_int32
+    L.crisp_kv_append_workspace_size.argtypes = [P(KVCache), P(sz)]
+    L.crisp_decode_workspace_size.argtypes = [P(KVCache), i32, i32, i32, P(sz)]
+    L.crisp_kv_evict_workspace_size.argtypes = [P(KVCache), i32, P(sz)]
+    L.crisp_kv_append.argtypes = [P(KVCache), P(Tokens), P(Tokens), i32, vp, vp, sz, st]
+    L.crisp_decode_attention.argtypes = [P(KVCache), i32, i32, ctypes.c_float, P(Tokens), P(Tokens), vp, vp, vp, sz,
+                                         st]
+    L.crisp_kv_evict.argtypes = [P(KVCache), P(KVCache), vp, i32, i32, i32, vp, vp, vp, sz, st]
     L.crisp_read_status.argtypes = [vp, st, P(ctypes.c_int)]
     L.crisp_status_string.argtypes = [ctypes.c_int]
     L.crisp_status_string.restype = ctypes.c_char_p
@@ -121,7 +143,8 @@ def load_library(path):
                  "crisp_build_mask", "crisp_sparse_prefill", "crisp_sparse_prefill_mask", "crisp_dense_prefill",
                  "crisp_layer_views_get", "crisp_prefill_layer", "crisp_read_status",
                  "crisp_host_pipeline_create", "crisp_host_pipeline_destroy", "crisp_prefill_layer_host",
-                 "crisp_wait_selftest"):
+                 "crisp_kv_append_workspace_size", "crisp_decode_workspace_size", "crisp_kv_evict_workspace_size",
+                 "crisp_kv_append", "crisp_decode_attention", "crisp_kv_evict", "crisp_wait_selftest"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -331,6 +354,130 @@ def prefill_layer_host(pipeline, shape, params, q_host, k_host, v_host, out_host
                                           _ptr(k_host), _ptr(v_host), _ptr(out_host), _ptr(q), _ptr(k), _ptr(v),
                                           _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)),
            "crisp_prefill_layer_host")
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def make_kv_cache(k, v, k_scale, v_scale, table, lens) -> KVCache:
+    """The cache that these CUDA tensors hold: k, v float8_e4m3fn (or uint8
+    codes) [num_pages][hkv][128][128] of the same strides, each head's page
+    contiguous; k_scale, v_scale fp32 [num_pages][hkv]; table int32
+    [batch][max_pages] of page ids; lens int32 [batch] of tokens held. The
+    structure keeps the tensors alive; their contents may change between calls."""
+    import torch
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    _need(k.dim() == 4 and k.shape == v.shape and k.shape[2:] == (B, D) and k.dtype in codes and v.dtype in codes,
+          "make_kv_cache: k and v must be 8-bit [num_pages][hkv][128][128]")
+    _need(k.stride() == v.stride() and k.stride()[2:] == (D, 1),
+          "make_kv_cache: k and v must share their strides and hold each head's page contiguously")
+    num, hkv = k.shape[:2]
+    for s in (k_scale, v_scale):
+        _need(s.shape == (num, hkv) and s.dtype == torch.float32 and s.is_contiguous(),
+              "make_kv_cache: the scales must be contiguous fp32 [num_pages][hkv]")
+    _need(table.dim() == 2 and table.dtype == torch.int32 and table.is_contiguous(),
+          "make_kv_cache: table must be contiguous int32 [batch][max_pages]")
+    _need(lens.shape == table.shape[:1] and lens.dtype == torch.int32 and lens.is_contiguous(),
+          "make_kv_cache: lens must be contiguous int32 [batch]")
+    keep = (k, v, k_scale, v_scale, table, lens)
+    _need(all(t.device == k.device for t in keep), "make_kv_cache: the tensors must be on one device")
+    c = KVCache(table.shape[0], hkv, D, B, num, table.shape[1], k.stride(0), k.stride(1), k.data_ptr(), v.data_ptr(),
+                k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr())
+    c.tensors = keep
+    return c
+
+
+def _tokens(name, t, cache, heads):
+    import torch
+    _need(t.dim() == 4 and t.shape[0] == cache.batch and t.shape[1] == heads and t.shape[3] == D and t.stride(3) == 1
+          and t.dtype == torch.bfloat16, f"{name} must be bf16 [batch][heads][tokens][128], features contiguous")
+    return Tokens(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _rows(name, t, cache, dtype):
+    _need(t.shape == (cache.batch, cache.hkv, cache.max_pages * B) and t.dtype == dtype and t.is_contiguous(),
+          f"{name} must be contiguous {dtype} [batch][hkv][128 * max_pages]")
+
+
+def _on_device(cache, *tensors):
+    """The calls run on the current device and stream: everything has to be there."""
+    import torch
+    dev = cache.tensors[0].device
+    _need(dev.type == "cuda" and dev.index == torch.cuda.current_device() and
+          all(t is None or t.device == dev for t in tensors),
+          "the cache and every tensor of the call must be on the current CUDA device")
+
+
+def kv_append_workspace_size(cache: KVCache) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().crisp_kv_append_workspace_size(ctypes.byref(cache), ctypes.byref(n)),
+           "crisp_kv_append_workspace_size")
+    return n.value
+
+
+def decode_workspace_size(cache: KVCache, hq: int, q_len: int = 1, weights: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().crisp_decode_workspace_size(ctypes.byref(cache), hq, q_len, int(weights), ctypes.byref(n)),
+           "crisp_decode_workspace_size")
+    return n.value
+
+
+def kv_evict_workspace_size(cache: KVCache, keep: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().crisp_kv_evict_workspace_size(ctypes.byref(cache), keep, ctypes.byref(n)),
+           "crisp_kv_evict_workspace_size")
+    return n.value
+
+
+def kv_append(cache, k_new, v_new, ws, new_lens=None, stream=None):
+    """Writes bf16 [batch][hkv][n_new][128] tokens into the cache, the last of
+    sequence b at position lens[b] - 1 (advance lens first); new_lens: int32
+    [batch], how many of the n_new tokens each sequence has (default: all)."""
+    import torch
+    kt, vt = _tokens("kv_append: k_new", k_new, cache, cache.hkv), _tokens("kv_append: v_new", v_new, cache, cache.hkv)
+    _need(k_new.shape == v_new.shape, "kv_append: k_new and v_new must have one shape")
+    _need(new_lens is None or (new_lens.shape == (cache.batch,) and new_lens.dtype == torch.int32 and
+                               new_lens.is_contiguous()), "kv_append: new_lens must be contiguous int32 [batch]")
+    _on_device(cache, k_new, v_new, ws, new_lens)
+    _check(lib().crisp_kv_append(ctypes.byref(cache), ctypes.byref(kt), ctypes.byref(vt), k_new.shape[2],
+                                 _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)), "crisp_kv_append")
+
+
+def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale=0.0, stream=None):
+    """Attention of the last q_len tokens of every sequence over the cache: q,
+    out bf16 [batch][hq][q_len][128]. With weights_out (fp32 [batch][hkv][128 *
+    max_pages]) each key's weight, summed over the kv head's rows, is added to
+    weights_in's (None: zeros; may be the same tensor)."""
+    import torch
+    hq, q_len = q.shape[1], q.shape[2]
+    qt, ot = _tokens("decode_attention: q", q, cache, hq), _tokens("decode_attention: out", out, cache, hq)
+    _need(out.shape == q.shape, "decode_attention: q and out must have one shape")
+    for name, t in (("weights_in", weights_in), ("weights_out", weights_out)):
+        if t is not None:
+            _rows(f"decode_attention: {name}", t, cache, torch.float32)
+    _on_device(cache, q, out, ws, weights_in, weights_out)
+    _check(lib().crisp_decode_attention(ctypes.byref(cache), hq, q_len, scale, ctypes.byref(qt), ctypes.byref(ot),
+                                        _ptr(weights_in), _ptr(weights_out), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "crisp_decode_attention")
+
+
+def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=None, kept=None, stream=None):
+    """Copies at most `keep` tokens of every sequence and kv head -- the first
+    `sink`, the last `recent`, and those of largest weight -- into new_cache's
+    pages, in their order, and sets its lens. new_weights (fp32) and kept (int32,
+    old positions) are [batch][hkv][128 * new_cache.max_pages]."""
+    import torch
+    _rows("kv_evict: weights", weights, cache, torch.float32)
+    if new_weights is not None:
+        _rows("kv_evict: new_weights", new_weights, new_cache, torch.float32)
+    if kept is not None:
+        _rows("kv_evict: kept", kept, new_cache, torch.int32)
+    _on_device(cache, *new_cache.tensors, weights, ws, new_weights, kept)
+    _check(lib().crisp_kv_evict(ctypes.byref(cache), ctypes.byref(new_cache), _ptr(weights), keep, sink, recent,
+                                _ptr(new_weights), _ptr(kept), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "crisp_kv_evict")
 
 
 def wait_selftest(ws, limit_ns, stream=None):

@@ -878,6 +878,190 @@ crisp_status crisp_prefill_layer_host(crisp_host_pipeline* pipeline, const crisp
 
 }  // extern "C"
 
+// ---------------------------------------------------------------------------
+// The paged 8-bit cache.
+namespace crisp {
+namespace {
+
+constexpr int kMaxPages = kMaxSeq / kB;  // entries of a table row
+
+crisp_status check_cache(const crisp_kv_cache* c) {
+  if (!c) return CRISP_ERR_INVALID_ARG;
+  if (c->head_dim != kD || c->block != kB) return CRISP_ERR_SHAPE;
+  if (c->batch < 0 || c->batch > kMaxBatch || c->hkv <= 0 || c->hkv > 4096) return CRISP_ERR_SHAPE;
+  if (c->num_pages <= 0 || c->max_pages <= 0 || c->max_pages > kMaxPages) return CRISP_ERR_SHAPE;
+  if (static_cast<int64_t>(c->batch) * c->max_pages * c->hkv > INT32_MAX) return CRISP_ERR_SHAPE;
+  for (int64_t st : {c->page_stride, c->head_stride})
+    if (st <= 0 || st % 16 != 0 || st > (int64_t(1) << 38)) return CRISP_ERR_ALIGN;
+  if (c->page_stride < kB * kD || (c->hkv > 1 && c->head_stride < kB * kD)) return CRISP_ERR_SHAPE;
+  if (c->batch == 0) return CRISP_OK;  // no sequences: nothing is addressed
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens) return CRISP_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(c->table, 4) || !aligned(c->lens, 4))
+    return CRISP_ERR_ALIGN;
+  return CRISP_OK;
+}
+
+// [batch][heads][tokens][128]; the stride of an axis of one entry is not used.
+crisp_status check_tokens(const crisp_tokens* t, int batch, int heads, int tokens) {
+  if (!t || !t->data) return CRISP_ERR_INVALID_ARG;
+  if (!aligned16(t->data)) return CRISP_ERR_ALIGN;
+  const int64_t strides[3] = {t->batch_stride, t->head_stride, t->tok_stride};
+  const int sizes[3] = {batch, heads, tokens};
+  for (int i = 0; i < 3; ++i) {
+    if (sizes[i] <= 1) continue;
+    if (strides[i] <= 0 || strides[i] % 8 != 0 || strides[i] > (int64_t(1) << 38)) return CRISP_ERR_ALIGN;
+    if (strides[i] < kD) return CRISP_ERR_SHAPE;
+  }
+  return CRISP_OK;
+}
+
+crisp_status check_cache_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return CRISP_ERR_WORKSPACE;
+  if (!aligned(ws, kAlign)) return CRISP_ERR_ALIGN;
+  return ws_bytes >= need ? CRISP_OK : CRISP_ERR_WORKSPACE;
+}
+
+crisp_status check_decode(const crisp_kv_cache* c, int hq, int q_len) {
+  crisp_status st = check_cache(c);
+  if (st != CRISP_OK) return st;
+  if (hq <= 0 || hq > 4096 || hq % c->hkv != 0 || q_len < 1 || q_len > kMaxQLen) return CRISP_ERR_SHAPE;
+  const int rows = hq / c->hkv * q_len;
+  if (rows > kMaxGroupRows) return CRISP_ERR_SHAPE;
+  const int64_t heads = static_cast<int64_t>(c->batch) * c->hkv;
+  if (heads * c->max_pages * decode_row_chunks(rows) > INT32_MAX || heads * (rows + c->max_pages) > INT32_MAX)
+    return CRISP_ERR_SHAPE;
+  return CRISP_OK;
+}
+
+// Whole pages of one head: [num_pages][hkv][128][128] bytes.
+crisp_status make_page_map(CUtensorMap* m, const void* ptr, const crisp_kv_cache& c) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return CRISP_ERR_CUDA;
+  cuuint64_t dims[4] = {kD, kB, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
+  // a single head's stride is not used, but has to be one the map accepts
+  cuuint64_t strides[3] = {kD, static_cast<cuuint64_t>(c.head_stride), static_cast<cuuint64_t>(c.page_stride)};
+  cuuint32_t box[4] = {kD, kB, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CRISP_OK : CRISP_ERR_ALIGN;
+}
+
+size_t evict_list_offset() { return align_up(sizeof(DevStatus)); }
+size_t evict_bytes(const crisp_kv_cache& c, int keep) {
+  return align_up(evict_list_offset() + static_cast<size_t>(c.batch) * c.hkv * align_up(static_cast<size_t>(keep) * 4));
+}
+
+}  // namespace
+}  // namespace crisp
+
+extern "C" {
+
+crisp_status crisp_kv_append_workspace_size(const crisp_kv_cache* cache, size_t* bytes) {
+  return traced("crisp_kv_append_workspace_size", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if (!bytes) return CRISP_ERR_INVALID_ARG;
+    *bytes = align_up(sizeof(DevStatus));
+    return CRISP_OK;
+  });
+}
+
+crisp_status crisp_decode_workspace_size(const crisp_kv_cache* cache, int32_t hq, int32_t q_len, int32_t with_weights,
+                                         size_t* bytes) {
+  return traced("crisp_decode_workspace_size", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_decode(cache, hq, q_len);
+    if (st != CRISP_OK) return st;
+    if (!bytes) return CRISP_ERR_INVALID_ARG;
+    *bytes = decode_layout(*cache, hq, q_len, with_weights != 0).total;
+    return CRISP_OK;
+  });
+}
+
+crisp_status crisp_kv_evict_workspace_size(const crisp_kv_cache* cache, int32_t keep, size_t* bytes) {
+  return traced("crisp_kv_evict_workspace_size", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if (!bytes || keep < 1 || keep > kMaxSeq) return CRISP_ERR_INVALID_ARG;
+    *bytes = evict_bytes(*cache, keep);
+    return CRISP_OK;
+  });
+}
+
+crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_tokens* k_new, const crisp_tokens* v_new,
+                             int32_t n_new, const int32_t* new_lens, void* ws, size_t ws_bytes, crisp_stream_t stream) {
+  return traced("crisp_kv_append", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if (n_new < 0 || n_new > cache->max_pages * kB) return CRISP_ERR_SHAPE;
+    if (n_new == 0 || cache->batch == 0) return CRISP_OK;  // no tokens
+    if ((st = check_tokens(k_new, cache->batch, cache->hkv, n_new)) != CRISP_OK) return st;
+    if ((st = check_tokens(v_new, cache->batch, cache->hkv, n_new)) != CRISP_OK) return st;
+    if (!aligned(new_lens, 4)) return CRISP_ERR_ALIGN;
+    if ((st = check_cache_ws(ws, ws_bytes, align_up(sizeof(DevStatus)))) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    return from_cuda(launch_kv_append(*cache, *k_new, *v_new, n_new, new_lens, status_of(ws), stream));
+  });
+}
+
+crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32_t hq, int32_t q_len, float scale,
+                                    const crisp_tokens* q, const crisp_tokens* out, const float* weights_in,
+                                    float* weights_out, void* ws, size_t ws_bytes, crisp_stream_t stream) {
+  return traced("crisp_decode_attention", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_decode(cache, hq, q_len);
+    if (st != CRISP_OK) return st;
+    if (!(scale >= 0.f) || std::isinf(scale)) return CRISP_ERR_INVALID_ARG;
+    if (weights_in && !weights_out) return CRISP_ERR_INVALID_ARG;
+    if (cache->batch == 0) return CRISP_OK;
+    if ((st = check_tokens(q, cache->batch, hq, q_len)) != CRISP_OK) return st;
+    if ((st = check_tokens(out, cache->batch, hq, q_len)) != CRISP_OK) return st;
+    if (!aligned16(weights_in) || !aligned16(weights_out)) return CRISP_ERR_ALIGN;
+    if ((st = check_cache_ws(ws, ws_bytes, decode_layout(*cache, hq, q_len, weights_out != nullptr).total)) != CRISP_OK)
+      return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return CRISP_ERR_CUDA;
+    KvMaps maps;
+    if ((st = make_page_map(&maps.k, cache->k, *cache)) != CRISP_OK) return st;
+    if ((st = make_page_map(&maps.v, cache->v, *cache)) != CRISP_OK) return st;
+    const float c = scale == 0.f ? 1.0f / std::sqrt(static_cast<float>(kD)) : scale;
+    return from_cuda(launch_decode(*cache, maps, hq, q_len, c, *q, *out, weights_in, weights_out,
+                                   static_cast<char*>(ws), sms, stream));
+  });
+}
+
+crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst, const float* weights, int32_t keep,
+                            int32_t sink, int32_t recent, float* new_weights, int32_t* kept, void* ws, size_t ws_bytes,
+                            crisp_stream_t stream) {
+  return traced("crisp_kv_evict", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(src);
+    if (st != CRISP_OK) return st;
+    if ((st = check_cache(dst)) != CRISP_OK) return st;
+    if (src->batch != dst->batch || src->hkv != dst->hkv) return CRISP_ERR_SHAPE;
+    if (keep < 1 || keep > dst->max_pages * kB || sink < 0 || recent < 0 ||
+        static_cast<int64_t>(sink) + recent > keep)
+      return CRISP_ERR_INVALID_ARG;
+    if (src->batch == 0) return CRISP_OK;
+    if (!weights || weights == new_weights) return CRISP_ERR_INVALID_ARG;
+    if (src->table == dst->table || src->lens == dst->lens) return CRISP_ERR_INVALID_ARG;  // written while read
+    if (!aligned16(weights) || !aligned16(new_weights) || !aligned(kept, 4)) return CRISP_ERR_ALIGN;
+    if ((st = check_cache_ws(ws, ws_bytes, evict_bytes(*src, keep))) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    // the kept positions go to the caller's array or, without one, to the workspace
+    int32_t* list = kept != nullptr ? kept : reinterpret_cast<int32_t*>(static_cast<char*>(ws) + evict_list_offset());
+    const int64_t stride = kept != nullptr ? static_cast<int64_t>(dst->max_pages) * kB
+                                           : static_cast<int64_t>(align_up(static_cast<size_t>(keep) * 4) / 4);
+    return from_cuda(launch_kv_evict(*src, *dst, weights, keep, sink, recent, new_weights, list, stride,
+                                     status_of(ws), stream));
+  });
+}
+
+}  // extern "C"
+
 namespace crisp {
 namespace {
 

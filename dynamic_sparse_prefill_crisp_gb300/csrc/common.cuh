@@ -62,6 +62,17 @@ __device__ __forceinline__ uint64_t q32(float p) {
   return x < kTwo23 ? static_cast<uint64_t>(q32_small(x)) : q32_large(x);
 }
 
+// Scale of a set of values held in e4m3: the smallest e >= kMinScaleExp with
+// amax <= 448 * 2^e (448 = 1.75 * 2^8 is e4m3's largest value).
+constexpr int kMinScaleExp = -100;
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+  return e < kMinScaleExp ? kMinScaleExp : e;
+}
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
 // Blocks are aligned at token 0; when 128 does not divide n the last block
 // is short: it holds tail_len(n) in [1, 128] tokens.
 inline int num_blocks(int n) { return (n + kB - 1) / kB; }
@@ -105,6 +116,29 @@ struct TmaMaps {
   CUtensorMap q, k, v, k64;  // k: 128-token boxes (proxy); k64, v: 64-token boxes (attention)
 };
 
+// The 8-bit cache.
+constexpr int kMaxBatch = 1024;
+constexpr int kMaxQLen = 16;
+constexpr int kMaxDecodeCtas = 304;   // 152 SMs x 2
+constexpr int kMaxGroupRows = 1024;   // query heads per kv head x q_len
+
+struct KvMaps {
+  CUtensorMap k, v;  // whole pages of one head: 128 tokens x 128 codes
+};
+
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of crisp_decode_attention (the status word comes first).
+struct DecodeLayout {
+  size_t part;     // fp32 [2 CTAs][rows of a chunk][128]  unfinished accumulators
+  size_t part_ml;  // float2 [2 CTAs][rows of a chunk]     their running maximum and sum
+  size_t lse;      // fp32 [items][rows of a chunk]        log2 of the sum, finished items
+  size_t scores;   // fp32 [batch][hkv][rows][128 max_pages]  scores in base 2 (weights only)
+  size_t total;
+};
+DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights);
+int decode_row_chunks(int rows);  // row chunks of a (sequence, kv head)
+
 // ---- launchers (one per translation unit); return cudaSuccess or the launch error
 cudaError_t launch_proxy(const crisp_shape& s, const TmaMaps& maps, float* pmap, char* ws, cudaStream_t st);
 cudaError_t launch_proxy_masses(const crisp_shape& s, const TmaMaps& maps, uint64_t* vmass, uint64_t* smass,
@@ -131,5 +165,14 @@ cudaError_t launch_build_mask(const crisp_shape& s, const uint8_t* route, const 
                               int32_t* order, char* ws, cudaStream_t st);
 cudaError_t launch_attention(const crisp_shape& s, const TmaMaps& maps, const uint32_t* rowbits,
                              const int32_t* order, void* out, char* ws, bool dense, cudaStream_t st);
+cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, int q_len, float scale,
+                          const crisp_tokens& q, const crisp_tokens& out, const float* weights_in, float* weights_out,
+                          char* ws, int sms, cudaStream_t st);
+cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
+                             const int32_t* new_lens, DevStatus* status, cudaStream_t st);
+// list: int32 [batch][hkv][list_stride], the kept positions (the caller's or in the workspace)
+cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
+                            int sink, int recent, float* new_weights, int32_t* list, int64_t list_stride,
+                            DevStatus* status, cudaStream_t st);
 
 }  // namespace crisp

@@ -23,6 +23,9 @@
  *   crisp_prefill_layer         A1..A8 in order, intermediates in the workspace
  *   crisp_prefill_layer_host    the same from host buffers, copies overlapped with compute
  *   crisp_proxy_map_noalloc     A1 without a caller workspace (static scratch)
+ *   crisp_kv_append             new K and V tokens into a paged 8-bit cache
+ *   crisp_decode_attention      attention of 1..16 new tokens per sequence over that cache
+ *   crisp_kv_evict              keeps a cache's sink, recent and heaviest tokens
  *   crisp_wait_selftest         failure detection: a bounded wait that must time out
  *
  * Conventions (every function):
@@ -80,8 +83,9 @@ typedef enum crisp_status {
   CRISP_ERR_CUDA = 5,        /* a CUDA runtime call failed (launch, copy) */
   CRISP_ERR_TIMEOUT = 6,     /* device: a bounded wait inside a kernel ran out */
   CRISP_ERR_DEVICE = 7,      /* the current device is not sm_103 */
-  CRISP_ERR_BOUNDS = 8       /* device, bounds-checking build only: an index fell outside its
-                                buffer; the access was skipped (the release build has no checks) */
+  CRISP_ERR_BOUNDS = 8       /* device: an index fell outside its buffer; the access was skipped. From
+                                the cache calls, which read page ids and lengths on the device, in
+                                every build; from the others in the bounds-checking build only */
 } crisp_status;
 
 typedef enum crisp_pe_mode {
@@ -434,6 +438,110 @@ CRISP_API crisp_status crisp_prefill_layer_host(crisp_host_pipeline* pipeline, c
                                                 const crisp_params* params, const void* q_host, const void* k_host,
                                                 const void* v_host, void* out_host, void* q, void* k, void* v,
                                                 void* out, void* ws, size_t ws_bytes, crisp_stream_t stream);
+
+/* ---- A paged key/value cache held in 8 bits --------------------------------
+ * What a prefilled layer leaves for decoding. Page p of kv head h holds 128
+ * tokens of 128 e4m3 codes; one power-of-two scale per page and head, K and V
+ * apart, gives the values: value = code * scale. The scale is 2^e with the
+ * smallest integer e >= -100 for which amax <= 448 * 2^e, amax the largest
+ * finite magnitude: scaling by it is exact, each stored element is off by at
+ * most half an e4m3 step (2^-4 of itself, or 2^-10 scales where it is
+ * below 2^-6 scales), and a page's scale can grow without a second rounding
+ * of codes of at least 2^-6 scales. A non-finite element is stored as NaN.
+ *
+ * Token j of sequence b is row j % 128 of page table[b][j / 128]. Entries of
+ * the table past a sequence's last page are not read. A page id outside [0,
+ * num_pages) or a length outside [0, 128 * max_pages] sets CRISP_ERR_BOUNDS in
+ * the status word: such a page reads as holding no tokens and is not written,
+ * such a length counts as the nearest one inside. A page may stand in several
+ * sequences' tables (a shared prefix) as long as no call writes it; a page
+ * written by a call (crisp_kv_append, the destination of crisp_kv_evict) must
+ * stand there once, and its contents are unspecified otherwise.
+ *
+ * lens[b] counts the tokens held, the ones being appended or asked about
+ * included: advance it, then append, then attend. Rows of a page at or past
+ * lens[b] may hold anything. 1 <= batch <= 1024, max_pages <= 8192. Pointers
+ * are device pointers: k and v (and the strides) 16-byte aligned, the others
+ * 4-byte aligned. */
+typedef struct crisp_kv_cache {
+  int32_t batch;        /* sequences */
+  int32_t hkv;          /* key/value heads */
+  int32_t head_dim;     /* must be 128 */
+  int32_t block;        /* tokens of a page; must be 128 */
+  int32_t num_pages;    /* pages of the pool */
+  int32_t max_pages;    /* entries of a table row */
+  int64_t page_stride;  /* bytes from page to page, k and v alike */
+  int64_t head_stride;  /* bytes from head to head of a page; a head's 128 x 128 codes are contiguous */
+  void* k;              /* e4m3 [num_pages][hkv][128][128] */
+  void* v;
+  float* k_scale;       /* fp32 [num_pages][hkv], contiguous */
+  float* v_scale;
+  const int32_t* table; /* int32 [batch][max_pages], contiguous */
+  int32_t* lens;        /* int32 [batch]; written by crisp_kv_evict on its destination only */
+} crisp_kv_cache;
+
+/* bf16 [batch][heads][tokens][128] with element strides (the 128 features
+ * contiguous): the pointer 16-byte aligned, strides multiples of 8. */
+typedef struct crisp_tokens {
+  const void* data;
+  int64_t batch_stride, head_stride, tok_stride;
+} crisp_tokens;
+
+/* Workspace bytes of the three cache calls (as for the other steps, call
+ * crisp_workspace_init once after allocating). with_weights: whether the
+ * decode call gets weights_out. */
+CRISP_API crisp_status crisp_kv_append_workspace_size(const crisp_kv_cache* cache, size_t* bytes /* host */);
+CRISP_API crisp_status crisp_decode_workspace_size(const crisp_kv_cache* cache, int32_t hq, int32_t q_len,
+                                                   int32_t with_weights, size_t* bytes /* host */);
+CRISP_API crisp_status crisp_kv_evict_workspace_size(const crisp_kv_cache* cache, int32_t keep,
+                                                     size_t* bytes /* host */);
+
+/* Writes new tokens into the cache: with c = new_lens[b] (NULL: n_new for
+ * every sequence; clamped to [0, min(n_new, lens[b])], CRISP_ERR_BOUNDS if it
+ * was outside), token i < c of sequence b goes to position lens[b] - c + i.
+ * The scale of a page that already held tokens below the first new position
+ * only grows; when it does, those tokens' codes are rounded again at the new
+ * scale. Rows at or past lens[b] are left as they were. k_new, v_new: bf16
+ * [batch][hkv][n_new][128], 0 <= n_new <= 128 * max_pages. */
+CRISP_API crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_tokens* k_new,
+                                       const crisp_tokens* v_new, int32_t n_new, const int32_t* new_lens, void* ws,
+                                       size_t ws_bytes, crisp_stream_t stream);
+
+/* Exact softmax attention of the last q_len tokens of every sequence over the
+ * cache (the dense step's formula, over the values the cache stands for).
+ * Query token i of sequence b sees the keys j < lens[b] - (q_len - 1 - i); with
+ * s_j = scale * q . k_j (scale 0: 1/sqrt(128)), kv head h / (hq / hkv):
+ *   out[b][h][i] = sum_j softmax_j(s) v_j,       zeros where no key is seen,
+ *   weights_out[b][g][j] = weights_in[b][g][j] + sum over the heads h of kv head
+ *                g and the tokens i of softmax_j(s),     j < lens[b],
+ * the second only with weights_out (weights_in NULL counts as zeros; the two
+ * may be the same array; entries at or past lens[b] are left as they were).
+ * q, out: bf16 [batch][hq][q_len][128], 1 <= q_len <= 16, hq % hkv == 0;
+ * weights: fp32 [batch][hkv][128 * max_pages], contiguous, 16-byte aligned.
+ * Precision: q is held as two e4m3 pieces (exact down to 2^-14 of the row's
+ * largest element), p as two (2^-8 of itself); products and sums are fp32. */
+CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32_t hq, int32_t q_len, float scale,
+                                              const crisp_tokens* q, const crisp_tokens* out,
+                                              const float* weights_in, float* weights_out, void* ws, size_t ws_bytes,
+                                              crisp_stream_t stream);
+
+/* Cuts every sequence to at most `keep` tokens by accumulated attention weight
+ * (crisp_decode_attention's weights). With n = src->lens[b], per sequence and kv
+ * head: all tokens if n <= keep; else the first `sink`, the last `recent`, and
+ * the keep - sink - recent others of largest weight (equal weights: the lowest
+ * position; NaN counts as larger than any number). The kept tokens go, in their
+ * order, to positions 0, 1, .. of dst: each of its pages gets the scale its
+ * values need, codes rounded again where that differs. dst->lens[b] = min(n,
+ * keep). dst may share the pools with src (k, v, scales), but its table's pages
+ * must not stand in any src table. new_weights fp32 [batch][hkv][128 *
+ * dst->max_pages] (16-byte aligned) and kept int32 [batch][hkv][128 *
+ * dst->max_pages] (each kept token's old position) are written below the new
+ * length; either may be NULL. 1 <= keep <= 128 * dst->max_pages, sink + recent
+ * <= keep. weights: as for crisp_decode_attention, not the same array as
+ * new_weights. */
+CRISP_API crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst, const float* weights,
+                                      int32_t keep, int32_t sink, int32_t recent, float* new_weights, int32_t* kept,
+                                      void* ws, size_t ws_bytes, crisp_stream_t stream);
 
 /* Synchronises `stream` and copies the workspace status word to *status
  * (host). Returns CRISP_ERR_CUDA if the stream or the copy failed. */
