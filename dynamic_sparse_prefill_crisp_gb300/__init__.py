@@ -162,10 +162,19 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr() if hasattr(t, "data_ptr") else int(t))
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
+        # the current device's current stream, without building a Stream object (3 us a call)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            raw, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _raw_stream = lambda: raw(dev())
+        return ctypes.c_void_p(_raw_stream())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -385,29 +394,37 @@ def make_kv_cache(k, v, k_scale, v_scale, table, lens) -> KVCache:
     _need(all(t.device == k.device for t in keep), "make_kv_cache: the tensors must be on one device")
     c = KVCache(table.shape[0], hkv, D, B, num, table.shape[1], k.stride(0), k.stride(1), k.data_ptr(), v.data_ptr(),
                 k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr())
-    c.tensors = keep
+    c.tensors, c.device_index, c.token_dtype = keep, k.get_device(), torch.bfloat16
     return c
 
 
-def _tokens(name, t, cache, heads):
-    import torch
-    _need(t.dim() == 4 and t.shape[0] == cache.batch and t.shape[1] == heads and t.shape[3] == D and t.stride(3) == 1
-          and t.dtype == torch.bfloat16, f"{name} must be bf16 [batch][heads][tokens][128], features contiguous")
-    return Tokens(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+def _tokens(what, t, cache, heads, tokens):
+    if t.shape != (cache.batch, heads, tokens, D) or t.dtype != cache.token_dtype:
+        raise ValueError(f"{what} must be bf16 [batch][heads][tokens][128] = "
+                         f"{(cache.batch, heads, tokens, D)}: {t.dtype} {tuple(t.shape)}")
+    b, h, i, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{what}: the 128 features must be contiguous")
+    return Tokens(t.data_ptr(), b, h, i)
 
 
-def _rows(name, t, cache, dtype):
-    _need(t.shape == (cache.batch, cache.hkv, cache.max_pages * B) and t.dtype == dtype and t.is_contiguous(),
-          f"{name} must be contiguous {dtype} [batch][hkv][128 * max_pages]")
+def _rows(what, t, cache, dtype):
+    """The address of contiguous [batch][hkv][128 * max_pages] (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.shape != (cache.batch, cache.hkv, cache.max_pages * B) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {dtype} [batch][hkv][128 * max_pages]")
+    return t.data_ptr()
 
 
 def _on_device(cache, *tensors):
     """The calls run on the current device and stream: everything has to be there."""
-    import torch
-    dev = cache.tensors[0].device
-    _need(dev.type == "cuda" and dev.index == torch.cuda.current_device() and
-          all(t is None or t.device == dev for t in tensors),
-          "the cache and every tensor of the call must be on the current CUDA device")
+    dev = cache.device_index
+    if dev >= 0:
+        import torch
+        if torch.cuda.current_device() == dev and all(t is None or t.get_device() == dev for t in tensors):
+            return
+    raise ValueError("the cache and every tensor of the call must be on the current CUDA device")
 
 
 def kv_append_workspace_size(cache: KVCache) -> int:
@@ -435,14 +452,18 @@ def kv_append(cache, k_new, v_new, ws, new_lens=None, stream=None):
     """Writes bf16 [batch][hkv][n_new][128] tokens into the cache, the last of
     sequence b at position lens[b] - 1 (advance lens first); new_lens: int32
     [batch], how many of the n_new tokens each sequence has (default: all)."""
-    import torch
-    kt, vt = _tokens("kv_append: k_new", k_new, cache, cache.hkv), _tokens("kv_append: v_new", v_new, cache, cache.hkv)
-    _need(k_new.shape == v_new.shape, "kv_append: k_new and v_new must have one shape")
-    _need(new_lens is None or (new_lens.shape == (cache.batch,) and new_lens.dtype == torch.int32 and
-                               new_lens.is_contiguous()), "kv_append: new_lens must be contiguous int32 [batch]")
+    _need(k_new.dim() == 4, "kv_append: k_new must be [batch][hkv][n_new][128]")
+    n_new = k_new.shape[2]
+    kt = _tokens("kv_append: k_new", k_new, cache, cache.hkv, n_new)
+    vt = _tokens("kv_append: v_new", v_new, cache, cache.hkv, n_new)
+    if new_lens is not None:
+        lens = cache.tensors[5]
+        _need(new_lens.shape == lens.shape and new_lens.dtype == lens.dtype and new_lens.is_contiguous(),
+              "kv_append: new_lens must be contiguous int32 [batch]")
     _on_device(cache, k_new, v_new, ws, new_lens)
-    _check(lib().crisp_kv_append(ctypes.byref(cache), ctypes.byref(kt), ctypes.byref(vt), k_new.shape[2],
-                                 _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)), "crisp_kv_append")
+    _check(lib().crisp_kv_append(ctypes.byref(cache), ctypes.byref(kt), ctypes.byref(vt), n_new,
+                                 None if new_lens is None else new_lens.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                                 _stream(stream)), "crisp_kv_append")
 
 
 def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale=0.0, stream=None):
@@ -450,16 +471,16 @@ def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale
     out bf16 [batch][hq][q_len][128]. With weights_out (fp32 [batch][hkv][128 *
     max_pages]) each key's weight, summed over the kv head's rows, is added to
     weights_in's (None: zeros; may be the same tensor)."""
-    import torch
-    hq, q_len = q.shape[1], q.shape[2]
-    qt, ot = _tokens("decode_attention: q", q, cache, hq), _tokens("decode_attention: out", out, cache, hq)
-    _need(out.shape == q.shape, "decode_attention: q and out must have one shape")
-    for name, t in (("weights_in", weights_in), ("weights_out", weights_out)):
-        if t is not None:
-            _rows(f"decode_attention: {name}", t, cache, torch.float32)
+    _need(q.dim() == 4, "decode_attention: q must be [batch][hq][q_len][128]")
+    _, hq, q_len, _ = q.shape
+    qt = _tokens("decode_attention: q", q, cache, hq, q_len)
+    ot = _tokens("decode_attention: out", out, cache, hq, q_len)
+    f32 = cache.tensors[2].dtype
+    w_in = _rows("decode_attention: weights_in", weights_in, cache, f32)
+    w_out = _rows("decode_attention: weights_out", weights_out, cache, f32)
     _on_device(cache, q, out, ws, weights_in, weights_out)
     _check(lib().crisp_decode_attention(ctypes.byref(cache), hq, q_len, scale, ctypes.byref(qt), ctypes.byref(ot),
-                                        _ptr(weights_in), _ptr(weights_out), _ptr(ws), _nbytes(ws), _stream(stream)),
+                                        w_in, w_out, ws.data_ptr(), _nbytes(ws), _stream(stream)),
            "crisp_decode_attention")
 
 
@@ -468,16 +489,13 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
     `sink`, the last `recent`, and those of largest weight -- into new_cache's
     pages, in their order, and sets its lens. new_weights (fp32) and kept (int32,
     old positions) are [batch][hkv][128 * new_cache.max_pages]."""
-    import torch
-    _rows("kv_evict: weights", weights, cache, torch.float32)
-    if new_weights is not None:
-        _rows("kv_evict: new_weights", new_weights, new_cache, torch.float32)
-    if kept is not None:
-        _rows("kv_evict: kept", kept, new_cache, torch.int32)
-    _on_device(cache, *new_cache.tensors, weights, ws, new_weights, kept)
-    _check(lib().crisp_kv_evict(ctypes.byref(cache), ctypes.byref(new_cache), _ptr(weights), keep, sink, recent,
-                                _ptr(new_weights), _ptr(kept), _ptr(ws), _nbytes(ws), _stream(stream)),
-           "crisp_kv_evict")
+    f32, i32 = cache.tensors[2].dtype, cache.tensors[5].dtype
+    w = _rows("kv_evict: weights", weights, cache, f32)
+    new_w = _rows("kv_evict: new_weights", new_weights, new_cache, f32)
+    pos = _rows("kv_evict: kept", kept, new_cache, i32)
+    _on_device(cache, new_cache.tensors[0], weights, ws, new_weights, kept)
+    _check(lib().crisp_kv_evict(ctypes.byref(cache), ctypes.byref(new_cache), w, keep, sink, recent, new_w, pos,
+                                ws.data_ptr(), _nbytes(ws), _stream(stream)), "crisp_kv_evict")
 
 
 def wait_selftest(ws, limit_ns, stream=None):

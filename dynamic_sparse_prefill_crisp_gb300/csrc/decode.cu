@@ -1,19 +1,24 @@
 // Attention of a few new tokens over the paged 8-bit cache.
 //
-// Per kv head the rows are the G query heads times the q_len tokens, kR of
-// them at a time. One page (128 keys) is one tile; codes kc, vc in e4m3 with
+// Per kv head the rows are the G query heads times the q_len tokens, up to 32
+// of them at a time. One page (128 keys) is one tile; codes kc, vc in e4m3 with
 // the page's scales ks, vs:
-//   S^T = Kc Q'^T        tcgen05.mma kind::f8f6f4: A = the K page (M = 128 keys, K-major), B = Q' (N = 2 kR)
-//   p   = 2^(s - m_t)    softmax warps, m_t = the row's largest s of the tile
-//   O^T = Vc^T P'^T      A = the V page (M = 128 features, MN-major), B = P' (N = 2 kR, 128 keys)
+//   S^T = Kc Q'^T        tcgen05.mma kind::f8f6f4: A = the K page (M = 128 keys, K-major), B = Q' (N = 2 x rows)
+//   p   = 2^(s - m_t)    softmax warps, m_t = the row's largest s of the step
+//   O^T = Vc^T P'^T      A = the V page (M = 128 features, MN-major), B = P' (N = 2 x rows, 128 keys)
 //   acc = acc 2^(m - m') + O^T vs 2^(m_t - m')      fp32 registers, m' = max(m, m_t)
 // K and V go from HBM by TMA to shared memory and into the tensor cores as
 // they are: nothing dequantises them. The other operand is made of two e4m3
-// pieces, x = hi + lo / 16 (rows r and kR + r of B): a bf16 q at a power-of-two
+// pieces, x = hi + lo / 16 (rows r and rows + r of B): a bf16 q at a power-of-two
 // row scale is exactly that sum down to 2^-14 of the row's largest element;
-// p (scaled to 256 at the tile's maximum) is off by at most 2^-8 of itself, as
+// p (scaled to 256 at the step's maximum) is off by at most 2^-8 of itself, as
 // a bf16 p would be. O^T is read back every tile, so that page scales and the
 // running maximum act in fp32 and a tile of small p is as exact as any other.
+//
+// Two tiles of an item make a step. What bounds a step is the chain of waits
+// from its scores to its P', not arithmetic: one tile at a time took 2300
+// cycles (2800 with weights; 44.7 bytes per ns and SM leave 2800 for two CTAs'
+// tiles), so a step shares the waits, the maximum and the fence between two.
 //
 // The work is the list of all tiles of the batch, item (sequence, kv head, row
 // chunk) by item; every CTA takes an equal run of it, so ragged batches stay
@@ -21,9 +26,11 @@
 // CTA's run is finished there; the others leave (m, l, acc) per CTA and
 // join_kernel adds them in CTA order: results do not depend on timing.
 //
-// Warps: 0-3 softmax and accumulation (thread t: key t of a tile, feature t
-// of the output), 4 TMA, 5 MMA issue (and TMEM), 6 the Q' operand.
+// Warps: kWG groups of four for softmax and accumulation, eight rows each
+// (thread t of a group: key t of a tile, feature t of the output), then TMA, MMA
+// issue (and TMEM), and the Q' operand.
 #include <algorithm>
+#include <utility>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -34,36 +41,54 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kWorkers = 4;                       // softmax warps
-constexpr int kTmaWarp = 4, kMmaWarp = 5, kQWarp = 6;
-constexpr int kThreads = 7 * 32;
+constexpr int kWgRows = 8;                        // rows of a softmax warp group
 constexpr uint32_t kPage = kB * kD;               // bytes of a page of one head, K or V
 constexpr int kMaxTail = kMaxQLen - 1;            // keys that only some of the rows see
 constexpr float kLo = 16.f;                       // the second piece's scale
+constexpr int kStep = 2;                           // tiles of a step
+constexpr int kMaxSlots = 6;                      // K (or V) page slots
 
-// Rows a CTA takes at once and the page slots that leave two CTAs per SM.
-template <int kR>
+// kWG groups: rows, CTAs per SM, and the page slots that leave room for them.
+template <int kWG>
 struct Cfg {
-  static constexpr int slots = kR == 8 ? 6 : kR == 16 ? 5 : 4;
-  static constexpr int N = 2 * kR;                          // columns of B
-  static constexpr uint32_t op = N * 128;                   // bytes of Q' or P'
-  static constexpr uint32_t smem = 1024 + slots * kPage + 4 * op;
-  static constexpr uint32_t tmem = 4 * N;                   // S and O, two buffers each
+  static constexpr int rows = kWG * kWgRows;
+  static constexpr int workers = kWG * 4;                   // softmax warps
+  static constexpr int threads = (workers + 3) * 32;
+  static constexpr int per_sm = kWG == 1 ? 2 : 1;
+  static constexpr int k_slots = kWG == 1 ? 3 : 5;
+  static constexpr int v_slots = kWG == 1 ? 3 : 5;
+  // Where one CTA has the SM to itself, nothing else runs while it waits for a
+  // step's V product: P' and O get a second buffer, and O is added a step later.
+  static constexpr int bufs = kWG == 1 ? 1 : 2;
+  static constexpr int N = 2 * rows;                        // columns of B
+  static constexpr uint32_t op = N * 128;                   // bytes of Q' or of a tile's P'
+  static constexpr uint32_t smem = 1024 + (k_slots + v_slots) * kPage + (2 + kStep * bufs) * op;
+  static constexpr uint32_t o_col = 2 * kStep * N;          // S: two buffers of a step, then O
+  static constexpr uint32_t tmem = 4 * kStep * N;           // (a power of two)
 };
 
-template <int kR>
+template <int kWG>
 struct Shared {
-  uint64_t full[6], empty[6];          // page slots
+  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem_base;
   int abort;
-  int warp_sum[8];
-  float qs[2][kR];                     // q scale * scale * log2(e) per row
-  float red[2][kWorkers][kR];          // warps' row maxima (sums at an item's end)
-  float ref[kWorkers][kR];             // m_t - 8 (0 for a row without keys), per warp
-  float alpha[kWorkers][2][kR], wl[kWorkers][2][kR];
-  float tail[2][kR][kMaxTail + 1];     // p of keys that only some rows see
+  int warp_sum[kWG * 4 + 3];
+  alignas(16) float qs[2][kWG * kWgRows];           // q scale * scale * log2(e) per row
+  alignas(16) float red[2][kWG][4][kWgRows];        // warps' row maxima
+  float sum[kWG][4][kWgRows];                       // and, at an item's end, their row sums
+  alignas(16) float ref[kWG * 4][kWgRows];          // per warp: the step's maximum - 8 (0 for a row without keys)
+  alignas(16) float alpha[kWG * 4][kWgRows];        // what scales the accumulators to the new maximum
+  alignas(16) float wl[kWG * 4][2][kWgRows];        // weight of the step's p and O at it
+  float tail[2][kWG * kWgRows][kMaxTail + 1];       // p of keys that only some rows see
+};
+
+// A split item, by the CTA in which it begins.
+struct Split {
+  int b, gc;   // sequence (-1: no item begins here and goes on); kv head * chunks + row chunk
+  int last;    // the CTA in which it ends
+  int pad;
 };
 
 struct Args {
@@ -77,9 +102,10 @@ struct Args {
   __nv_bfloat16* out;
   int64_t o_b, o_h, o_t;
   float c;                             // scale * log2(e)
-  float* part;                         // [2 ctas][kR][128]
-  float2* part_ml;                     // [2 ctas][kR]  (m, l)
-  float* lse;                          // [items][kR]   log2 sum of 2^s, +inf for a row without keys
+  float* part;                         // [2 ctas][rows of a chunk][128]
+  float2* part_ml;                     // [2 ctas][rows of a chunk]  (m, l)
+  Split* split;                        // [ctas]
+  float* lse;                          // [batch][hkv][rows]  log2 sum of 2^s, +inf for a row without keys; or null
   float* scores;                       // [batch][hkv][rows][128 max_pages] or null
   DevStatus* status;
 };
@@ -100,40 +126,6 @@ __device__ __forceinline__ int run_of(long long total, long long t, int runs) {
   return static_cast<int>(((t + 1) * runs - 1) / total);
 }
 
-// One tile of the list.
-struct Tile {
-  int b, gc;       // sequence; kv head * chunks + row chunk
-  int page;        // page of the sequence
-  int pages;       // pages of the sequence
-  int len;         // tokens of the sequence
-};
-
-// pre[b]: pages of the sequences before b.
-__device__ __forceinline__ Tile find_tile(const int* pre, const Args& a, long long t) {
-  const int hc = a.hkv * a.chunks;
-  int lo = 0, hi = a.batch - 1;  // the last b with pre[b] * hc <= t that has pages: pre[b + 1] * hc > t
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<long long>(pre[mid + 1]) * hc > t) hi = mid;
-    else lo = mid + 1;
-  }
-  Tile x;
-  x.b = lo;
-  x.pages = pre[lo + 1] - pre[lo];
-  const int rem = static_cast<int>(t - static_cast<long long>(pre[lo]) * hc);
-  x.gc = rem / x.pages;
-  x.page = rem - x.gc * x.pages;
-  bool bad;
-  x.len = clamped_len(a, lo, bad);
-  return x;
-}
-
-// The page id of a tile, -1 if the table holds none of the pool's.
-__device__ __forceinline__ int page_id(const Args& a, const Tile& x) {
-  const int id = a.table[static_cast<int64_t>(x.b) * a.max_pages + x.page];
-  return id >= 0 && id < a.num_pages ? id : -1;
-}
-
 template <class T>
 __device__ __forceinline__ T bcast(T v, int lane) {
   return __shfl_sync(0xffffffffu, v, lane);
@@ -145,13 +137,49 @@ __device__ __forceinline__ void fail(int* abort, DevStatus* st, uint32_t where) 
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  const bool ok = mbar_wait(bar, parity, abort);
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  ok = mbar_wait(bar, parity, abort);
   return __all_sync(0xffffffffu, ok);
 }
 
-// Slot positions in the order the products need them: K0 K1 V0 K2 V1 .. K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int v_pos(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+// Walks the items of a run: the tile's sequence, kv head and chunk, and how
+// many of the item's tiles the run still has from it on.
+struct Walk {
+  int b, gc, page, pages, left;
+  __device__ __forceinline__ void begin(const int* pre, const Args& a, long long t, int n) {
+    const int hc = a.hkv * a.chunks;
+    int lo = 0, hi = a.batch - 1;  // the last b with pre[b] * hc <= t that has pages: pre[b + 1] * hc > t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<long long>(pre[mid + 1]) * hc > t) hi = mid;
+      else lo = mid + 1;
+    }
+    b = lo;
+    pages = pre[lo + 1] - pre[lo];
+    const int rem = static_cast<int>(t - static_cast<long long>(pre[lo]) * hc);
+    gc = rem / pages;
+    page = rem - gc * pages;
+    left = min(pages - page, n);
+  }
+  // To the next item; n: tiles of the run from it on (> 0).
+  __device__ __forceinline__ void next(const int* pre, const Args& a, int n) {
+    page = 0;
+    if (++gc == a.hkv * a.chunks) {
+      gc = 0;
+      do ++b;
+      while (pre[b + 1] == pre[b]);
+      pages = pre[b + 1] - pre[b];
+    }
+    left = min(pages, n);
+  }
+};
+
+// The page of a tile: its id (-1 if the table names none of the pool's).
+__device__ __forceinline__ int page_id(const Args& a, int b, int page) {
+  const int id = a.table[static_cast<int64_t>(b) * a.max_pages + page];
+  return id >= 0 && id < a.num_pages ? id : -1;
+}
 
 // Row r of the lanes' values v[r], reduced over the warp: lane L returns row
 // L >> (5 - log2 kR). Halves the rows a step while it can: kR - 1 + (5 -
@@ -175,57 +203,54 @@ __device__ __forceinline__ float warp_rows(float (&v)[kR]) {
   return v[0];
 }
 
-// 2 kR accumulator columns: v[r] = hi + lo / 16.
-template <int kR>
-__device__ __forceinline__ void load_rows(uint32_t taddr, float (&v)[kR]) {
-  if constexpr (kR == 8) {
-    uint32_t x[16];
-    tmem_ld16(taddr, x);
+// A group's eight rows of an accumulator: v[r] = hi + lo / 16, hi in columns
+// [0, 8) of taddr, lo `n` columns further on.
+__device__ __forceinline__ void load_rows(uint32_t taddr, int n, float (&v)[kWgRows]) {
+  uint32_t x[8], y[8];
+  tmem_ld8x2(taddr, taddr + n, x, y);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = fmaf(__uint_as_float(x[8 + r]), 1.f / kLo, __uint_as_float(x[r]));
-  } else if constexpr (kR == 16) {
-    uint32_t x[32];
-    tmem_ld32(taddr, x);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) v[r] = fmaf(__uint_as_float(x[16 + r]), 1.f / kLo, __uint_as_float(x[r]));
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t x[16], y[16];
-      tmem_ld16(taddr + 16 * h, x);
-      tmem_ld16(taddr + 32 + 16 * h, y);
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        v[16 * h + r] = fmaf(__uint_as_float(y[r]), 1.f / kLo, __uint_as_float(x[r]));
-    }
-  }
+  for (int r = 0; r < 8; r += 2)
+    ffma2(v[r], v[r + 1], __uint_as_float(y[r]), __uint_as_float(y[r + 1]), 1.f / kLo, 1.f / kLo,
+          __uint_as_float(x[r]), __uint_as_float(x[r + 1]));
 }
 
-template <int kR>
-__global__ void __launch_bounds__(kThreads, 2)
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+template <int kWG, bool kScores>
+__global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ Args a) {
-  using C = Cfg<kR>;
+  using C = Cfg<kWG>;
+  constexpr int kR = C::rows, kTmaWarp = C::workers, kMmaWarp = C::workers + 1, kQWarp = C::workers + 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* slots = base;
-  uint8_t* sQ = base + C::slots * kPage;  // two buffers
-  uint8_t* sP = sQ + 2 * C::op;           // two buffers
-  int* pre = reinterpret_cast<int*>(sP + 2 * C::op);
-  __shared__ Shared<kR> sh;
+  uint8_t* sK = base;
+  uint8_t* sV = sK + C::k_slots * kPage;
+  uint8_t* sQ = sV + C::v_slots * kPage;  // two buffers
+  uint8_t* sP = sQ + 2 * C::op;           // C::bufs steps' tiles
+  int* pre = reinterpret_cast<int*>(sP + C::bufs * kStep * C::op);
+  __shared__ Shared<kWG> sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     sh.abort = 0;
-    for (int s = 0; s < C::slots; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 1);
+    for (int s = 0; s < C::k_slots; ++s) {
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_empty[s], 1);
+    }
+    for (int s = 0; s < C::v_slots; ++s) {
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.q_full[s], 1);
-      mbar_init(&sh.q_empty[s], 2);  // the last score product of the item; the softmax warps' end of it
+      mbar_init(&sh.q_empty[s], 1 + kWG);  // the last score product of the item; the softmax groups' end of it
       mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.p_full[s], kWorkers * 32);
+      mbar_init(&sh.p_full[s], C::workers * 32);
       mbar_init(&sh.o_full[s], 1);
     }
     mbar_init(&sh.drain, 1);
@@ -242,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // Pages before each sequence (an inclusive scan over the batch, a block of sequences at a time).
   int before = 0;
   if (threadIdx.x == 0) pre[0] = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.batch; b0 += C::threads) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     int n = 0;
     if (b < a.batch) {
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int add = before;
     for (int w = 0; w < warp; ++w) add += sh.warp_sum[w];
     if (b < a.batch) pre[b + 1] = n + add;
-    for (int w = 0; w < kThreads / 32; ++w) before += sh.warp_sum[w];
+    for (int w = 0; w < C::threads / 32; ++w) before += sh.warp_sum[w];
     __syncthreads();
   }
   tc_fence_before();
@@ -274,115 +299,134 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int n = run < runs ? static_cast<int>(run_begin(total, run + 1, runs) - t_lo) : 0;
 
   if (n > 0 && warp == kTmaWarp) {
-    // Tiles by 32: each lane looks up one tile's page, lane 0 issues the copies.
+    // Tiles by 32: each lane looks up one tile's page, lane 0 issues the
+    // copies: K(0) .. K(3), then V(i - 3) behind K(i), as the products take them.
+    constexpr int kLead = 2 * kStep - 1;
     bool go = true;
-    int pos = 0;
-    int zk = 0, gk = 0, zv = 0, gv = 0;  // the tile being loaded (K), and the one before (V)
-    auto load = [&](const CUtensorMap* map, int z, int g) {
-      const int s = pos % C::slots;
-      if (!mbar_wait(&sh.empty[s], ((pos / C::slots) & 1) ^ 1, &sh.abort)) {
+    auto load = [&](uint8_t* slots, uint64_t* full, uint64_t* empty, int count, const CUtensorMap* map, int i, int z,
+                    int g) {
+      const int s = i % count;
+      if (!mbar_wait(&empty[s], ((i / count) & 1) ^ 1, &sh.abort)) {
         fail(&sh.abort, a.status, 0x610);
         go = false;
         return;
       }
-      ++pos;
       if (z >= 0) {
-        mbar_arrive_expect_tx(&sh.full[s], kPage);
-        tma_load_4d(slots + s * kPage, map, &sh.full[s], 0, 0, g, z);
+        mbar_arrive_expect_tx(&full[s], kPage);
+        tma_load_4d(slots + s * kPage, map, &full[s], 0, 0, g, z);
       } else {
-        mbar_arrive(&sh.full[s]);  // a bad page id: nothing is copied, and the tile counts as empty
+        mbar_arrive(&full[s]);  // a bad page id: nothing is copied, and the tile counts as empty
       }
     };
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      int z = -1, g = 0;
-      if (i0 + lane < n) {
-        const Tile x = find_tile(pre, a, t_lo + i0 + lane);
-        z = page_id(a, x);
-        g = x.gc / a.chunks;
-        if (z < 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x602);
+    int kn = 0, vn = 0;                  // copies issued
+    int z = -1, g = 0, z_old = -1, g_old = 0;  // lanes' tiles of this window of 32 and of the one before
+    for (int i = 0; i < n + kLead; ++i) {
+      if ((i & 31) == 0) {
+        z_old = z;
+        g_old = g;
+        z = -1;
+        if (i + lane < n) {
+          Walk x;
+          x.begin(pre, a, t_lo + i + lane, n);
+          z = page_id(a, x.b, x.page);
+          g = x.gc / a.chunks;
+          if (z < 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x602);
+        }
       }
-      for (int k = 0; k < 32 && i0 + k < n; ++k) {
-        zv = zk;
-        gv = gk;
-        zk = bcast(z, k);
-        gk = bcast(g, k);
-        if (lane == 0 && go) load(&tk, zk, gk);
-        if (lane == 0 && go && i0 + k > 0) load(&tv, zv, gv);
+      const int v = i - kLead;  // the V tile of this turn
+      const bool same = v >= (i & ~31);
+      const int zk = bcast(z, i & 31), gk = bcast(g, i & 31);
+      const int zv = bcast(same ? z : z_old, v & 31), gv = bcast(same ? g : g_old, v & 31);
+      if (lane == 0 && go && i < n) {
+        load(sK, sh.k_full, sh.k_empty, C::k_slots, &tk, i, zk, gk);
+        kn += go;
+      }
+      if (lane == 0 && go && v >= 0) {
+        load(sV, sh.v_full, sh.v_empty, C::v_slots, &tv, v, zv, gv);
+        vn += go;
       }
     }
     if (lane == 0) {
-      if (go) load(&tv, zk, gk);
-      // Every copy issued has landed before the CTA ends (a bounded wait that
-      // ignores the abort flag).
+      // Every copy issued has landed before the CTA ends (bounded waits that
+      // ignore the abort flag).
       const int never = 0;
-      for (int q = max(0, pos - C::slots); q < pos; ++q)
-        mbar_wait(&sh.full[q % C::slots], (q / C::slots) & 1, &never);
+      for (int q = max(0, kn - C::k_slots); q < kn; ++q)
+        mbar_wait(&sh.k_full[q % C::k_slots], (q / C::k_slots) & 1, &never);
+      for (int q = max(0, vn - C::v_slots); q < vn; ++q)
+        mbar_wait(&sh.v_full[q % C::v_slots], (q / C::v_slots) & 1, &never);
     }
   } else if (n > 0 && warp == kMmaWarp) {
     constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, C::N, false, false);
     constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, C::N, true, false);
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dp = sdesc_sw128(smem_u32(sP), 16, 1024);
     bool go = true;
-    int item = -1;  // items begun
-    // first/last tile of an item in this run: bits of the 32 tiles looked up by the lanes
-    uint32_t first = 0, last = 0;
-    int held = -1;
-    auto flags = [&](int i) {
-      if (i / 32 == held) return;
-      held = i / 32;
-      bool f = false, l = false;
-      const int t = held * 32 + lane;
-      if (t < n) {
-        const Tile x = find_tile(pre, a, t_lo + t);
-        f = t == 0 || x.page == 0;
-        l = t == n - 1 || x.page == x.pages - 1;
-      }
-      first = __ballot_sync(0xffffffffu, f);
-      last = __ballot_sync(0xffffffffu, l);
-    };
-    auto issue_qk = [&](int i) {
-      flags(i);
-      if (first >> (i & 31) & 1u) {
+    Walk x;  // of the score products, up to two steps ahead of the others
+    x.begin(pre, a, t_lo, n);
+    int ik = 0, iv = 0, item = -1, sk = 0;  // tiles taken, items begun, steps of scores issued
+    bool begins = true;
+    int size[3];                            // tiles of the steps in flight, by step % 3
+    // S of the next step; false when the run has no more (or on abort: go)
+    auto issue_qk = [&]() {
+      if (ik == n) return;
+      if (begins) {
         ++item;
-        if (!mbar_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) go = false;
+        if (!warp_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) go = false;
       }
-      const int pos = k_pos(i), s = pos % C::slots;
-      if (go && !mbar_wait(&sh.full[s], (pos / C::slots) & 1, &sh.abort)) go = false;
-      go = __all_sync(0xffffffffu, go);
+      const int m = min(kStep, x.left), buf = sk & 1;
+      for (int j = 0; go && j < m; ++j, ++ik) {
+        const int s = ik % C::k_slots;
+        if (!warp_wait(&sh.k_full[s], (ik / C::k_slots) & 1, &sh.abort)) go = false;
+        if (!go) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dk = sdesc_sw128(smem_u32(sK + s * kPage), 16, 1024);
+          const uint64_t dqi = dq + (item & 1) * (C::op >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 features a step
+            umma_f8_ss(tmem + (buf * kStep + j) * C::N, dk + 2 * kk, dqi + 2 * kk, idesc_qk, kk > 0);
+          umma_commit(&sh.k_empty[s]);
+        }
+        __syncwarp();
+      }
       if (!go) return;
-      tc_fence_after();
+      x.left -= m;
+      begins = x.left == 0;
       if (lane == 0) {
-        const uint64_t dk = sdesc_sw128(smem_u32(slots + s * kPage), 16, 1024);
-        const uint64_t dqi = dq + (item & 1) * (C::op >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 features a step
-          umma_f8_ss(tmem + (i & 1) * C::N, dk + 2 * kk, dqi + 2 * kk, idesc_qk, kk > 0);
-        umma_commit(&sh.s_full[i & 1]);
-        umma_commit(&sh.empty[s]);
-        if (last >> (i & 31) & 1u) umma_commit(&sh.q_empty[item & 1]);
+        umma_commit(&sh.s_full[buf]);
+        if (begins) umma_commit(&sh.q_empty[item & 1]);
       }
       __syncwarp();
+      if (begins && ik < n) x.next(pre, a, n - ik);
+      if (sk % 3 == 0) size[0] = m;
+      else if (sk % 3 == 1) size[1] = m;
+      else size[2] = m;
+      ++sk;
     };
-    issue_qk(0);
-    if (go && n > 1) issue_qk(1);
-    for (int i = 0; go && i < n; ++i) {
-      const int pos = v_pos(i, n), s = pos % C::slots;
-      if (!mbar_wait(&sh.p_full[i & 1], (i >> 1) & 1, &sh.abort)) go = false;
-      if (go && !mbar_wait(&sh.full[s], (pos / C::slots) & 1, &sh.abort)) go = false;
-      go = __all_sync(0xffffffffu, go);
-      if (!go) break;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t dv = sdesc_sw128(smem_u32(slots + s * kPage), 1024, 1024);
-        const uint64_t dpi = dp + (i & 1) * (C::op >> 4);
+    issue_qk();
+    if (go) issue_qk();
+    for (int st = 0; go && iv < n; ++st) {
+      const int ob = st % C::bufs;
+      if (!warp_wait(&sh.p_full[ob], (st / C::bufs) & 1, &sh.abort)) go = false;
+      const int m = st % 3 == 0 ? size[0] : st % 3 == 1 ? size[1] : size[2];
+      for (int j = 0; go && j < m; ++j, ++iv) {
+        const int s = iv % C::v_slots;
+        if (!warp_wait(&sh.v_full[s], (iv / C::v_slots) & 1, &sh.abort)) go = false;
+        if (!go) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t dv = sdesc_sw128(smem_u32(sV + s * kPage), 1024, 1024);
+          const uint64_t dpj = dp + (ob * kStep + j) * (C::op >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4096 bytes of V, 32 of P'
-          umma_f8_ss(tmem + 2 * C::N + (i & 1) * C::N, dv + 256 * kk, dpi + 2 * kk, idesc_pv, kk > 0);
-        umma_commit(&sh.o_full[i & 1]);
-        umma_commit(&sh.empty[s]);
+          for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4096 bytes of V, 32 of P'
+            umma_f8_ss(tmem + C::o_col + (ob * kStep + j) * C::N, dv + 256 * kk, dpj + 2 * kk, idesc_pv, kk > 0);
+          umma_commit(&sh.v_empty[s]);
+        }
+        __syncwarp();
       }
+      if (!go) break;
+      if (lane == 0) umma_commit(&sh.o_full[ob]);
       __syncwarp();
-      if (i + 2 < n) issue_qk(i + 2);
+      issue_qk();
     }
     if (lane == 0) {
       if (!go) fail(&sh.abort, a.status, 0x611);
@@ -393,35 +437,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (n > 0 && warp == kQWarp) {
     // Q' of each item of the run: one row at a time, four features a lane.
-    int item = 0;
-    for (int t = 0; t < n; ++item) {
-      const Tile x = find_tile(pre, a, t_lo + t);
-      const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc % a.chunks) * kR;
+    Walk x;
+    x.begin(pre, a, t_lo, n);
+    for (int t = 0, item = 0; t < n; ++item) {
+      const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc - g * a.chunks) * kR;
       if (!warp_wait(&sh.q_empty[buf], ((item >> 1) & 1) ^ 1, &sh.abort)) {
         if (lane == 0) fail(&sh.abort, a.status, 0x613);
         break;
       }
       uint8_t* dst = sQ + buf * C::op;
-#pragma unroll 4
-      for (int r = 0; r < kR; ++r) {
-        const int row = r0 + r;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (row < a.rows) {
-          const int i = row / a.group, h = g * a.group + row % a.group;
-          const uint2 w = *reinterpret_cast<const uint2*>(a.q + x.b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
-          v[0] = __uint_as_float(w.x << 16);
-          v[1] = __uint_as_float(w.x & 0xffff0000u);
-          v[2] = __uint_as_float(w.y << 16);
-          v[3] = __uint_as_float(w.y & 0xffff0000u);
+#pragma unroll 1
+      for (int rb = 0; rb < kR; rb += 8) {
+        uint2 w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int row = r0 + rb + r;
+          w[r] = make_uint2(0u, 0u);
+          if (row < a.rows) {
+            const int i = row / a.group, h = g * a.group + row - i * a.group;
+            w[r] = *reinterpret_cast<const uint2*>(a.q + x.b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
+          }
         }
+#pragma unroll
+      for (int rr = 0; rr < 8; ++rr) {
+        const int r = rb + rr;
+        float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
+                      __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
         float amax = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
           amax = fmaxf(amax, fabsf(v[e]));                          // ignores NaN
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        amax = warp_max(amax);
         const int e2 = scale_exponent(amax);
         const float inv = exp2_int(-e2);
         uint32_t hi = 0, lo = 0;
@@ -439,225 +487,355 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<uint32_t*>(dst + (kR + r) * 128 + at) = lo;
         if (lane == 0) sh.qs[buf][r] = exp2_int(e2) * a.c;
       }
+      }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[buf]);
-      t += x.pages - x.page;
+      t += x.left;
+      if (t < n) x.next(pre, a, n - t);
     }
-  } else if (n > 0 && warp < kWorkers) {
-    const int tid = threadIdx.x;
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const int my_row = lane & (kR - 1);            // row of the lane-held statistics
-    constexpr int kShift = kR == 8 ? 2 : kR == 16 ? 1 : 0;  // warp_rows: lane L holds row L >> kShift
-    float acc[kR], l[kR];
+  } else if (n > 0 && warp < C::workers) {
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int tid = threadIdx.x & 127;              // key of a tile, feature of the output
+    const int row0 = wg * kWgRows;                  // the group's rows of the chunk
+    const int bar = 1 + wg;
+    const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + row0;
+    // byte `tid` of rows row0 + r (hi) and kR + row0 + r (lo) of P'; 16-byte chunks are swizzled by the row's low 3 bits
+    uint8_t* const p_at = sP + row0 * 128 + (tid & 15);
+    const uint32_t p_col = static_cast<uint32_t>(tid >> 4);
+    const int my_row = lane & (kWgRows - 1);        // row of the lane-held maximum
+    float acc[kWgRows], l[kWgRows];
     float m = -INFINITY;                            // running maximum of row my_row, base 2
-    int item = -1;
     bool ok = true;
-    // tiles by 32: each lane looks up one
-    Tile mine{};
-    int z = -1;
+    // tiles by 32: lane L looks up tile win + L (its page, scales, and sequence's length)
+    int win = 0, z = -1, ln = 0;
     float ks = 0.f, vs = 0.f;
-    // of the tile whose O is still to be added
-    float o_vs = 0.f;
-    int o_tail0 = 0, o_ntail = 0, o_g = 0, o_z = -1, o_row0 = 0;
-
-    auto add_o = [&](int i) -> bool {
-      if (!warp_wait(&sh.o_full[i & 1], (i >> 1) & 1, &sh.abort)) return false;
-      tc_fence_after();
-      float o[kR];
-      load_rows<kR>(tmem + lane_addr + 2 * C::N + (i & 1) * C::N, o);
-      if (o_ntail > 0) {
-        // keys that only the later tokens see: added here, one by one, so
-        // that what they hold does not reach the rows that do not see them
-        const uint8_t* vp = a.v + o_z * a.page_stride + o_g * a.head_stride + tid;
-        for (int k = 0; k < o_ntail; ++k) {
-          float val, none;
-          unpack_e4m3x2(vp[(o_row0 + k) * kD], val, none);
-#pragma unroll
-          for (int r = 0; r < kR; ++r) {
-            const float p = sh.tail[i & 1][r][o_tail0 + k];
-            if (p >= 0.f || p != p) o[r] = fmaf(p, val, o[r]);  // -1: not seen
-          }
+    auto look_up = [&](int i) {
+      win = i;
+      z = -1;
+      ks = vs = 0.f;
+      if (i + lane < n) {
+        Walk y;
+        y.begin(pre, a, t_lo + i + lane, n);
+        z = page_id(a, y.b, y.page);
+        bool bad;
+        ln = clamped_len(a, y.b, bad);
+        if (z >= 0) {
+          const int64_t at = static_cast<int64_t>(z) * a.hkv + y.gc / a.chunks;
+          ks = a.k_scale[at];
+          vs = a.v_scale[at];
         }
       }
-      const float* al = sh.alpha[warp][i & 1];
-      const float* wl = sh.wl[warp][i & 1];
+    };
+    Walk x;
+    x.begin(pre, a, t_lo, n);
+    look_up(0);
+    int item = 0, i = 0, steps = 0, len = 0, g = 0, r0 = 0, toks_r0 = -1;
+    uint32_t toks = 0;
+    auto tok_of = [&](int r) { return static_cast<int>(toks >> (4 * r) & 15u); };
+    bool begins = true;
+    // An item as its end needs it (`end`: the page behind the last one taken).
+    struct Item {
+      int b, gc, g, r0, end, pages, len;
+      uint32_t toks;
+    };
+    // the step whose O is still to be added
+    struct {
+      int tiles, page;
+      float vs[kStep];
+      bool tail;
+    } o{};
+    Item prev{};  // its item (one buffer: an item ends while the next one's first step runs)
+
+    // A page's rows [lo, end) hold keys that only the later tokens see.
+    auto tail_rows = [&](int len, int page, int& lo, int& end) {
+      lo = max(len - (a.q_len - 1) - page * kB, 0);
+      end = min(max(len - page * kB, 0), kB);
+    };
+
+    auto add_o = [&](int st, const Item& of) -> bool {
+      const int ob = st % C::bufs;
+      if (!warp_wait(&sh.o_full[ob], (st / C::bufs) & 1, &sh.abort)) return false;
+      tc_fence_after();
+      float wl[kWgRows];
+      load8(sh.wl[warp][ob], wl);
 #pragma unroll
-      for (int r = 0; r < kR; ++r) acc[r] = fmaf(o[r], wl[r] * o_vs, acc[r] * al[r]);
+      for (int j = 0; j < kStep; ++j) {
+        if (j >= o.tiles) break;
+        float v[kWgRows];
+        load_rows(lane_tmem + C::o_col + (ob * kStep + j) * C::N, kR, v);
+        if (o.tail) {
+          // added here, one by one, so that what those keys hold does not
+          // reach the rows that do not see them
+          const int page = o.page + j, id = page_id(a, of.b, page);
+          int lo, end;
+          tail_rows(of.len, page, lo, end);
+          const int first = page * kB - (of.len - (a.q_len - 1));  // row 0's place among those keys
+          const uint8_t* vp = a.v + id * a.page_stride + of.g * a.head_stride + tid;
+          for (int k = lo; id >= 0 && k < end; ++k) {
+            float val, none;
+            unpack_e4m3x2(vp[k * kD], val, none);
+#pragma unroll
+            for (int r = 0; r < kWgRows; ++r) {
+              const float p = sh.tail[ob][row0 + r][first + k];
+              if (p >= 0.f || p != p) v[r] = fmaf(p, val, v[r]);  // -1: not seen
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kWgRows; r += 2) {
+          float w0, w1;
+          fmul2(w0, w1, wl[r], wl[r + 1], o.vs[j], o.vs[j]);
+          ffma2(acc[r], acc[r + 1], v[r], v[r + 1], w0, w1, acc[r], acc[r + 1]);
+        }
+      }
       return true;
     };
 
-    for (int i = 0; ok && i < n; ++i) {
-      const int k32 = i & 31, buf = i & 1;
-      if (k32 == 0) {
-        z = -1;
-        ks = vs = 0.f;
-        if (i + lane < n) {
-          mine = find_tile(pre, a, t_lo + i + lane);
-          z = page_id(a, mine);
-          if (z >= 0) {
-            const int64_t at = static_cast<int64_t>(z) * a.hkv + mine.gc / a.chunks;
-            ks = a.k_scale[at];
-            vs = a.v_scale[at];
-          }
+    // The end of an item in this run; i_end: tiles of the run up to it.
+    auto finish = [&](int i_end, const Item& of) {
+      const float wsum = warp_rows<kWgRows, false>(l);
+      if ((lane & 3) == 0) sh.sum[wg][quarter][lane >> 2] = wsum;
+      named_bar_sync(bar, 128);
+      const long long t_item = t_lo + i_end - of.end;  // the item's first tile
+      const bool whole = t_item >= t_lo && of.end == of.pages;
+      const int slot = 2 * run + (t_item < t_lo ? 0 : 1);
+      const int nr = min(kWgRows, a.rows - of.r0);
+      // lane r holds row r's sum, its inverse, and where it goes
+      const float (&sum)[4][kWgRows] = sh.sum[wg];
+      const float ls = (sum[0][my_row] + sum[1][my_row]) + (sum[2][my_row] + sum[3][my_row]);
+      if (whole) {
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;
+        const int tok = static_cast<int>(of.toks >> (4 * my_row) & 15u), h = of.g * a.group + of.r0 + my_row - tok * a.group;
+        const int64_t at = of.b * a.o_b + h * a.o_h + tok * a.o_t;
+#pragma unroll
+        for (int r = 0; r < kWgRows; ++r) {
+          const float f = bcast(inv, r);
+          const int64_t to = bcast(at, r);
+          if (r < nr) a.out[to + tid] = __float2bfloat16_rn(acc[r] * f);
+        }
+        if (kScores && tid < nr)
+          a.lse[(static_cast<int64_t>(of.b) * a.hkv + of.g) * a.rows + of.r0 + tid] = ls == 0.f ? INFINITY : m + log2f(ls);
+      } else {
+        float* to = a.part + (static_cast<int64_t>(slot) * kR + row0) * kD + tid;
+#pragma unroll
+        for (int r = 0; r < kWgRows; ++r)
+          if (r < nr) to[r * kD] = acc[r];
+        if (tid < nr) a.part_ml[slot * kR + row0 + tid] = make_float2(m, ls);
+      }
+      if (i_end == n && threadIdx.x == 0) {
+        // an item that begins here and goes on is joined under this CTA's number
+        const bool goes_on = t_item >= t_lo && of.end < of.pages;
+        a.split[run] = Split{goes_on ? of.b : -1, of.gc, run_of(total, t_item + of.pages - 1, runs), 0};
+      }
+    };
+
+    for (int st = 0; ok && i < n; ++st) {
+      const int mt_tiles = min(kStep, x.left), buf = st & 1;
+      if (i + kStep > win + 32) look_up(i);
+      if (begins) {
+        len = bcast(ln, i - win);
+        g = a.chunks == 1 ? x.gc : x.gc / a.chunks;
+        r0 = (x.gc - g * a.chunks) * kR + row0;
+        if (r0 != toks_r0) {
+          // the rows' tokens, four bits each (rows past the last count as the last token's)
+          toks_r0 = r0;
+          const int tok = a.q_len == 1 ? 0 : min((r0 + my_row) / a.group, kMaxQLen - 1);
+          toks = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(tok) << (4 * my_row));
+        }
+        if (!warp_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) {
+          ok = false;
+          break;
         }
       }
-      const int b = bcast(mine.b, k32), gc = bcast(mine.gc, k32), page = bcast(mine.page, k32);
-      const int pages = bcast(mine.pages, k32), len = bcast(mine.len, k32), zt = bcast(z, k32);
-      const float kst = bcast(ks, k32), vst = bcast(vs, k32);
-      const int g = gc / a.chunks, r0 = (gc - g * a.chunks) * kR;
-      if (i == 0 || page == 0) {
-        ++item;
-        m = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < kR; ++r) acc[r] = l[r] = 0.f;
-      }
-      if (!warp_wait(&sh.s_full[buf], (i >> 1) & 1, &sh.abort) ||
-          !warp_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) {
+      if (!warp_wait(&sh.s_full[buf], (st >> 1) & 1, &sh.abort)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      float s[kR];
-      load_rows<kR>(tmem + lane_addr + buf * C::N, s);
-      const float* qs = sh.qs[item & 1];
+      // Row r's token sees the keys below len - (q_len - 1) + its number.
+      float s[kStep][kWgRows], t[kWgRows], vst[kStep];
+      bool partial[kStep], held[kStep];  // some rows do not see some keys; the page is there
+      load8(&sh.qs[item & 1][row0], t);
 #pragma unroll
-      for (int r = 0; r < kR; ++r) s[r] *= qs[r] * kst;
-      // Row r belongs to token (r0 + r) / group, which sees keys below all_see + that.
-      const int key0 = page * kB, all_see = zt < 0 ? -1 : len - (a.q_len - 1);
-      const bool partial = key0 + kB > all_see;
-      if (partial) {
-        const int past = zt < 0 ? kB : key0 + tid - all_see;  // < 0: every row sees the key
+      for (int j = 0; j < kStep; ++j) {
+        held[j] = bcast(z, (i - win + j) & 31) >= 0;
+        vst[j] = bcast(vs, (i - win + j) & 31);
+        const float kst = bcast(ks, (i - win + j) & 31);
+        if (j >= mt_tiles) {
+          partial[j] = false;
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
-          if (past >= 0 && (zt < 0 || past >= (r0 + r) / a.group)) s[r] = -INFINITY;
+          for (int r = 0; r < kWgRows; ++r) s[j][r] = -INFINITY;
+          continue;
+        }
+        load_rows(lane_tmem + (buf * kStep + j) * C::N, kR, s[j]);
+#pragma unroll
+        for (int r = 0; r < kWgRows; r += 2) {
+          float c0, c1;
+          fmul2(c0, c1, t[r], t[r + 1], kst, kst);
+          fmul2(s[j][r], s[j][r + 1], s[j][r], s[j][r + 1], c0, c1);
+        }
+        const int past = (x.page + j) * kB + tid - (len - (a.q_len - 1));  // < 0: every row sees the key
+        partial[j] = !held[j] || (x.page + j + 1) * kB > len - (a.q_len - 1);
+        if (partial[j]) {
+#pragma unroll
+          for (int r = 0; r < kWgRows; ++r)
+            if (!held[j] || past >= tok_of(r)) s[j][r] = -INFINITY;
+        }
       }
-      if (a.scores != nullptr) {
-        float* dst = a.scores + ((static_cast<int64_t>(b) * a.hkv + g) * a.rows + r0) *
-                                    (static_cast<int64_t>(a.max_pages) * kB) + key0 + tid;
+      // The step's row maxima, over the group's four warps.
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
-          if (r0 + r < a.rows) dst[static_cast<int64_t>(r) * a.max_pages * kB] = s[r];
+      for (int r = 0; r < kWgRows; ++r) t[r] = warp_max(fmaxf(s[0][r], s[1][r]));
+      if (lane == 0) {
+        float4* red = reinterpret_cast<float4*>(sh.red[buf][wg][quarter]);
+        red[0] = make_float4(t[0], t[1], t[2], t[3]);
+        red[1] = make_float4(t[4], t[5], t[6], t[7]);
       }
-      // The tile's row maxima, over the four warps.
+      // The step before: its product has run meanwhile.
+      if (C::bufs == 1 && st > 0 && !add_o(st - 1, prev)) {
+        ok = false;
+        break;
+      }
+      if (begins) {
+        if (C::bufs == 1 && st > 0) finish(i, prev);
+#pragma unroll
+        for (int r = 0; r < kWgRows; ++r) acc[r] = l[r] = 0.f;
+        m = -INFINITY;
+      }
+      named_bar_sync(bar, 128);
+      if (x.left == mt_tiles && tid == 0) mbar_arrive(&sh.q_empty[item & 1]);  // the item's last step has its q scales
       {
-        float t[kR];
-#pragma unroll
-        for (int r = 0; r < kR; ++r) t[r] = s[r];
-        const float wm = warp_rows<kR, true>(t);
-        if ((lane & ((1 << kShift) - 1)) == 0) sh.red[buf][warp][lane >> kShift] = wm;
-      }
-      named_bar_sync(1, kWorkers * 32);
-      {
-        const float mt = fmaxf(fmaxf(sh.red[buf][0][my_row], sh.red[buf][1][my_row]),
-                               fmaxf(sh.red[buf][2][my_row], sh.red[buf][3][my_row]));
+        const float (&red)[4][kWgRows] = sh.red[buf][wg];
+        const float mt = fmaxf(fmaxf(red[0][my_row], red[1][my_row]), fmaxf(red[2][my_row], red[3][my_row]));
         const float mn = fmaxf(m, mt);
         // a row without keys so far: nothing to scale, and weight 0 (2^(-inf))
         const float base2 = mn == -INFINITY ? 0.f : mn;
-        if (lane < kR) {
+        if (lane < kWgRows) {
+          const float al = ex2_approx(m - base2);
           sh.ref[warp][my_row] = mt == -INFINITY ? 0.f : mt - 8.f;
-          sh.alpha[warp][buf][my_row] = ex2_approx(m - base2);
-          sh.wl[warp][buf][my_row] = ex2_approx(mt - base2 - 8.f);
+          sh.alpha[warp][my_row] = al;
+          sh.wl[warp][st % C::bufs][my_row] = ex2_approx(mt - base2 - 8.f);
+          // the O still to be added is weighted for the maximum before
+          if (C::bufs == 2 && !begins) sh.wl[warp][(st - 1) % C::bufs][my_row] *= al;
         }
         m = mn;
       }
       __syncwarp();
-      uint8_t* dst = sP + buf * C::op;
-      const int ntail_lo = max(all_see - key0, 0);           // first row of the page some rows do not see
-      const int row_end = min(max(len - key0, 0), kB);       // tokens held in the page
-      const bool is_tail = partial && zt >= 0 && tid >= ntail_lo && tid < row_end;
-      const uint32_t col = ((tid >> 4) << 4), in16 = tid & 15;
+      float wl[kWgRows];
+      load8(sh.alpha[warp], t);
+      load8(sh.wl[warp][st % C::bufs], wl);
 #pragma unroll
-      for (int r = 0; r < kR; r += 2) {
-        float p0 = ex2_approx(s[r] - sh.ref[warp][r]), p1 = ex2_approx(s[r + 1] - sh.ref[warp][r + 1]);
-        l[r] = fmaf(p0, sh.wl[warp][buf][r], l[r] * sh.alpha[warp][buf][r]);
-        l[r + 1] = fmaf(p1, sh.wl[warp][buf][r + 1], l[r + 1] * sh.alpha[warp][buf][r + 1]);
-        if (is_tail) {
-          const int past = key0 + tid - all_see;
-          sh.tail[buf][r][past] = past < (r0 + r) / a.group ? p0 : -1.f;
-          sh.tail[buf][r + 1][past] = past < (r0 + r + 1) / a.group ? p1 : -1.f;
-          p0 = p1 = 0.f;
-        }
-        const uint16_t hi = pack_e4m3x2(p0, p1);
-        float h0, h1;
-        unpack_e4m3x2(hi, h0, h1);
-        const uint16_t lo = pack_e4m3x2((p0 - h0) * kLo, (p1 - h1) * kLo);
-        const uint32_t c0 = (col ^ ((r & 7) << 4)) + in16, c1 = (col ^ (((r + 1) & 7) << 4)) + in16;
-        dst[r * 128 + c0] = static_cast<uint8_t>(hi);
-        dst[(r + 1) * 128 + c1] = static_cast<uint8_t>(hi >> 8);
-        dst[(kR + r) * 128 + c0] = static_cast<uint8_t>(lo);
-        dst[(kR + r + 1) * 128 + c1] = static_cast<uint8_t>(lo >> 8);
+      for (int r = 0; r < kWgRows; r += 2) {
+        fmul2(acc[r], acc[r + 1], acc[r], acc[r + 1], t[r], t[r + 1]);
+        fmul2(l[r], l[r + 1], l[r], l[r + 1], t[r], t[r + 1]);
       }
-      if (partial) {
-        // V rows that not every row sees become zeros: p = 0 there, and what
-        // the page holds (anything past the end) must not matter
-        const int pos = v_pos(i, n), sl = pos % C::slots;
-        if (!warp_wait(&sh.full[sl], (pos / C::slots) & 1, &sh.abort)) {
-          ok = false;
-          break;
-        }
-        if (tid >= ntail_lo) {
-          uint4* rowp = reinterpret_cast<uint4*>(slots + sl * kPage + tid * 128);
+      load8(sh.ref[warp], t);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rowp[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < kStep; ++j) {
+        if (j >= mt_tiles) break;
+        float p[kWgRows];
+#pragma unroll
+        for (int r = 0; r < kWgRows; ++r) p[r] = ex2_approx(s[j][r] - t[r]);
+#pragma unroll
+        for (int r = 0; r < kWgRows; r += 2) ffma2(l[r], l[r + 1], p[r], p[r + 1], wl[r], wl[r + 1], l[r], l[r + 1]);
+        if (partial[j]) {
+          int lo, end;
+          tail_rows(len, x.page + j, lo, end);
+          if (!held[j]) lo = 0;
+          if (held[j] && tid >= lo && tid < end) {
+            const int past = (x.page + j) * kB + tid - (len - (a.q_len - 1));
+#pragma unroll
+            for (int r = 0; r < kWgRows; ++r) {
+              sh.tail[st % C::bufs][row0 + r][past] = past < tok_of(r) ? p[r] : -1.f;
+              p[r] = 0.f;
+            }
+          }
+          if (wg == 0) {
+            // V rows that not every row sees become zeros: p = 0 there, and what
+            // the page holds (anything past the end) must not matter
+            const int sl = (i + j) % C::v_slots;
+            if (!warp_wait(&sh.v_full[sl], ((i + j) / C::v_slots) & 1, &sh.abort)) ok = false;
+            if (tid >= lo) {
+              uint4* rowp = reinterpret_cast<uint4*>(sV + sl * kPage + tid * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) rowp[e] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kWgRows; r += 2) {
+          uint16_t hi, lo;
+          split_e4m3x2(p[r], p[r + 1], hi, lo);
+          const uint32_t c0 = r * 128 + ((p_col ^ r) << 4), c1 = (r + 1) * 128 + ((p_col ^ (r + 1)) << 4);
+          uint8_t* at = p_at + (st % C::bufs * kStep + j) * C::op;
+          at[c0] = static_cast<uint8_t>(hi);
+          at[c1] = static_cast<uint8_t>(hi >> 8);
+          at[kR * 128 + c0] = static_cast<uint8_t>(lo);
+          at[kR * 128 + c1] = static_cast<uint8_t>(lo >> 8);
         }
       }
+      if (!ok) break;
       fence_async_shared();
       tc_fence_before();
-      mbar_arrive(&sh.p_full[buf]);
-      // The tile before: its product has run meanwhile.
-      if (i > 0 && page != 0 && !add_o(i - 1)) {
+      mbar_arrive(&sh.p_full[st % C::bufs]);
+      if (kScores) {
+        const int64_t cap = static_cast<int64_t>(a.max_pages) * kB;
+        float* dst = a.scores + ((static_cast<int64_t>(x.b) * a.hkv + g) * a.rows + r0) * cap + x.page * kB + tid;
+        const int nr = min(kWgRows, a.rows - r0);
+#pragma unroll
+        for (int r = 0; r < kWgRows; ++r) {
+          if (r >= nr) break;
+          dst[0] = s[0][r];
+          if (mt_tiles > 1) dst[kB] = s[1][r];
+          dst += cap;
+        }
+      }
+      const Item now{x.b, x.gc, g, r0, x.page + mt_tiles, x.pages, len, toks};
+      if (C::bufs == 2 && !begins && !add_o(st - 1, now)) {
         ok = false;
         break;
       }
-      o_vs = vst;
-      o_z = zt;
-      o_g = g;
-      o_row0 = ntail_lo;
-      o_tail0 = key0 + ntail_lo - all_see;
-      o_ntail = partial && zt >= 0 ? max(row_end - ntail_lo, 0) : 0;
-      if (o_ntail > 0) named_bar_sync(2, kWorkers * 32);  // every warp's tail p is written
-      if (i == n - 1 || page == pages - 1) {
-        // End of the item in this run.
-        if (!add_o(i)) {
-          ok = false;
-          break;
-        }
-        const float wsum = warp_rows<kR, false>(l);
-        named_bar_sync(1, kWorkers * 32);  // red's readers of this tile are done
-        if ((lane & ((1 << kShift) - 1)) == 0) sh.red[buf][warp][lane >> kShift] = wsum;
-        if (lane < kR) sh.ref[warp][my_row] = m;
-        named_bar_sync(1, kWorkers * 32);
-        if (tid == 0) mbar_arrive(&sh.q_empty[item & 1]);
-        const long long t_item = t_lo + i - page;  // the item's first tile
-        const bool whole = t_item >= t_lo && page == pages - 1;
-        const int slot = 2 * blockIdx.x + (t_item < t_lo ? 0 : 1);
-        const int nr = min(kR, a.rows - r0);
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          if (r >= nr) break;
-          const float ls = (sh.red[buf][0][r] + sh.red[buf][1][r]) + (sh.red[buf][2][r] + sh.red[buf][3][r]);
-          if (whole) {
-            const int tok = (r0 + r) / a.group, h = g * a.group + (r0 + r) % a.group;
-            const float v = ls == 0.f ? 0.f : acc[r] / ls;
-            a.out[b * a.o_b + h * a.o_h + tok * a.o_t + tid] = __float2bfloat16_rn(v);
-          } else {
-            a.part[(static_cast<int64_t>(slot) * kR + r) * kD + tid] = acc[r];
+      o.tiles = mt_tiles;
+      o.page = x.page;
+      o.vs[0] = vst[0];
+      o.vs[1] = vst[1];
+      o.tail = a.q_len > 1 && (partial[0] || partial[1]);
+      if (o.tail) named_bar_sync(bar, 128);  // every warp's tail p is written
+      if (C::bufs == 1) prev = now;
+      x.left -= mt_tiles;
+      x.page += mt_tiles;
+      i += mt_tiles;
+      steps = st + 1;
+      begins = x.left == 0;
+      if (begins) {
+        if (C::bufs == 2) {
+          if (!add_o(st, now)) {
+            ok = false;
+            break;
           }
+          finish(i, now);
         }
-        if (tid < nr) {
-          const float ls = (sh.red[buf][0][tid] + sh.red[buf][1][tid]) + (sh.red[buf][2][tid] + sh.red[buf][3][tid]);
-          const float mr = sh.ref[warp][tid];
-          if (whole)
-            a.lse[(static_cast<int64_t>(b) * a.hkv * a.chunks + gc) * kR + tid] =
-                ls == 0.f ? INFINITY : mr + log2f(ls);
-          else
-            a.part_ml[slot * kR + tid] = make_float2(mr, ls);
-        }
-        named_bar_sync(1, kWorkers * 32);  // red and ref are free again
+        ++item;
+        if (i < n) x.next(pre, a, n - i);
       }
     }
-    if (!ok && lane == 0) fail(&sh.abort, a.status, 0x614);
+    if (C::bufs == 1) {
+      if (ok && add_o(steps - 1, prev)) finish(n, prev);
+      else ok = false;
+    }
+    if (!ok) {
+      if (lane == 0) fail(&sh.abort, a.status, 0x614);
+      if (threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
+    }
+  }
+  if (n == 0 && threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
+  // Sequences without a page have no tile: their rows of the output are zeros.
+  for (int b = run; b < a.batch; b += a.ctas) {
+    if (pre[b + 1] != pre[b]) continue;
+    for (int e = threadIdx.x; e < a.hkv * a.rows * kD; e += C::threads) {
+      const int d = e % kD, row = e / kD % a.rows, g = e / kD / a.rows;
+      a.out[b * a.o_b + (g * a.group + row % a.group) * a.o_h + row / a.group * a.o_t + d] = __float2bfloat16_rn(0.f);
+    }
   }
 
   tc_fence_before();
@@ -666,195 +844,171 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kMmaWarp) tmem_dealloc(tmem, C::tmem);
 }
 
-constexpr int kJoinThreads = 512;
-constexpr int kWeightKeys = 2 * kJoinThreads;  // keys a block of the weights part takes
+constexpr int kJoinThreads = 256;
 
-// Joins the items that several CTAs worked on, and adds the weights. Blocks
-// [0, batch * hkv * rows): one row of the output. The rest: kWeightKeys keys of
-// one sequence and kv head.
-__global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const __grid_constant__ Args a, int kr, const float* w_in, float* w_out, int key_blocks) {
+// Joins the items that several CTAs worked on: block (c, r) takes row r of the
+// item that begins in CTA c and goes on. Eight warps share the CTAs of the
+// item, a lane has four features; the sums run in a fixed order.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int kr) {
+  constexpr int kWarps = kJoinThreads / 32;
   __shared__ float f[kMaxDecodeCtas];
-  __shared__ float red[kJoinThreads];
-  __shared__ int pages_before[kJoinThreads / 32], pages_all[kJoinThreads / 32];
-  __shared__ float lse[kMaxGroupRows];
+  __shared__ float red_m[kWarps], red_l[kWarps];
+  __shared__ float4 red[kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rows_total = a.batch * a.hkv * a.rows;
-  const bool is_row = static_cast<int>(blockIdx.x) < rows_total;
-  int b, g, row = 0, kb = 0;
-  if (is_row) {
-    row = blockIdx.x % a.rows;
-    const int bg = blockIdx.x / a.rows;
-    b = bg / a.hkv;
-    g = bg % a.hkv;
-  } else {
-    const int x = blockIdx.x - rows_total;
-    kb = x % key_blocks;
-    b = x / key_blocks / a.hkv;
-    g = x / key_blocks % a.hkv;
-  }
-  bool bad;
-  const int len = clamped_len(a, b, bad), pages = (len + kB - 1) / kB;
-  if (!is_row && kb * kWeightKeys >= len) return;
-  // pages of the sequences before b, and of all
-  int mine = 0, all = 0;
-  for (int x = tid; x < a.batch; x += kJoinThreads) {
-    bool bx;
-    const int p = (clamped_len(a, x, bx) + kB - 1) / kB;
-    all += p;
-    if (x < b) mine += p;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if (lane == 0) {
-    pages_before[warp] = mine;
-    pages_all[warp] = all;
-  }
-  __syncthreads();
-  mine = all = 0;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    mine += pages_before[w];
-    all += pages_all[w];
-  }
-  const int hc = a.hkv * a.chunks;
-  const long long total = static_cast<long long>(all) * hc;
+  const int c0 = blockIdx.x, r = blockIdx.y;
+  grid_dep_launch();
   grid_dep_wait();
-
-  // The CTAs of row chunk c of this (sequence, kv head): c0 .. c1.
-  auto span = [&](int c, int& c0, int& c1) {
-    const long long s0 = static_cast<long long>(mine) * hc + static_cast<long long>(g * a.chunks + c) * pages;
-    c0 = run_of(total, s0, sharing(total, a.ctas));
-    c1 = run_of(total, s0 + pages - 1, sharing(total, a.ctas));
-  };
-  auto slot_of = [](int c, int c0) { return 2 * c + (c == c0 ? 1 : 0); };
-
-  if (is_row) {
-    const int tok = row / a.group, h = g * a.group + row % a.group;
-    __nv_bfloat16* dst = a.out + b * a.o_b + h * a.o_h + tok * a.o_t;
-    if (pages == 0) {
-      if (tid < kD) dst[tid] = __float2bfloat16_rn(0.f);
-      return;
-    }
-    const int chunk = row / kr, r = row - chunk * kr;
-    int c0, c1;
-    span(chunk, c0, c1);
-    if (c0 == c1) return;  // finished by its CTA
-    const int nc = c1 - c0 + 1;
-    // factors 2^(m_c - M), in CTA order; nc <= kMaxDecodeCtas <= kJoinThreads
-    float mc = -INFINITY, lc = 0.f;
-    if (tid < nc) {
-      const float2 ml = a.part_ml[slot_of(c0 + tid, c0) * kr + r];
-      mc = ml.x;
-      lc = ml.y;
-    }
-    red[tid] = mc;
-    __syncthreads();
-    float M = -INFINITY;
-    for (int x = lane; x < nc; x += 32) M = fmaxf(M, red[x]);
+  const Split sp = a.split[c0];
+  const int g = sp.gc / a.chunks, row = (sp.gc - g * a.chunks) * kr + r;
+  if (sp.b < 0 || row >= a.rows) return;
+  const int nc = sp.last - c0 + 1;
+  auto slot_of = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
+  float m = -INFINITY;
+  for (int x = tid; x < nc; x += kJoinThreads) m = fmaxf(m, a.part_ml[slot_of(x) * kr + r].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    __syncthreads();
-    if (tid < nc) {
-      const float fc = ex2_approx(mc - (M == -INFINITY ? 0.f : M));
-      f[tid] = fc;
-      red[tid] = fc * lc;
-    }
-    __syncthreads();
-    float L = 0.f;
-    for (int x = lane; x < nc; x += 32) L += red[x];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    __syncthreads();
-    const int d = tid & (kD - 1), part = tid / kD;
-    float acc = 0.f;
-#pragma unroll 4
-    for (int x = part; x < nc; x += kJoinThreads / kD)
-      acc = fmaf(f[x], a.part[(static_cast<int64_t>(slot_of(c0 + x, c0)) * kr + r) * kD + d], acc);
-    red[tid] = acc;
-    __syncthreads();
-    if (tid < kD) {
-      float v = 0.f;
-      for (int x = 0; x < kJoinThreads / kD; ++x) v += red[tid + x * kD];
-      dst[tid] = __float2bfloat16_rn(L == 0.f ? 0.f : v / L);
-    }
-    return;
-  }
-
-  // weights_out = weights_in + sum over the rows of 2^(s - lse)
-  for (int row2 = warp; row2 < a.rows; row2 += kJoinThreads / 32) {
-    const int chunk = row2 / kr, r = row2 - chunk * kr;
-    int c0, c1;
-    span(chunk, c0, c1);
-    float v;
-    if (c0 == c1) {
-      v = a.lse[(static_cast<int64_t>(b) * hc + g * a.chunks + chunk) * kr + r];
-    } else {
-      float M = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[slot_of(c, c0) * kr + r].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float L = 0.f;
-      for (int c = c0 + lane; c <= c1; c += 32) {
-        const float2 ml = a.part_ml[slot_of(c, c0) * kr + r];
-        L = fmaf(ex2_approx(ml.x - (M == -INFINITY ? 0.f : M)), ml.y, L);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      v = L == 0.f ? INFINITY : M + log2f(L);
-    }
-    if (lane == 0) lse[row2] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red_m[warp] = m;
   __syncthreads();
-  const int64_t cap = static_cast<int64_t>(a.max_pages) * kB, bg = static_cast<int64_t>(b) * a.hkv + g;
-  const int key = kb * kWeightKeys + tid * 2;
-  if (key >= len) return;
-  const float* sc = a.scores + bg * a.rows * cap + key;
-  float w0 = 0.f, w1 = 0.f;
+  m = red_m[lane & (kWarps - 1)];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int x = tid; x < nc; x += kJoinThreads) {
+    const float2 ml = a.part_ml[slot_of(x) * kr + r];
+    const float fx = ex2_approx(ml.x - base);
+    f[x] = fx;
+    l = fmaf(fx, ml.y, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red_l[warp] = l;
+  __syncthreads();
+  l = 0.f;
+  for (int w = 0; w < kWarps; ++w) l += red_l[w];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int r = 0; r < a.rows; ++r) {
-    const float2 s = *reinterpret_cast<const float2*>(sc + r * cap);
-    w0 += ex2_approx(s.x - lse[r]);
-    w1 += ex2_approx(s.y - lse[r]);
+  for (int x = warp; x < nc; x += kWarps) {
+    const float4 v = *reinterpret_cast<const float4*>(
+        a.part + (static_cast<int64_t>(slot_of(x)) * kr + r) * kD + lane * 4);
+    acc.x = fmaf(f[x], v.x, acc.x);
+    acc.y = fmaf(f[x], v.y, acc.y);
+    acc.z = fmaf(f[x], v.z, acc.z);
+    acc.w = fmaf(f[x], v.w, acc.w);
   }
-  const int64_t at = bg * cap + key;
-  if (w_in != nullptr) {
-    w0 += w_in[at];
-    if (key + 1 < len) w1 += w_in[at + 1];
+  red[warp][lane] = acc;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 v = red[w][lane];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* dst = a.out + sp.b * a.o_b + (g * a.group + row % a.group) * a.o_h + row / a.group * a.o_t;
+    *reinterpret_cast<uint2*>(dst + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[(static_cast<int64_t>(sp.b) * a.hkv + g) * a.rows + row] = l == 0.f ? INFINITY : m + log2f(l);
   }
-  if (key + 1 < len)
-    *reinterpret_cast<float2*>(w_out + at) = make_float2(w0, w1);
-  else
-    w_out[at] = w0;
 }
 
-int rows_per_cta(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// weights_out = weights_in + the sum over the rows of 2^(s - lse): kWeightKeys
+// keys of one sequence and kv head a block, four a thread at a time.
+constexpr int kWeightThreads = 256;
+constexpr int kWeightKeys = 4 * kWeightThreads;
+__global__ void __launch_bounds__(kWeightThreads)
+    weights_kernel(const __grid_constant__ Args a, const float* w_in, float* w_out) {
+  __shared__ float lse[kMaxGroupRows];
+  const int g = blockIdx.y, b = blockIdx.z;
+  bool bad;
+  const int len = clamped_len(a, b, bad);
+  const int key = blockIdx.x * kWeightKeys + threadIdx.x * 4;
+  if (static_cast<int>(blockIdx.x) * kWeightKeys >= len) return;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * kB, bg = static_cast<int64_t>(b) * a.hkv + g;
+  const int64_t at = bg * cap + key;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  // rows of weights and scores end at a multiple of 128: whole groups of four are there
+  if (w_in != nullptr && key < len) w = *reinterpret_cast<const float4*>(w_in + at);
+  grid_dep_wait();
+  for (int r = threadIdx.x; r < a.rows; r += kWeightThreads) lse[r] = a.lse[bg * a.rows + r];
+  __syncthreads();
+  if (key >= len) return;
+  const float* sc = a.scores + bg * a.rows * cap + key;
+  float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = 0; r < a.rows; ++r) {
+    const float4 s = __ldcs(reinterpret_cast<const float4*>(sc + r * cap));
+    const float e = lse[r];
+    p.x += ex2_approx(s.x - e);
+    p.y += ex2_approx(s.y - e);
+    p.z += ex2_approx(s.z - e);
+    p.w += ex2_approx(s.w - e);
+  }
+  w.x += p.x;
+  w.y += p.y;
+  w.z += p.z;
+  w.w += p.w;
+  if (key + 4 <= len) {
+    *reinterpret_cast<float4*>(w_out + at) = w;
+  } else {
+    const float v[3] = {w.x, w.y, w.z};
+    for (int e = 0; key + e < len; ++e) w_out[at + e] = v[e];
+  }
+}
 
-template <int kR>
-cudaError_t launch_rows(const KvMaps& maps, const Args& a, cudaStream_t st) {
-  using C = Cfg<kR>;
+int groups_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <int kWG, bool kScores>
+cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {
+  using C = Cfg<kWG>;
   const uint32_t smem = C::smem + (a.batch + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e =
+      cudaFuncSetAttribute(decode_kernel<kWG, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_kernel<kR><<<a.ctas, kThreads, smem, st>>>(maps.k, maps.v, a);
+  decode_kernel<kWG, kScores><<<a.ctas, C::threads, smem, st>>>(maps.k, maps.v, a);
   return cudaGetLastError();
+}
+template <int kWG>
+cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {
+  return a.scores != nullptr ? launch_groups<kWG, true>(maps, a, st) : launch_groups<kWG, false>(maps, a, st);
+}
+
+// Launches that may start while the kernel before them ends (they wait for its results themselves).
+template <class... P, class... Q>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, Q&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
 }  // namespace
 
-int decode_row_chunks(int rows) { return (rows + rows_per_cta(rows) - 1) / rows_per_cta(rows); }
+int decode_row_chunks(int rows) {
+  const int kr = groups_of(rows) * kWgRows;
+  return (rows + kr - 1) / kr;
+}
 
 DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights) {
-  const int rows = hq / c.hkv * q_len, kr = rows_per_cta(rows), chunks = (rows + kr - 1) / kr;
+  const size_t rows = static_cast<size_t>(hq / c.hkv) * q_len, kr = groups_of(static_cast<int>(rows)) * kWgRows;
   DecodeLayout L{};
   size_t o = align_up(sizeof(DevStatus));
   L.part = o;    o = align_up(o + size_t(2) * kMaxDecodeCtas * kr * kD * 4);
   L.part_ml = o; o = align_up(o + size_t(2) * kMaxDecodeCtas * kr * 8);
-  L.lse = o;     o = align_up(o + size_t(c.batch) * c.hkv * chunks * kr * 4);
+  L.split = o;   o = align_up(o + size_t(kMaxDecodeCtas) * sizeof(Split));
+  L.lse = o;
+  if (with_weights) o = align_up(o + c.batch * c.hkv * rows * 4);
   L.scores = o;
-  if (with_weights) o = align_up(o + size_t(c.batch) * c.hkv * rows * c.max_pages * kB * 4);
+  if (with_weights) o = align_up(o + c.batch * c.hkv * rows * c.max_pages * kB * 4);
   L.total = o;
   return L;
 }
@@ -869,13 +1023,13 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
   a.group = hq / c.hkv;
   a.q_len = q_len;
   a.rows = a.group * q_len;
-  const int kr = rows_per_cta(a.rows);
-  a.chunks = (a.rows + kr - 1) / kr;
+  const int wg = groups_of(a.rows), kr = wg * kWgRows;
+  a.chunks = decode_row_chunks(a.rows);
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;
-  // two CTAs per SM, and no more than the table can hold tiles
+  // what the chip holds at once, and no more than the table can hold tiles
   const long long most = static_cast<long long>(c.batch) * c.max_pages * c.hkv * a.chunks;
-  a.ctas = static_cast<int>(std::min<long long>(std::min(2 * sms, kMaxDecodeCtas), most));
+  a.ctas = static_cast<int>(std::min<long long>(std::min((wg >= 2 ? 1 : 2) * sms, kMaxDecodeCtas), most));
   a.k_scale = c.k_scale;
   a.v_scale = c.v_scale;
   a.table = c.table;
@@ -894,24 +1048,19 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
   a.c = scale * 1.4426950408889634f;
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
-  a.lse = reinterpret_cast<float*>(ws + L.lse);
+  a.split = reinterpret_cast<Split*>(ws + L.split);
+  a.lse = weights_out ? reinterpret_cast<float*>(ws + L.lse) : nullptr;
   a.scores = weights_out ? reinterpret_cast<float*>(ws + L.scores) : nullptr;
   a.status = reinterpret_cast<DevStatus*>(ws);
-  cudaError_t e = kr == 8 ? launch_rows<8>(maps, a, st) : kr == 16 ? launch_rows<16>(maps, a, st)
-                                                                   : launch_rows<32>(maps, a, st);
+  cudaError_t e = wg == 1 ? launch_groups<1>(maps, a, st) : wg == 2 ? launch_groups<2>(maps, a, st)
+                                                                    : launch_groups<4>(maps, a, st);
   if (e != cudaSuccess) return e;
-  const int key_blocks = weights_out ? (c.max_pages * kB + kWeightKeys - 1) / kWeightKeys : 0;
-  const long long blocks = static_cast<long long>(c.batch) * c.hkv * (a.rows + key_blocks);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, a, kr, weights_in, weights_out, key_blocks);
+  const unsigned rows = static_cast<unsigned>(std::min(kr, a.rows));
+  e = launch_dependent(join_kernel, dim3(static_cast<unsigned>(a.ctas), rows), kJoinThreads, st, a, kr);
+  if (e != cudaSuccess || weights_out == nullptr) return e;
+  const unsigned blocks = static_cast<unsigned>((c.max_pages * kB + kWeightKeys - 1) / kWeightKeys);
+  return launch_dependent(weights_kernel, dim3(blocks, static_cast<unsigned>(c.hkv), static_cast<unsigned>(c.batch)),
+                          kWeightThreads, st, a, weights_in, weights_out);
 }
 
 }  // namespace crisp

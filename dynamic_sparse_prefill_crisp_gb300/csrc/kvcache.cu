@@ -3,9 +3,9 @@
 //
 // A page of a head is 128 tokens x 128 e4m3 codes with one power-of-two scale
 // (csrc/common.cuh, scale_exponent). Both kernels that write pages take one
-// page of one head, K or V, per CTA: 8 threads hold a row (16 codes each), 32
-// rows at a time, the whole page in registers between its maximum and its
-// codes, so every value is read once. They are bound by HBM.
+// page of one head per CTA: 8 threads hold a row (16 codes each), 32 rows at a
+// time, the whole page in registers between its maximum and its codes, so
+// every value is read once. They are bound by HBM.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -67,7 +67,7 @@ struct Pool {
 // New tokens of one page of one head, K or V: the page's new scale from the
 // new values (and its old scale, where it held tokens before them), the new
 // tokens' codes, and the old tokens' codes again if the scale grew.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     append_kernel(Pool pk, Pool pv, int64_t page_stride, int64_t head_stride, int hkv, int num_pages, int max_pages,
                   const int32_t* table, const int32_t* lens, const int32_t* new_lens, int n_new, crisp_tokens kt,
                   crisp_tokens vt, DevStatus* status) {
@@ -84,21 +84,12 @@ __global__ void __launch_bounds__(kThreads)
   const int page = start / kB + static_cast<int>(blockIdx.x);
   const int lo = page * kB;  // position of the page's row 0
   if (cnt == 0 || lo >= len) return;
-  const int id = table[static_cast<int64_t>(b) * max_pages + page];
-  if (id < 0 || id >= num_pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x702);
-    return;
-  }
-  const Pool pool = is_v ? pv : pk;
+  const int32_t* entry = table + static_cast<int64_t>(b) * max_pages + page;
   const crisp_tokens t = is_v ? vt : kt;
   const auto* src = static_cast<const __nv_bfloat16*>(t.data) + b * t.batch_stride + g * t.head_stride;
-  uint8_t* codes = pool.codes + id * page_stride + g * head_stride;
-  float* scale = pool.scale + static_cast<int64_t>(id) * hkv + g;
   const int col = (threadIdx.x & (kRowThreads - 1)) * 16, row0 = threadIdx.x / kRowThreads;
   const int first = max(start - lo, 0), end = min(len - lo, kB);  // rows [first, end) are new, [0, first) old
-  const bool held = first > 0;
-  const float s_old = held ? *scale : 0.f;
-
+  // the new values are asked for before the page is looked up
   uint4 x[kPasses][2];
   float amax = 0.f;
 #pragma unroll
@@ -111,6 +102,16 @@ __global__ void __launch_bounds__(kThreads)
       x[p][1] = __ldcs(s + 1);
     }
   }
+  const int id = *entry;
+  if (id < 0 || id >= num_pages) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x702);
+    return;
+  }
+  const Pool pool = is_v ? pv : pk;
+  uint8_t* codes = pool.codes + id * page_stride + g * head_stride;
+  float* scale = pool.scale + static_cast<int64_t>(id) * hkv + g;
+  const bool held = first > 0;
+  const float s_old = held ? *scale : 0.f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p)
 #pragma unroll
@@ -151,13 +152,14 @@ __global__ void __launch_bounds__(kThreads)
 // digit by digit from the top (11 + 11 + 10 bits): a histogram of the keys that
 // match the digits found so far, then the digit in which the keep-th falls. A
 // last pass writes the kept positions in order. The keys are read four times,
-// from L2 after the first; a long sequence takes a cluster of 8 CTAs with a
+// from L2 after the first; a long sequence takes a cluster of 16 CTAs with a
 // contiguous part each, which read each other's histograms through
-// distributed shared memory (512k tokens: one CTA would take 2 MB a pass).
+// distributed shared memory (512k tokens: one CTA would read 2 MB a pass).
 constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kClusterLen = 16384;  // capacities from which a cluster is used
-constexpr int kCluster = 8;
+constexpr int kCluster = 16;
+constexpr int kAhead = 4;           // loads of four keys a thread has in flight
 
 __device__ __forceinline__ uint32_t weight_key(float w, int pos, int sink, int tail) {
   if (pos < sink || pos >= tail) return 0xffffffffu;
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(kSelThreads, 1)
                   int recent, float* new_weights, int64_t new_cap, int32_t* list, int64_t list_stride,
                   DevStatus* status) {
   __shared__ int hist[2][kBins];
+  __shared__ int bin_total[2][kC > 1 ? kBins / kC : 1];
   __shared__ int warp_tot[kSelThreads / 32];
   __shared__ int digit, above_digit;
   __shared__ int own[2];  // this CTA's keys above the threshold, and equal to it
@@ -242,26 +245,42 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     h[tid] = h[tid + kSelThreads] = 0;
     __syncthreads();
     const uint32_t fixed = pass == 0 ? 0u : ~0u << kShift[pass - 1];
-    for (int i = lo + tid * 4; i < hi; i += kSelThreads * 4) {
-      float v[4];
-      load4(i, v);
+    for (int i0 = lo + tid * 4; i0 < hi; i0 += kSelThreads * 4 * kAhead) {
+      float v[kAhead][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t key = weight_key(v[e], i + e, sink, tail);
-        if (i + e < hi && (key & fixed) == found) atomicAdd(&h[(key >> kShift[pass]) & kMask[pass]], 1);
-      }
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u * kSelThreads * 4 < hi) load4(i0 + u * kSelThreads * 4, v[u]);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = i0 + u * kSelThreads * 4 + e;
+          if (i >= hi) continue;
+          const uint32_t key = weight_key(v[u][e], i, sink, tail);
+          if ((key & fixed) == found) atomicAdd(&h[(key >> kShift[pass]) & kMask[pass]], 1);
+        }
     }
     if (kC > 1) cg::this_cluster().sync();
     else __syncthreads();
     // thread t takes bins (largest first) 2t and 2t + 1 of the whole sequence
     const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
-    int c0 = 0, c1 = 0;
-    if (kC > 1) {
-      for (int r = 0; r < kC; ++r) {
-        const int* hr = cg::this_cluster().map_shared_rank(h, r);
-        c0 += hr[b0];
-        c1 += hr[b1];
-      }
+    int c0, c1;
+    if constexpr (kC > 1) {
+      // CTA r adds up bins r * kOwn .. of all CTAs; everyone then reads the sums
+      // from their owners (reading every CTA's whole histogram instead made
+      // all CTAs queue at one after the other: 40 us a pass against 3)
+      constexpr int kOwn = kBins / kC, kSplit = kSelThreads / kOwn;
+      int* total = bin_total[pass & 1];
+      if (tid < kOwn) total[tid] = 0;
+      __syncthreads();
+      int sum = 0;
+#pragma unroll
+      for (int u = 0; u < kC / kSplit; ++u)
+        sum += cg::this_cluster().map_shared_rank(h, tid / kOwn * (kC / kSplit) + u)[part * kOwn + tid % kOwn];
+      if (sum) atomicAdd(&total[tid % kOwn], sum);
+      cg::this_cluster().sync();
+      c0 = cg::this_cluster().map_shared_rank(total, b0 / kOwn)[b0 % kOwn];
+      c1 = cg::this_cluster().map_shared_rank(total, b1 / kOwn)[b1 % kOwn];
     } else {
       c0 = h[b0];
       c1 = h[b1];
@@ -301,10 +320,12 @@ __global__ void __launch_bounds__(kSelThreads, 1)
     }
     cg::this_cluster().sync();  // nobody's shared memory goes away while it is read
   }
+  float next[4] = {0.f, 0.f, 0.f, 0.f};
+  if (lo + tid * 4 < hi) load4(lo + tid * 4, next);
   for (int i0 = lo; i0 < hi; i0 += kSelThreads * 4) {
     const int i = i0 + tid * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (i < hi) load4(i, v);
+    const float v[4] = {next[0], next[1], next[2], next[3]};
+    if (i + kSelThreads * 4 < hi) load4(i + kSelThreads * 4, next);
     uint32_t key[4];
     int packed = 0;  // counts of this thread: above in the high half, equal in the low
 #pragma unroll
@@ -332,25 +353,26 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   }
 }
 
-// One new page of one head, K or V: its kept tokens' codes gathered from the
-// old pages, the scale their values need, and the codes at it.
+// One new page of one head, K and V: their kept tokens' codes gathered from the
+// old pages (a row is 128 contiguous bytes), the scale their values need, and
+// the codes at it. K and V together, so that the two lookups before a row
+// (its position, its page) are made once and eight row pieces a thread are in
+// flight.
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(Pool sk, Pool sv, int64_t s_page, int64_t s_head, const int32_t* s_table, int s_num, int s_max,
                 Pool dk, Pool dv, int64_t d_page, int64_t d_head, const int32_t* d_table, int d_num, int d_max, int hkv,
                 const int32_t* lens, int keep, const int32_t* list, int64_t list_stride, DevStatus* status) {
-  __shared__ float red[kThreads / 32];
-  const int g = blockIdx.y >> 1, b = blockIdx.z, page = blockIdx.x;
-  const bool is_v = blockIdx.y & 1;
+  __shared__ float red[2][kThreads / 32];
+  const int g = blockIdx.y, b = blockIdx.z, page = blockIdx.x;
   const int n = min(min(max(lens[b], 0), s_max * kB), keep);
   const int rows = min(n - page * kB, kB);
   if (rows <= 0) return;
   const int id = d_table[static_cast<int64_t>(b) * d_max + page];
   if (id < 0 || id >= d_num) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
+    if (g == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
     return;
   }
   grid_dep_wait();
-  const Pool from = is_v ? sv : sk, to = is_v ? dv : dk;
   const int col = (threadIdx.x & (kRowThreads - 1)) * 16, row0 = threadIdx.x / kRowThreads;
   const int32_t* pos = list + (static_cast<int64_t>(b) * hkv + g) * list_stride + page * kB;
   const int32_t* tab = s_table + static_cast<int64_t>(b) * s_max;
@@ -362,47 +384,54 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) src[p] = old[p] >= 0 ? tab[old[p] / kB] : -1;
-  uint4 c[kPasses];
-  float s[kPasses];
+  uint4 c[2][kPasses];
+  float s[2][kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    c[p] = make_uint4(0u, 0u, 0u, 0u);
-    s[p] = 0.f;
+    c[0][p] = c[1][p] = make_uint4(0u, 0u, 0u, 0u);
+    s[0][p] = s[1][p] = 0.f;
     if (old[p] < 0) continue;
     if (src[p] < 0 || src[p] >= s_num) {
       report_error(status, CRISP_ERR_BOUNDS, 0x713);
       continue;
     }
-    c[p] = __ldcs(reinterpret_cast<const uint4*>(from.codes + src[p] * s_page + g * s_head + (old[p] % kB) * kD + col));
-    s[p] = from.scale[static_cast<int64_t>(src[p]) * hkv + g];
+    const int64_t at = src[p] * s_page + g * s_head + (old[p] % kB) * kD + col;
+    const int64_t sat = static_cast<int64_t>(src[p]) * hkv + g;
+    c[0][p] = __ldcs(reinterpret_cast<const uint4*>(sk.codes + at));
+    c[1][p] = __ldcs(reinterpret_cast<const uint4*>(sv.codes + at));
+    s[0][p] = sk.scale[sat];
+    s[1][p] = sv.scale[sat];
   }
-  float amax = 0.f;
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    // the largest magnitude: codes without their sign order as the values do, 0x7f is NaN
-    uint32_t top = 0;
+  for (int x = 0; x < 2; ++x) {
+    float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t m = (&c[p].x)[e] & 0x7f7f7f7fu;
-      top = __vmaxu4(top, m & ~__vcmpeq4(m, 0x7f7f7f7fu));
+    for (int p = 0; p < kPasses; ++p) {
+      // the largest magnitude: codes without their sign order as the values do, 0x7f is NaN
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t m = (&c[x][p].x)[e] & 0x7f7f7f7fu;
+        top = __vmaxu4(top, m & ~__vcmpeq4(m, 0x7f7f7f7fu));
+      }
+      top = __vmaxu4(top, top >> 16);
+      top = __vmaxu4(top, top >> 8) & 0xffu;
+      float v, none;
+      unpack_e4m3x2(static_cast<uint16_t>(top), v, none);
+      amax = fmaxf(amax, v * s[x][p]);
     }
-    top = __vmaxu4(top, top >> 16);
-    top = __vmaxu4(top, top >> 8) & 0xffu;
-    float v, none;
-    unpack_e4m3x2(static_cast<uint16_t>(top), v, none);
-    amax = fmaxf(amax, v * s[p]);
-  }
-  amax = block_max(amax, red);
-  const float sn = exp2_int(scale_exponent(amax)), inv = 1.f / sn;
-  uint8_t* codes = to.codes + id * d_page + g * d_head;
+    amax = block_max(amax, red[x]);
+    const float sn = exp2_int(scale_exponent(amax)), inv = 1.f / sn;
+    uint8_t* codes = (x ? dv : dk).codes + id * d_page + g * d_head;
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int row = row0 + p * kRowsAtOnce;
-    if (row >= rows) continue;
-    const float ratio = s[p] * inv;
-    *reinterpret_cast<uint4*>(codes + row * kD + col) = ratio == 1.f ? c[p] : rescale16(c[p], ratio);
+    for (int p = 0; p < kPasses; ++p) {
+      const int row = row0 + p * kRowsAtOnce;
+      if (row >= rows) continue;
+      const float ratio = s[x][p] * inv;
+      *reinterpret_cast<uint4*>(codes + row * kD + col) = ratio == 1.f ? c[x][p] : rescale16(c[x][p], ratio);
+    }
+    if (threadIdx.x == 0) (x ? dv : dk).scale[static_cast<int64_t>(id) * hkv + g] = sn;
   }
-  if (threadIdx.x == 0) to.scale[static_cast<int64_t>(id) * hkv + g] = sn;
 }
 
 Pool k_pool(const crisp_kv_cache& c) { return {static_cast<uint8_t*>(c.k), c.k_scale}; }
@@ -432,6 +461,8 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   cfg.gridDim = dim3(static_cast<unsigned>(src.batch * src.hkv * (wide ? kCluster : 1)));
   cudaError_t e;
   if (wide) {
+    e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = kCluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -450,7 +481,7 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>((min(keep, cap) + kB - 1) / kB), 2 * src.hkv, src.batch);
+  cfg.gridDim = dim3(static_cast<unsigned>((min(keep, cap) + kB - 1) / kB), src.hkv, src.batch);
   return cudaLaunchKernelEx(&cfg, pack_kernel, k_pool(src), v_pool(src), src.page_stride, src.head_stride, src.table,
                             src.num_pages, src.max_pages, k_pool(dst), v_pool(dst), dst.page_stride, dst.head_stride,
                             dst.table, dst.num_pages, dst.max_pages, src.hkv, static_cast<const int32_t*>(src.lens),

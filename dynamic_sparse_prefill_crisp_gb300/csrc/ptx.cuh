@@ -249,13 +249,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// TMEM -> registers, 8 columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// TMEM -> registers, 8 columns of this thread's lane at each of two places, waited for.
+__device__ __forceinline__ void tmem_ld8x2(uint32_t ta, uint32_t tb, uint32_t (&x)[8], uint32_t (&y)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
+      : "=&r"(x[0]), "=&r"(x[1]), "=&r"(x[2]), "=&r"(x[3]), "=&r"(x[4]), "=&r"(x[5]), "=&r"(x[6]), "=&r"(x[7]),
+        "=&r"(y[0]), "=&r"(y[1]), "=&r"(y[2]), "=&r"(y[3]), "=&r"(y[4]), "=&r"(y[5]), "=&r"(y[6]), "=&r"(y[7])
+      : "r"(ta), "r"(tb)
       : "memory");
 }
 
@@ -335,6 +337,26 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   uint16_t d;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
+}
+// Two values of magnitude <= 448 as e4m3 pieces, x = hi + lo / 16, by way of
+// fp16 (x rounded to 11 bits first; the difference of fp16 values is exact).
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint16_t& hi, uint16_t& lo) {
+  asm("{\n\t.reg .b32 x, h, d, s;\n\t"
+      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, x;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %0;\n\t"
+      "sub.f16x2 d, x, h;\n\t"
+      "mov.b32 s, 0x4C004C00;\n\t"  // 16, 16
+      "mul.f16x2 d, d, s;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %1, d;\n\t}"
+      : "=&h"(hi), "=h"(lo)
+      : "f"(x0), "f"(x1));
+}
+// The warp's largest value, in every lane (a NaN among numbers is passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 // The two e4m3 values of a pair (exact): lo from bits 0..7.
 __device__ __forceinline__ void unpack_e4m3x2(uint16_t v, float& lo, float& hi) {
