@@ -72,11 +72,13 @@ crisp_shape normalised(const crisp_shape& s) {
   return t;
 }
 
-crisp_status check_device() {
+crisp_status check_device(int* sms = nullptr) {
   int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return CRISP_ERR_CUDA;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return CRISP_ERR_CUDA;
+  if (sms != nullptr && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return CRISP_ERR_CUDA;
   return (major == 10 && minor == 3) ? CRISP_OK : CRISP_ERR_DEVICE;
 }
@@ -890,7 +892,8 @@ crisp_status check_cache(const crisp_kv_cache* c) {
   if (c->head_dim != kD || c->block != kB) return CRISP_ERR_SHAPE;
   if (c->batch < 0 || c->batch > kMaxBatch || c->hkv <= 0 || c->hkv > 4096) return CRISP_ERR_SHAPE;
   if (c->num_pages <= 0 || c->max_pages <= 0 || c->max_pages > kMaxPages) return CRISP_ERR_SHAPE;
-  if (static_cast<int64_t>(c->batch) * c->max_pages * c->hkv > INT32_MAX) return CRISP_ERR_SHAPE;
+  if (c->num_pages > INT32_MAX / kB || static_cast<int64_t>(c->batch) * c->max_pages * c->hkv > INT32_MAX)
+    return CRISP_ERR_SHAPE;
   for (int64_t st : {c->page_stride, c->head_stride})
     if (st <= 0 || st % 16 != 0 || st > (int64_t(1) << 38)) return CRISP_ERR_ALIGN;
   if (c->page_stride < kB * kD || (c->hkv > 1 && c->head_stride < kB * kD)) return CRISP_ERR_SHAPE;
@@ -1020,11 +1023,8 @@ crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32_t hq, int
     if (!aligned16(weights_in) || !aligned16(weights_out)) return CRISP_ERR_ALIGN;
     if ((st = check_cache_ws(ws, ws_bytes, decode_layout(*cache, hq, q_len, weights_out != nullptr).total)) != CRISP_OK)
       return st;
-    if ((st = check_device()) != CRISP_OK) return st;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return CRISP_ERR_CUDA;
+    int sms = 0;
+    if ((st = check_device(&sms)) != CRISP_OK) return st;
     KvMaps maps;
     if ((st = make_page_map(&maps.k, cache->k, *cache)) != CRISP_OK) return st;
     if ((st = make_page_map(&maps.v, cache->v, *cache)) != CRISP_OK) return st;
@@ -1050,13 +1050,12 @@ crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst
     if (src->table == dst->table || src->lens == dst->lens) return CRISP_ERR_INVALID_ARG;  // written while read
     if (!aligned16(weights) || !aligned16(new_weights) || !aligned(kept, 4)) return CRISP_ERR_ALIGN;
     if ((st = check_cache_ws(ws, ws_bytes, evict_bytes(*src, keep))) != CRISP_OK) return st;
-    if ((st = check_device()) != CRISP_OK) return st;
-    // the kept positions go to the caller's array or, without one, to the workspace
-    int32_t* list = kept != nullptr ? kept : reinterpret_cast<int32_t*>(static_cast<char*>(ws) + evict_list_offset());
-    const int64_t stride = kept != nullptr ? static_cast<int64_t>(dst->max_pages) * kB
-                                           : static_cast<int64_t>(align_up(static_cast<size_t>(keep) * 4) / 4);
-    return from_cuda(launch_kv_evict(*src, *dst, weights, keep, sink, recent, new_weights, list, stride,
-                                     status_of(ws), stream));
+    int sms = 0;
+    if ((st = check_device(&sms)) != CRISP_OK) return st;
+    auto* list = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + evict_list_offset());
+    const int64_t stride = static_cast<int64_t>(align_up(static_cast<size_t>(keep) * 4) / 4);
+    return from_cuda(launch_kv_evict(*src, *dst, weights, keep, sink, recent, new_weights, kept, list, stride,
+                                     status_of(ws), sms, stream));
   });
 }
 

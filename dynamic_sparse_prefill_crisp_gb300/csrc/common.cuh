@@ -171,9 +171,9 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
                           char* ws, int sms, cudaStream_t st);
 cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
                              const int32_t* new_lens, DevStatus* status, cudaStream_t st);
-// list: int32 [batch][hkv][list_stride], the kept positions (the caller's or in the workspace)
+// list: int32 [batch][hkv][list_stride], where the kept tokens' codes are (page * 128 + row)
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
-                            int sink, int recent, float* new_weights, int32_t* list, int64_t list_stride,
-                            DevStatus* status, cudaStream_t st);
+                            int sink, int recent, float* new_weights, int32_t* kept, int32_t* list,
+                            int64_t list_stride, DevStatus* status, int sms, cudaStream_t st);
 
 }  // namespace crisp

@@ -47,16 +47,62 @@ __device__ __forceinline__ float scaled(float x, float inv) {
   return fabsf(x) <= 3.402823466e38f ? x * inv : __int_as_float(0x7fffffff);
 }
 
-// Four codes rounded again at `ratio` times their values.
-__device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
+// Two codes rounded again at `ratio` times their values, for a power of two
+// 2^-24 <= ratio <= 2^15: e4m3 values and their products with it are fp16
+// values (down to 2^-24, far below what a code can hold), so there is one rounding.
+__device__ __forceinline__ uint32_t rescale2(uint32_t c, uint32_t ratio2) {
+  uint16_t d;
+  asm("{\n\t.reg .b32 h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %1;\n\t"
+      "mul.f16x2 h, h, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, h;\n\t}"
+      : "=h"(d)
+      : "h"(static_cast<uint16_t>(c)), "r"(ratio2));
+  return d;
+}
+__device__ __forceinline__ uint32_t rescale4_any(uint32_t c, float ratio) {
   float a0, a1, a2, a3;
   unpack_e4m3x2(static_cast<uint16_t>(c), a0, a1);
   unpack_e4m3x2(static_cast<uint16_t>(c >> 16), a2, a3);
   return static_cast<uint32_t>(pack_e4m3x2(a0 * ratio, a1 * ratio)) |
          static_cast<uint32_t>(pack_e4m3x2(a2 * ratio, a3 * ratio)) << 16;
 }
+// 16 codes rounded again at `ratio` times their values.
 __device__ __forceinline__ uint4 rescale16(uint4 c, float ratio) {
-  return make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
+  if (ratio == 1.f) return c;
+  if ((__float_as_uint(ratio) & 0x7FFFFFu) == 0u && ratio >= 0x1p-24f && ratio <= 0x1p15f) {
+    uint32_t r2;
+    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r2) : "f"(ratio));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = (&c.x)[e];
+      (&c.x)[e] = rescale2(w, r2) | rescale2(w >> 16, r2) << 16;
+    }
+    return c;
+  }
+  // tiny codes scaled up a long way, or a scale that is no power of two
+  return make_uint4(rescale4_any(c.x, ratio), rescale4_any(c.y, ratio), rescale4_any(c.z, ratio),
+                    rescale4_any(c.w, ratio));
+}
+// The largest magnitude of 16 codes (NaN is passed over).
+__device__ __forceinline__ float max16(const uint4& c) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = (&c.x)[e];
+    asm("{\n\t.reg .b32 a, b;\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 a, l;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\t"
+        "and.b32 a, a, 0x7fff7fff;\n\tand.b32 b, b, 0x7fff7fff;\n\t"
+        "max.f16x2 a, a, b;\n\tmax.f16x2 %0, %0, a;\n\t}"
+        : "+r"(m)
+        : "r"(w));
+  }
+  float x, y;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "r"(m));
+  return fmaxf(x, y);
 }
 
 struct Pool {
@@ -155,17 +201,31 @@ __global__ void __launch_bounds__(kThreads, 4)
 // from L2 after the first; a long sequence takes a cluster of 16 CTAs with a
 // contiguous part each, which read each other's histograms through
 // distributed shared memory (512k tokens: one CTA would read 2 MB a pass).
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kClusterLen = 16384;  // capacities from which a cluster is used
 constexpr int kCluster = 16;
 constexpr int kAhead = 4;           // loads of four keys a thread has in flight
 
-__device__ __forceinline__ uint32_t weight_key(float w, int pos, int sink, int tail) {
-  if (pos < sink || pos >= tail) return 0xffffffffu;
-  if (w != w) return 0xfffffffeu;
-  const uint32_t u = __float_as_uint(w + 0.f);  // -0 as 0
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  // + 0 makes one zero of both and one NaN of all (0x7fffffff)
+  const int u = __float_as_int(w + 0.f);
+  return min(static_cast<uint32_t>(u ^ (u >> 31 | INT32_MIN)), 0xfffffffeu);
+}
+// Keys of the four weights from position i on; those at or past n do not count
+// (0, which is no weight's key).
+__device__ __forceinline__ void weight_keys(const float4& w, int i, int sink, int tail, int n, uint32_t (&key)[4]) {
+  key[0] = weight_key(w.x);
+  key[1] = weight_key(w.y);
+  key[2] = weight_key(w.z);
+  key[3] = weight_key(w.w);
+  if (i < sink || i + 4 > tail) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e < sink || i + e >= tail) key[e] = 0xffffffffu;
+      if (i + e >= n) key[e] = 0u;
+    }
+  }
 }
 
 // Inclusive scan over the block of one value a thread; returns it and the total.
@@ -178,7 +238,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int& total) {
   }
   if (lane == 31) warp_tot[warp] = v;
   __syncthreads();
-  int w = warp_tot[lane];  // kSelThreads / 32 = 32 warps
+  int w = lane < kSelThreads / 32 ? warp_tot[lane] : 0;
   int before = lane < warp ? w : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -191,14 +251,15 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int& total) {
 }
 
 template <int kC>
-__global__ void __launch_bounds__(kSelThreads, 1)
+__global__ void __launch_bounds__(kSelThreads, 2)
     select_kernel(const float* weights, const int32_t* lens, int32_t* new_lens, int hkv, int cap, int keep, int sink,
-                  int recent, float* new_weights, int64_t new_cap, int32_t* list, int64_t list_stride,
-                  DevStatus* status) {
-  __shared__ int hist[2][kBins];
+                  int recent, const int32_t* table, int num_pages, float* new_weights, int64_t new_cap, int32_t* kept,
+                  int64_t kept_stride, int32_t* list, int64_t list_stride, DevStatus* status) {
+  __shared__ alignas(8) int hist[2][kBins];
   __shared__ int bin_total[2][kC > 1 ? kBins / kC : 1];
   __shared__ int warp_tot[kSelThreads / 32];
   __shared__ int digit, above_digit;
+  __shared__ alignas(8) int tot[2][kAhead * kSelThreads / 32];
   __shared__ int own[2];  // this CTA's keys above the threshold, and equal to it
   grid_dep_launch();
   const int tid = threadIdx.x;
@@ -213,58 +274,68 @@ __global__ void __launch_bounds__(kSelThreads, 1)
   const float* w = weights + static_cast<int64_t>(bg) * cap;
   int32_t* dst = list + bg * list_stride;
   float* dst_w = new_weights != nullptr ? new_weights + bg * new_cap : nullptr;
+  int32_t* dst_pos = kept != nullptr ? kept + bg * kept_stride : nullptr;
+  const int32_t* pages = table + static_cast<int64_t>(b) * (cap / kB);
+  // Position i is kept in place `at`: where its codes are (-1: on no page), and what it carries along.
+  auto emit = [&](int at, int i, int id, float weight) {
+    dst[at] = id >= 0 && id < num_pages ? id * kB + i % kB : -1;
+    if (dst_pos) dst_pos[at] = i;
+    if (dst_w) dst_w[at] = weight;
+  };
   // this CTA's part of the positions, whole groups of four
   const int quads = (n + 3) / 4;
   const int lo = static_cast<int>(static_cast<int64_t>(quads) * part / kC) * 4;
   const int hi = min(static_cast<int>(static_cast<int64_t>(quads) * (part + 1) / kC) * 4, n);
   if (n <= keep) {  // uniform over the cluster
-    for (int i = lo + tid; i < hi; i += kSelThreads) {
-      dst[i] = i;
-      if (dst_w) dst_w[i] = w[i];
-    }
+    for (int i = lo + tid; i < hi; i += kSelThreads) emit(i, i, pages[i / kB], w[i]);
     return;
   }
   const int tail = n - recent;
-  auto load4 = [&](int i, float (&v)[4]) {
-    // rows are 512-byte aligned and cap is a multiple of 128
-    const float4 q = *reinterpret_cast<const float4*>(w + i);
-    v[0] = q.x;
-    v[1] = q.y;
-    v[2] = q.z;
-    v[3] = q.w;
+  // rows are 512-byte aligned and cap is a multiple of 128: whole groups of four are there
+  auto load4 = [&](int i) { return *reinterpret_cast<const float4*>(w + i); };
+
+  constexpr int kTurn = kSelThreads * 4;  // positions the block takes with one load a thread
+  float4 v[kAhead];                       // a part of one turn is read once
+  auto load_first = [&]() {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (lo + u * kTurn + tid * 4 < hi) v[u] = load4(lo + u * kTurn + tid * 4);
   };
 
   uint32_t found = 0;   // the digits found, in place
   int want = keep;      // the threshold is the want-th largest of the keys that match them
-  int above_own = 0;    // this CTA's keys above
+  int above_own = 0;    // this CTA's keys above (this thread's part)
   constexpr int kShift[3] = {21, 10, 0};
   constexpr uint32_t kMask[3] = {2047u, 2047u, 1023u};
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     int* h = hist[pass & 1];
-    h[tid] = h[tid + kSelThreads] = 0;
+    for (int x = tid; x < kBins; x += kSelThreads) h[x] = 0;
     __syncthreads();
     const uint32_t fixed = pass == 0 ? 0u : ~0u << kShift[pass - 1];
-    for (int i0 = lo + tid * 4; i0 < hi; i0 += kSelThreads * 4 * kAhead) {
-      float v[kAhead][4];
+    if (pass == 0 || hi - lo > kTurn * kAhead) load_first();
+    for (int i0 = lo + tid * 4; i0 < hi; i0 += kTurn * kAhead) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (i0 + u * kSelThreads * 4 < hi) load4(i0 + u * kSelThreads * 4, v[u]);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kTurn;
+        if (i >= hi) break;
+        uint32_t key[4];
+        weight_keys(v[u], i, sink, tail, n, key);
+        if (i + kTurn * kAhead < hi) v[u] = load4(i + kTurn * kAhead);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = i0 + u * kSelThreads * 4 + e;
-          if (i >= hi) continue;
-          const uint32_t key = weight_key(v[u][e], i, sink, tail);
-          if ((key & fixed) == found) atomicAdd(&h[(key >> kShift[pass]) & kMask[pass]], 1);
+          // a key of 0 counts only in the first pass, in bin 0, where no weight's key falls (-inf is in bin 3)
+          if (pass == 0 || ((key[e] ^ found) & fixed) == 0u)
+            atomicAdd(&h[pass == 0 ? key[e] >> kShift[0] : (key[e] >> kShift[pass]) & kMask[pass]], 1);
         }
+      }
     }
     if (kC > 1) cg::this_cluster().sync();
     else __syncthreads();
-    // thread t takes bins (largest first) 2t and 2t + 1 of the whole sequence
-    const int b0 = kBins - 1 - 2 * tid, b1 = b0 - 1;
-    int c0, c1;
+    // thread t takes kPer bins of the whole sequence, the largest first
+    constexpr int kPer = kBins / kSelThreads;
+    const int top = kBins - 1 - kPer * tid;
+    int c[kPer], sum = 0;
     if constexpr (kC > 1) {
       // CTA r adds up bins r * kOwn .. of all CTAs; everyone then reads the sums
       // from their owners (reading every CTA's whole histogram instead made
@@ -273,165 +344,277 @@ __global__ void __launch_bounds__(kSelThreads, 1)
       int* total = bin_total[pass & 1];
       if (tid < kOwn) total[tid] = 0;
       __syncthreads();
-      int sum = 0;
+      int part_sum = 0;
 #pragma unroll
       for (int u = 0; u < kC / kSplit; ++u)
-        sum += cg::this_cluster().map_shared_rank(h, tid / kOwn * (kC / kSplit) + u)[part * kOwn + tid % kOwn];
-      if (sum) atomicAdd(&total[tid % kOwn], sum);
+        part_sum += cg::this_cluster().map_shared_rank(h, tid / kOwn * (kC / kSplit) + u)[part * kOwn + tid % kOwn];
+      if (part_sum) atomicAdd(&total[tid % kOwn], part_sum);
       cg::this_cluster().sync();
-      c0 = cg::this_cluster().map_shared_rank(total, b0 / kOwn)[b0 % kOwn];
-      c1 = cg::this_cluster().map_shared_rank(total, b1 / kOwn)[b1 % kOwn];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        c[u] = cg::this_cluster().map_shared_rank(total, (top - u) / kOwn)[(top - u) % kOwn];
     } else {
-      c0 = h[b0];
-      c1 = h[b1];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) c[u] = h[top - u];
     }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) sum += c[u];
     int all;
-    const int incl = block_scan(c0 + c1, warp_tot, all);
-    const int before = incl - c0 - c1;
+    const int incl = block_scan(sum, warp_tot, all);
+    int before = incl - sum;
     if (before < want && want <= incl) {
-      const bool second = want > before + c0;
-      digit = second ? b1 : b0;
-      above_digit = before + (second ? c0 : 0);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        if (before < want && want <= before + c[u]) {
+          digit = top - u;
+          above_digit = before;
+        }
+        before += c[u];
+      }
     }
     __syncthreads();
     const int d = digit;
     want -= above_digit;
     found |= static_cast<uint32_t>(d) << kShift[pass];
     // this CTA's own keys above the digit
-    int mine = (b0 > d ? h[b0] : 0) + (b1 > d ? h[b1] : 0);
-    int own_above;
-    block_scan(mine, warp_tot, own_above);
-    above_own += own_above;
-    if (pass == 2 && tid == 0) {
-      own[0] = above_own;
-      own[1] = h[d];
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) mine += top - u > d ? h[top - u] : 0;
+    above_own += mine;
+    if (kC > 1 && pass == 2) {
+      int own_above;
+      block_scan(above_own, warp_tot, own_above);
+      if (tid == 0) {
+        own[0] = own_above;
+        own[1] = h[d];
+      }
     }
-    __syncthreads();
   }
   // Kept before this CTA's part: all keys above the threshold `found`, and the
   // first `want` equal to it.
   int gt = 0, eq = 0;
   if (kC > 1) {
     cg::this_cluster().sync();
-    for (int r = 0; r < part; ++r) {
-      const int* o = cg::this_cluster().map_shared_rank(own, r);
-      gt += o[0];
-      eq += o[1];
+    if ((tid & 31) < part) {
+      const int* o = cg::this_cluster().map_shared_rank(own, tid & 31);
+      gt = o[0];
+      eq = o[1];
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
     cg::this_cluster().sync();  // nobody's shared memory goes away while it is read
   }
-  float next[4] = {0.f, 0.f, 0.f, 0.f};
-  if (lo + tid * 4 < hi) load4(lo + tid * 4, next);
-  for (int i0 = lo; i0 < hi; i0 += kSelThreads * 4) {
-    const int i = i0 + tid * 4;
-    const float v[4] = {next[0], next[1], next[2], next[3]};
-    if (i + kSelThreads * 4 < hi) load4(i + kSelThreads * 4, next);
-    uint32_t key[4];
-    int packed = 0;  // counts of this thread: above in the high half, equal in the low
+  // A turn's kept positions are first put in order in shared memory (where the
+  // histograms were), then written out by neighbouring threads.
+  constexpr int kWarps = kSelThreads / 32;
+  const int warp = tid >> 5, lane = tid & 31;
+  static_assert(sizeof(hist) >= 2 * kTurn * kAhead, "a turn's offsets fit the histograms");
+  uint16_t* order = reinterpret_cast<uint16_t*>(hist);
+  if (hi - lo > kTurn * kAhead) load_first();
+  for (int i0 = lo, turn = 0; i0 < hi; i0 += kTurn * kAhead, ++turn) {
+    // counts before this thread: keys above in the high half, equal in the low
+    // (at most 8192 of either in a turn)
+    int before[kAhead];
+    uint32_t above = 0, tie = 0;  // one bit a key
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      key[e] = i + e < hi ? weight_key(v[e], i + e, sink, tail) : 0u;
-      if (i + e < hi) packed += key[e] > found ? 1 << 16 : key[e] == found ? 1 : 0;
-    }
-    int all;
-    const int incl = block_scan(packed, warp_tot, all) - packed;  // at most 4096 of either before
-    int g1 = gt + (incl >> 16), e1 = eq + (incl & 0xffff);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * kTurn + tid * 4;
+      int mine = 0;
+      if (i < hi) {
+        uint32_t key[4];
+        weight_keys(v[u], i, sink, tail, n, key);
+        if (i + kTurn * kAhead < hi) v[u] = load4(i + kTurn * kAhead);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (i + e >= hi) break;
-      const bool above = key[e] > found, tie = key[e] == found;
-      if (above || (tie && e1 < want)) {
-        const int at = g1 + min(e1, want);
-        dst[at] = i + e;
-        if (dst_w) dst_w[at] = v[e];
+        for (int e = 0; e < 4; ++e) {
+          above |= (key[e] > found ? 1u : 0u) << (4 * u + e);
+          tie |= (key[e] == found ? 1u : 0u) << (4 * u + e);
+        }
+        mine = __popc(above >> (4 * u) & 15u) << 16 | __popc(tie >> (4 * u) & 15u);
       }
-      g1 += above;
-      e1 += tie;
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      before[u] = incl - mine;
+      if (lane == 31) tot[turn & 1][u * kWarps + warp] = incl;
+    }
+    __syncthreads();
+    // the kAhead * kWarps totals in order, two a lane
+    static_assert(kAhead * kWarps == 64, "two totals a lane");
+    const int2 pair = *reinterpret_cast<const int2*>(&tot[turn & 1][2 * lane]);
+    int incl = pair.x + pair.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int all = __shfl_sync(0xffffffffu, incl, 31), excl = incl - pair.x - pair.y;
+    const int begin = gt + min(eq, want);  // the turn's first place
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int place = u * kWarps + warp;  // of this warp's total
+      const int at2 = __shfl_sync(0xffffffffu, excl, place / 2), first = __shfl_sync(0xffffffffu, pair.x, place / 2);
+      const int base = before[u] + at2 + (place & 1 ? first : 0);
+      int g1 = gt + (base >> 16) - begin, e1 = eq + (base & 0xffff);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool a = above >> (4 * u + e) & 1u, t = tie >> (4 * u + e) & 1u;
+        if (a || (t && e1 < want)) order[g1 + min(e1, want)] = static_cast<uint16_t>(u * kTurn + tid * 4 + e);
+        g1 += a;
+        e1 += t;
+      }
     }
     gt += all >> 16;
     eq += all & 0xffff;
+    const int count = gt + min(eq, want) - begin;
+    __syncthreads();
+    for (int j0 = tid; j0 < count; j0 += kSelThreads * 4) {
+      int i[4], id[4];
+      float f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        i[u] = j0 + u * kSelThreads < count ? i0 + order[j0 + u * kSelThreads] : i0;
+        id[u] = pages[i[u] / kB];
+        f[u] = dst_w ? w[i[u]] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (j0 + u * kSelThreads < count) emit(begin + j0 + u * kSelThreads, i[u], id[u], f[u]);
+    }
   }
 }
 
-// One new page of one head, K and V: their kept tokens' codes gathered from the
-// old pages (a row is 128 contiguous bytes), the scale their values need, and
-// the codes at it. K and V together, so that the two lookups before a row
-// (its position, its page) are made once and eight row pieces a thread are in
-// flight.
-__global__ void __launch_bounds__(kThreads)
-    pack_kernel(Pool sk, Pool sv, int64_t s_page, int64_t s_head, const int32_t* s_table, int s_num, int s_max,
-                Pool dk, Pool dv, int64_t d_page, int64_t d_head, const int32_t* d_table, int d_num, int d_max, int hkv,
-                const int32_t* lens, int keep, const int32_t* list, int64_t list_stride, DevStatus* status) {
-  __shared__ float red[2][kThreads / 32];
-  const int g = blockIdx.y, b = blockIdx.z, page = blockIdx.x;
-  const int n = min(min(max(lens[b], 0), s_max * kB), keep);
-  const int rows = min(n - page * kB, kB);
-  if (rows <= 0) return;
-  const int id = d_table[static_cast<int64_t>(b) * d_max + page];
-  if (id < 0 || id >= d_num) {
-    if (g == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
-    return;
-  }
+// Asynchronous copies of 16 or 4 bytes to shared memory; nothing is read and
+// zeros are written where `there` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// New pages: their kept tokens' codes gathered from the old pages (a row is
+// 128 contiguous bytes), the scale their values need, and the codes at it. A
+// CTA takes every gridDim.x-th page of one head, K and V together. A row is
+// found through the list, so a page is three dependent reads and a write: the
+// copies of the next two pages are under way while one is packed (each thread
+// copies what it packs itself, so nothing but the maximum is shared). Without
+// that, with four such CTAs on an SM, 512k -> 128k tokens took 105 us against
+// 79 at the copy rate.
+constexpr int kStages = 3;
+struct PackStage {
+  uint4 codes[2][kPasses][kThreads];
+  float scale[2][kPasses][kRowsAtOnce];  // copied and read by a row's first thread
+};
+constexpr size_t kPackSmem = kStages * sizeof(PackStage);
+
+__global__ void __launch_bounds__(kThreads, 2)
+    pack_kernel(Pool sk, Pool sv, int64_t s_page, int64_t s_head, int s_max, Pool dk, Pool dv, int64_t d_page,
+                int64_t d_head, const int32_t* d_table, int d_num, int d_max, int hkv, const int32_t* lens, int keep,
+                int new_pages, int items, const int32_t* list, int64_t list_stride, DevStatus* status) {
+  extern __shared__ uint8_t smem_raw[];
+  PackStage* stages = reinterpret_cast<PackStage*>(smem_raw);
+  __shared__ float red[2][2][kThreads / 32];
+  const int tid = threadIdx.x;
+  const int col = (tid & (kRowThreads - 1)) * 16, row0 = tid / kRowThreads;
   grid_dep_wait();
-  const int col = (threadIdx.x & (kRowThreads - 1)) * 16, row0 = threadIdx.x / kRowThreads;
-  const int32_t* pos = list + (static_cast<int64_t>(b) * hkv + g) * list_stride + page * kB;
-  const int32_t* tab = s_table + static_cast<int64_t>(b) * s_max;
-  int src[kPasses], old[kPasses];
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int row = row0 + p * kRowsAtOnce;
-    old[p] = row < rows ? pos[row] : -1;
-  }
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) src[p] = old[p] >= 0 ? tab[old[p] / kB] : -1;
-  uint4 c[2][kPasses];
-  float s[2][kPasses];
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    c[0][p] = c[1][p] = make_uint4(0u, 0u, 0u, 0u);
-    s[0][p] = s[1][p] = 0.f;
-    if (old[p] < 0) continue;
-    if (src[p] < 0 || src[p] >= s_num) {
-      report_error(status, CRISP_ERR_BOUNDS, 0x713);
-      continue;
-    }
-    const int64_t at = src[p] * s_page + g * s_head + (old[p] % kB) * kD + col;
-    const int64_t sat = static_cast<int64_t>(src[p]) * hkv + g;
-    c[0][p] = __ldcs(reinterpret_cast<const uint4*>(sk.codes + at));
-    c[1][p] = __ldcs(reinterpret_cast<const uint4*>(sv.codes + at));
-    s[0][p] = sk.scale[sat];
-    s[1][p] = sv.scale[sat];
-  }
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float amax = 0.f;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      // the largest magnitude: codes without their sign order as the values do, 0x7f is NaN
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t m = (&c[x][p].x)[e] & 0x7f7f7f7fu;
-        top = __vmaxu4(top, m & ~__vcmpeq4(m, 0x7f7f7f7fu));
+
+  // The next item of this CTA that has rows: its head, rows, and page (-1: none left).
+  struct Item {
+    int g, rows, id;
+  };
+  int at = static_cast<int>(blockIdx.x);
+  auto start = [&](PackStage& st) -> Item {
+    Item it{0, 0, -1};
+    for (; at < items; at += static_cast<int>(gridDim.x)) {
+      const int page = at % new_pages, bg = at / new_pages, b = bg / hkv;
+      const int n = min(min(max(lens[b], 0), s_max * kB), keep);
+      if (n <= page * kB) continue;
+      it.g = bg - b * hkv;
+      it.rows = min(n - page * kB, kB);
+      it.id = d_table[static_cast<int64_t>(b) * d_max + page];
+      if (it.id < 0 || it.id >= d_num) {
+        if (tid == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
+        it.id = -1;
+        continue;
       }
-      top = __vmaxu4(top, top >> 16);
-      top = __vmaxu4(top, top >> 8) & 0xffu;
-      float v, none;
-      unpack_e4m3x2(static_cast<uint16_t>(top), v, none);
-      amax = fmaxf(amax, v * s[x][p]);
-    }
-    amax = block_max(amax, red[x]);
-    const float sn = exp2_int(scale_exponent(amax)), inv = 1.f / sn;
-    uint8_t* codes = (x ? dv : dk).codes + id * d_page + g * d_head;
+      const int32_t* where = list + bg * list_stride + page * kB;
+      int src[kPasses];
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int row = row0 + p * kRowsAtOnce;
-      if (row >= rows) continue;
-      const float ratio = s[x][p] * inv;
-      *reinterpret_cast<uint4*>(codes + row * kD + col) = ratio == 1.f ? c[x][p] : rescale16(c[x][p], ratio);
+      for (int p = 0; p < kPasses; ++p) {
+        const int row = row0 + p * kRowsAtOnce;
+        src[p] = row < it.rows ? where[row] : 0;
+      }
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const bool there = row0 + p * kRowsAtOnce < it.rows && src[p] >= 0;
+        if (src[p] < 0) {
+          report_error(status, CRISP_ERR_BOUNDS, 0x713);
+          src[p] = 0;
+        }
+        const int64_t from = src[p] / kB * s_page + it.g * s_head + (src[p] % kB) * kD + col;
+        const int64_t sat = static_cast<int64_t>(src[p] / kB) * hkv + it.g;
+        copy16(&st.codes[0][p][tid], sk.codes + from, there);
+        copy16(&st.codes[1][p][tid], sv.codes + from, there);
+        if (col == 0) {
+          copy4(&st.scale[0][p][row0], sk.scale + sat, there);
+          copy4(&st.scale[1][p][row0], sv.scale + sat, there);
+        }
+      }
+      at += static_cast<int>(gridDim.x);
+      break;
     }
-    if (threadIdx.x == 0) (x ? dv : dk).scale[static_cast<int64_t>(id) * hkv + g] = sn;
+    copies_commit();
+    return it;
+  };
+
+  Item now = start(stages[0]), next = start(stages[1]);
+  for (int k = 0; now.id >= 0; ++k) {
+    const Item after = start(stages[(k + 2) % kStages]);
+    copies_wait<2>();
+    const PackStage& st = stages[k % kStages];
+    float amax[2] = {0.f, 0.f}, s[2][kPasses];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        s[x][p] = __shfl_sync(0xffffffffu, col == 0 ? st.scale[x][p][row0] : 0.f, tid & 31 & ~(kRowThreads - 1));
+        amax[x] = fmaxf(amax[x], max16(st.codes[x][p][tid]) * s[x][p]);
+      }
+    // both maxima over the block
+    float(&rd)[2][kThreads / 32] = red[k & 1];
+    amax[0] = warp_max(amax[0]);
+    amax[1] = warp_max(amax[1]);
+    if ((tid & 31) == 0) {
+      rd[0][tid >> 5] = amax[0];
+      rd[1][tid >> 5] = amax[1];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float sn = exp2_int(scale_exponent(warp_max(rd[x][tid & (kThreads / 32 - 1)]))), inv = 1.f / sn;
+      uint8_t* codes = (x ? dv : dk).codes + now.id * d_page + now.g * d_head;
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int row = row0 + p * kRowsAtOnce;
+        if (row >= now.rows) continue;
+        *reinterpret_cast<uint4*>(codes + row * kD + col) = rescale16(st.codes[x][p][tid], s[x][p] * inv);
+      }
+      if (tid == 0) (x ? dv : dk).scale[static_cast<int64_t>(now.id) * hkv + now.g] = sn;
+    }
+    now = next;
+    next = after;
   }
+  copies_wait<0>();
 }
 
 Pool k_pool(const crisp_kv_cache& c) { return {static_cast<uint8_t*>(c.k), c.k_scale}; }
@@ -449,9 +632,10 @@ cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new,
 }
 
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
-                            int sink, int recent, float* new_weights, int32_t* list, int64_t list_stride,
-                            DevStatus* status, cudaStream_t st) {
+                            int sink, int recent, float* new_weights, int32_t* kept, int32_t* list,
+                            int64_t list_stride, DevStatus* status, int sms, cudaStream_t st) {
   const int cap = src.max_pages * kB;
+  const int64_t new_cap = static_cast<int64_t>(dst.max_pages) * kB;
   const bool wide = cap >= kClusterLen;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
@@ -459,33 +643,34 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   cfg.attrs = &attr;
   cfg.blockDim = dim3(kSelThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(src.batch * src.hkv * (wide ? kCluster : 1)));
-  cudaError_t e;
   if (wide) {
-    e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = kCluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, select_kernel<kCluster>, weights, static_cast<const int32_t*>(src.lens), dst.lens,
-                           src.hkv, cap, keep, sink, recent, new_weights, static_cast<int64_t>(dst.max_pages) * kB,
-                           list, list_stride, status);
-  } else {
-    e = cudaLaunchKernelEx(&cfg, select_kernel<1>, weights, static_cast<const int32_t*>(src.lens), dst.lens, src.hkv,
-                           cap, keep, sink, recent, new_weights, static_cast<int64_t>(dst.max_pages) * kB, list,
-                           list_stride, status);
   }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? select_kernel<kCluster> : select_kernel<1>, weights,
+                                     static_cast<const int32_t*>(src.lens), dst.lens, src.hkv, cap, keep, sink, recent,
+                                     src.table, src.num_pages, new_weights, new_cap, kept, new_cap, list, list_stride,
+                                     status);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(pack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPackSmem));
+  if (e != cudaSuccess) return e;
+  const int new_pages = (min(keep, cap) + kB - 1) / kB;
+  const int items = src.batch * src.hkv * new_pages;
   attr = cudaLaunchAttribute{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>((min(keep, cap) + kB - 1) / kB), src.hkv, src.batch);
-  return cudaLaunchKernelEx(&cfg, pack_kernel, k_pool(src), v_pool(src), src.page_stride, src.head_stride, src.table,
-                            src.num_pages, src.max_pages, k_pool(dst), v_pool(dst), dst.page_stride, dst.head_stride,
-                            dst.table, dst.num_pages, dst.max_pages, src.hkv, static_cast<const int32_t*>(src.lens),
-                            keep, static_cast<const int32_t*>(list), list_stride, status);
+  cfg.gridDim = dim3(static_cast<unsigned>(min(items, 2 * sms)));
+  cfg.dynamicSmemBytes = kPackSmem;
+  return cudaLaunchKernelEx(&cfg, pack_kernel, k_pool(src), v_pool(src), src.page_stride, src.head_stride,
+                            src.max_pages, k_pool(dst), v_pool(dst), dst.page_stride, dst.head_stride, dst.table,
+                            dst.num_pages, dst.max_pages, src.hkv, static_cast<const int32_t*>(src.lens), keep,
+                            new_pages, items, static_cast<const int32_t*>(list), list_stride, status);
 }
 
 }  // namespace crisp

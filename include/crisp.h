@@ -460,8 +460,8 @@ CRISP_API crisp_status crisp_prefill_layer_host(crisp_host_pipeline* pipeline, c
  *
  * lens[b] counts the tokens held, the ones being appended or asked about
  * included: advance it, then append, then attend. Rows of a page at or past
- * lens[b] may hold anything. 1 <= batch <= 1024, max_pages <= 8192. Pointers
- * are device pointers: k and v (and the strides) 16-byte aligned, the others
+ * lens[b] may hold anything. batch <= 1024, max_pages <= 8192, num_pages <
+ * 2^24. Pointers are device pointers: k and v (and the strides) 16-byte aligned, the others
  * 4-byte aligned. */
 typedef struct crisp_kv_cache {
   int32_t batch;        /* sequences */
