@@ -162,19 +162,27 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr() if hasattr(t, "data_ptr") else int(t))
 
 
-_raw_stream = None
+_current = None
+
+
+def _cuda_state():
+    """(current device index, its current stream's handle), without building a
+    Stream object (3 us a call)."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        dev, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+        def _current():
+            d = dev()
+            return d, raw(d)
+    return _current()
 
 
 def _stream(stream):
     if stream is None:
-        # the current device's current stream, without building a Stream object (3 us a call)
-        global _raw_stream
-        if _raw_stream is None:
-            import torch
-            torch.cuda.init()
-            raw, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            _raw_stream = lambda: raw(dev())
-        return ctypes.c_void_p(_raw_stream())
+        return ctypes.c_void_p(_cuda_state()[1])
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -417,13 +425,20 @@ def _rows(what, t, cache, dtype):
     return t.data_ptr()
 
 
-def _on_device(cache, *tensors):
-    """The calls run on the current device and stream: everything has to be there."""
-    dev = cache.device_index
-    if dev >= 0:
-        import torch
-        if torch.cuda.current_device() == dev and all(t is None or t.get_device() == dev for t in tensors):
-            return
+def _on_device(cache, stream, *tensors):
+    """The handle of the stream to run on (None: the current device's current
+    one). Everything has to be on the current device."""
+    want = cache.device_index
+    if want >= 0:
+        dev, handle = _cuda_state()
+        if dev == want:
+            for t in tensors:
+                if t is not None and t.get_device() != want:
+                    break
+            else:
+                if stream is None:
+                    return handle
+                return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     raise ValueError("the cache and every tensor of the call must be on the current CUDA device")
 
 
@@ -460,10 +475,10 @@ def kv_append(cache, k_new, v_new, ws, new_lens=None, stream=None):
         lens = cache.tensors[5]
         _need(new_lens.shape == lens.shape and new_lens.dtype == lens.dtype and new_lens.is_contiguous(),
               "kv_append: new_lens must be contiguous int32 [batch]")
-    _on_device(cache, k_new, v_new, ws, new_lens)
+    st = _on_device(cache, stream, k_new, v_new, ws, new_lens)
     _check(lib().crisp_kv_append(ctypes.byref(cache), ctypes.byref(kt), ctypes.byref(vt), n_new,
-                                 None if new_lens is None else new_lens.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                                 _stream(stream)), "crisp_kv_append")
+                                 None if new_lens is None else new_lens.data_ptr(), ws.data_ptr(), _nbytes(ws), st),
+           "crisp_kv_append")
 
 
 def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale=0.0, stream=None):
@@ -478,10 +493,9 @@ def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale
     f32 = cache.tensors[2].dtype
     w_in = _rows("decode_attention: weights_in", weights_in, cache, f32)
     w_out = _rows("decode_attention: weights_out", weights_out, cache, f32)
-    _on_device(cache, q, out, ws, weights_in, weights_out)
+    st = _on_device(cache, stream, q, out, ws, weights_in, weights_out)
     _check(lib().crisp_decode_attention(ctypes.byref(cache), hq, q_len, scale, ctypes.byref(qt), ctypes.byref(ot),
-                                        w_in, w_out, ws.data_ptr(), _nbytes(ws), _stream(stream)),
-           "crisp_decode_attention")
+                                        w_in, w_out, ws.data_ptr(), _nbytes(ws), st), "crisp_decode_attention")
 
 
 def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=None, kept=None, stream=None):
@@ -493,9 +507,9 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
     w = _rows("kv_evict: weights", weights, cache, f32)
     new_w = _rows("kv_evict: new_weights", new_weights, new_cache, f32)
     pos = _rows("kv_evict: kept", kept, new_cache, i32)
-    _on_device(cache, new_cache.tensors[0], weights, ws, new_weights, kept)
+    st = _on_device(cache, stream, new_cache.tensors[0], weights, ws, new_weights, kept)
     _check(lib().crisp_kv_evict(ctypes.byref(cache), ctypes.byref(new_cache), w, keep, sink, recent, new_w, pos,
-                                ws.data_ptr(), _nbytes(ws), _stream(stream)), "crisp_kv_evict")
+                                ws.data_ptr(), _nbytes(ws), st), "crisp_kv_evict")
 
 
 def wait_selftest(ws, limit_ns, stream=None):

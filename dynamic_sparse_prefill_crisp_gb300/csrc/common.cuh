@@ -140,6 +140,25 @@ struct DecodeLayout {
 DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights);
 int decode_row_chunks(int rows);  // row chunks of a (sequence, kv head)
 
+// A launch that may be scheduled while the kernel before it in the stream still
+// ends: the kernel calls ptx::grid_dep_wait before it reads or writes what
+// others do.
+template <class... P, class... Q>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                             const Q&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // ---- launchers (one per translation unit); return cudaSuccess or the launch error
 cudaError_t launch_proxy(const crisp_shape& s, const TmaMaps& maps, float* pmap, char* ws, cudaStream_t st);
 cudaError_t launch_proxy_masses(const crisp_shape& s, const TmaMaps& maps, uint64_t* vmass, uint64_t* smass,

@@ -9,7 +9,7 @@
 //   acc = acc 2^(m - m') + O^T vs 2^(m_t - m')      fp32 registers, m' = max(m, m_t)
 // K and V go from HBM by TMA to shared memory and into the tensor cores as
 // they are: nothing dequantises them. The other operand is made of two e4m3
-// pieces, x = hi + lo / 16 (rows r and rows + r of B): a bf16 q at a power-of-two
+// pieces, x = hi + lo / 16 (columns r and 8 + r of 16 for eight rows): a bf16 q at a power-of-two
 // row scale is exactly that sum down to 2^-14 of the row's largest element;
 // p (scaled to 256 at the step's maximum) is off by at most 2^-8 of itself, as
 // a bf16 p would be. O^T is read back every tile, so that page scales and the
@@ -203,15 +203,17 @@ __device__ __forceinline__ float warp_rows(float (&v)[kR]) {
   return v[0];
 }
 
-// A group's eight rows of an accumulator: v[r] = hi + lo / 16, hi in columns
-// [0, 8) of taddr, lo `n` columns further on.
-__device__ __forceinline__ void load_rows(uint32_t taddr, int n, float (&v)[kWgRows]) {
-  uint32_t x[8], y[8];
-  tmem_ld8x2(taddr, taddr + n, x, y);
+// A group's eight rows of two accumulators (16 columns each): v[r] = hi + lo / 16.
+__device__ __forceinline__ void load_rows(uint32_t ta, uint32_t tb, float (&v)[kWgRows], float (&w)[kWgRows]) {
+  uint32_t x[16], y[16];
+  tmem_ld16x2(ta, tb, x, y);
 #pragma unroll
-  for (int r = 0; r < 8; r += 2)
-    ffma2(v[r], v[r + 1], __uint_as_float(y[r]), __uint_as_float(y[r + 1]), 1.f / kLo, 1.f / kLo,
+  for (int r = 0; r < 8; r += 2) {
+    ffma2(v[r], v[r + 1], __uint_as_float(x[8 + r]), __uint_as_float(x[9 + r]), 1.f / kLo, 1.f / kLo,
           __uint_as_float(x[r]), __uint_as_float(x[r + 1]));
+    ffma2(w[r], w[r + 1], __uint_as_float(y[8 + r]), __uint_as_float(y[9 + r]), 1.f / kLo, 1.f / kLo,
+          __uint_as_float(y[r]), __uint_as_float(y[r + 1]));
+  }
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
@@ -264,6 +266,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
+  // From here on what earlier kernels of the stream wrote is read, and results are written.
+  grid_dep_wait();
   // Pages before each sequence (an inclusive scan over the batch, a block of sequences at a time).
   int before = 0;
   if (threadIdx.x == 0) pre[0] = 0;
@@ -357,8 +361,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     }
   } else if (n > 0 && warp == kMmaWarp) {
     constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, C::N, false, false);
-    constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, C::N, true, false);
-    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dp = sdesc_sw128(smem_u32(sP), 16, 1024);
+    constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, C::N, true, true);
+    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dp = sdesc_mn8(smem_u32(sP), 128, kB * 16);
     bool go = true;
     Walk x;  // of the score products, up to two steps ahead of the others
     x.begin(pre, a, t_lo, n);
@@ -417,8 +422,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
           const uint64_t dv = sdesc_sw128(smem_u32(sV + s * kPage), 1024, 1024);
           const uint64_t dpj = dp + (ob * kStep + j) * (C::op >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4096 bytes of V, 32 of P'
-            umma_f8_ss(tmem + C::o_col + (ob * kStep + j) * C::N, dv + 256 * kk, dpj + 2 * kk, idesc_pv, kk > 0);
+          for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4096 bytes of V, 512 of P'
+            umma_f8_ss(tmem + C::o_col + (ob * kStep + j) * C::N, dv + 256 * kk, dpj + 32 * kk, idesc_pv, kk > 0);
           umma_commit(&sh.v_empty[s]);
         }
         __syncwarp();
@@ -446,47 +451,48 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         break;
       }
       uint8_t* dst = sQ + buf * C::op;
+      constexpr int kAtOnce = kR < 16 ? kR : 16;  // rows asked for together
 #pragma unroll 1
-      for (int rb = 0; rb < kR; rb += 8) {
-        uint2 w[8];
+      for (int rb = 0; rb < kR; rb += kAtOnce) {
+        uint2 w[kAtOnce];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int row = r0 + rb + r;
-          w[r] = make_uint2(0u, 0u);
+        for (int rr = 0; rr < kAtOnce; ++rr) {
+          const int row = r0 + rb + rr;
+          w[rr] = make_uint2(0u, 0u);
           if (row < a.rows) {
-            const int i = row / a.group, h = g * a.group + row - i * a.group;
-            w[r] = *reinterpret_cast<const uint2*>(a.q + x.b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
+            const int i = a.q_len == 1 ? 0 : row / a.group, h = g * a.group + row - i * a.group;
+            w[rr] = *reinterpret_cast<const uint2*>(a.q + x.b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
           }
         }
 #pragma unroll
-      for (int rr = 0; rr < 8; ++rr) {
-        const int r = rb + rr;
-        float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
-                      __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
-        float amax = 0.f;
+        for (int rr = 0; rr < kAtOnce; ++rr) {
+          const int r = rb + rr;
+          float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
+                        __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
+          float amax = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
-          amax = fmaxf(amax, fabsf(v[e]));                          // ignores NaN
-        }
-        amax = warp_max(amax);
-        const int e2 = scale_exponent(amax);
-        const float inv = exp2_int(-e2);
-        uint32_t hi = 0, lo = 0;
+          for (int e = 0; e < 4; ++e) {
+            if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
+            amax = fmaxf(amax, fabsf(v[e]));                          // passes over NaN
+          }
+          const int e2 = scale_exponent(warp_max(amax));
+          const float inv = exp2_int(-e2);
+          uint32_t hi = 0, lo = 0;
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
-          const uint16_t h2 = pack_e4m3x2(y0, y1);
-          float h0, h1;
-          unpack_e4m3x2(h2, h0, h1);
-          hi |= static_cast<uint32_t>(h2) << (8 * e);
-          lo |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
+          for (int e = 0; e < 4; e += 2) {
+            const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
+            const uint16_t h2 = pack_e4m3x2(y0, y1);
+            float h0, h1;
+            unpack_e4m3x2(h2, h0, h1);
+            hi |= static_cast<uint32_t>(h2) << (8 * e);
+            lo |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
+          }
+          // rows 16 (r / 8) + r % 8 and 8 further on; 16-byte chunks are swizzled by the row's low 3 bits
+          const uint32_t at = (r / 8 * 16 + r % 8) * 128 + (((lane >> 2) ^ (r % 8)) << 4) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(dst + at) = hi;
+          *reinterpret_cast<uint32_t*>(dst + 8 * 128 + at) = lo;
+          if (lane == 0) sh.qs[buf][r] = exp2_int(e2) * a.c;
         }
-        const uint32_t at = (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;  // kR is a multiple of 8
-        *reinterpret_cast<uint32_t*>(dst + r * 128 + at) = hi;
-        *reinterpret_cast<uint32_t*>(dst + (kR + r) * 128 + at) = lo;
-        if (lane == 0) sh.qs[buf][r] = exp2_int(e2) * a.c;
-      }
       }
       fence_async_shared();
       __syncwarp();
@@ -499,10 +505,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     const int tid = threadIdx.x & 127;              // key of a tile, feature of the output
     const int row0 = wg * kWgRows;                  // the group's rows of the chunk
     const int bar = 1 + wg;
-    const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + row0;
-    // byte `tid` of rows row0 + r (hi) and kR + row0 + r (lo) of P'; 16-byte chunks are swizzled by the row's low 3 bits
-    uint8_t* const p_at = sP + row0 * 128 + (tid & 15);
-    const uint32_t p_col = static_cast<uint32_t>(tid >> 4);
+    const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 2 * row0;
+    // P' is MN-major: key `tid`'s 16 bytes of the group's rows (hi, then lo) lie together
+    uint8_t* const p_at = sP + (wg * kB + tid) * 16;
     const int my_row = lane & (kWgRows - 1);        // row of the lane-held maximum
     float acc[kWgRows], l[kWgRows];
     float m = -INFINITY;                            // running maximum of row my_row, base 2
@@ -559,11 +564,12 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       tc_fence_after();
       float wl[kWgRows];
       load8(sh.wl[warp][ob], wl);
+      float both[kStep][kWgRows];  // of a step of one tile, the second is not used
+      load_rows(lane_tmem + C::o_col + ob * kStep * C::N, lane_tmem + C::o_col + (ob * kStep + 1) * C::N, both[0], both[1]);
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
         if (j >= o.tiles) break;
-        float v[kWgRows];
-        load_rows(lane_tmem + C::o_col + (ob * kStep + j) * C::N, kR, v);
+        float(&v)[kWgRows] = both[j];
         if (o.tail) {
           // added here, one by one, so that what those keys hold does not
           // reach the rows that do not see them
@@ -657,6 +663,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       float s[kStep][kWgRows], t[kWgRows], vst[kStep];
       bool partial[kStep], held[kStep];  // some rows do not see some keys; the page is there
       load8(&sh.qs[item & 1][row0], t);
+      // of a step of one tile, the second buffer's old scores are read and not used
+      load_rows(lane_tmem + buf * kStep * C::N, lane_tmem + (buf * kStep + 1) * C::N, s[0], s[1]);
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
         held[j] = bcast(z, (i - win + j) & 31) >= 0;
@@ -668,7 +676,6 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
           for (int r = 0; r < kWgRows; ++r) s[j][r] = -INFINITY;
           continue;
         }
-        load_rows(lane_tmem + (buf * kStep + j) * C::N, kR, s[j]);
 #pragma unroll
         for (int r = 0; r < kWgRows; r += 2) {
           float c0, c1;
@@ -762,17 +769,16 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
             }
           }
         }
+        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int r = 0; r < kWgRows; r += 2) {
-          uint16_t hi, lo;
-          split_e4m3x2(p[r], p[r + 1], hi, lo);
-          const uint32_t c0 = r * 128 + ((p_col ^ r) << 4), c1 = (r + 1) * 128 + ((p_col ^ (r + 1)) << 4);
-          uint8_t* at = p_at + (st % C::bufs * kStep + j) * C::op;
-          at[c0] = static_cast<uint8_t>(hi);
-          at[c1] = static_cast<uint8_t>(hi >> 8);
-          at[kR * 128 + c0] = static_cast<uint8_t>(lo);
-          at[kR * 128 + c1] = static_cast<uint8_t>(lo >> 8);
+          uint16_t h, l2;
+          split_e4m3x2(p[r], p[r + 1], h, l2);
+          hi[r / 2] = h;
+          lo[r / 2] = l2;
         }
+        *reinterpret_cast<uint4*>(p_at + (st % C::bufs * kStep + j) * C::op) = make_uint4(
+            hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
       if (!ok) break;
       fence_async_shared();
@@ -923,16 +929,18 @@ __global__ void __launch_bounds__(kWeightThreads)
     weights_kernel(const __grid_constant__ Args a, const float* w_in, float* w_out) {
   __shared__ float lse[kMaxGroupRows];
   const int g = blockIdx.y, b = blockIdx.z;
+  grid_dep_launch();
   bool bad;
   const int len = clamped_len(a, b, bad);
   const int key = blockIdx.x * kWeightKeys + threadIdx.x * 4;
-  if (static_cast<int>(blockIdx.x) * kWeightKeys >= len) return;
   const int64_t cap = static_cast<int64_t>(a.max_pages) * kB, bg = static_cast<int64_t>(b) * a.hkv + g;
   const int64_t at = bg * cap + key;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
   // rows of weights and scores end at a multiple of 128: whole groups of four are there
   if (w_in != nullptr && key < len) w = *reinterpret_cast<const float4*>(w_in + at);
+  // before any return: this kernel may not end before the ones it depends on
   grid_dep_wait();
+  if (static_cast<int>(blockIdx.x) * kWeightKeys >= len) return;
   for (int r = threadIdx.x; r < a.rows; r += kWeightThreads) lse[r] = a.lse[bg * a.rows + r];
   __syncthreads();
   if (key >= len) return;
@@ -968,27 +976,12 @@ cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {
   cudaError_t e =
       cudaFuncSetAttribute(decode_kernel<kWG, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_kernel<kWG, kScores><<<a.ctas, C::threads, smem, st>>>(maps.k, maps.v, a);
-  return cudaGetLastError();
+  return launch_dependent(decode_kernel<kWG, kScores>, dim3(static_cast<unsigned>(a.ctas)), C::threads, smem, st,
+                          maps.k, maps.v, a);
 }
 template <int kWG>
 cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {
   return a.scores != nullptr ? launch_groups<kWG, true>(maps, a, st) : launch_groups<kWG, false>(maps, a, st);
-}
-
-// Launches that may start while the kernel before them ends (they wait for its results themselves).
-template <class... P, class... Q>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, Q&&... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Q>(args)...);
 }
 
 }  // namespace
@@ -1056,11 +1049,11 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
                                                                     : launch_groups<4>(maps, a, st);
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(std::min(kr, a.rows));
-  e = launch_dependent(join_kernel, dim3(static_cast<unsigned>(a.ctas), rows), kJoinThreads, st, a, kr);
+  e = launch_dependent(join_kernel, dim3(static_cast<unsigned>(a.ctas), rows), kJoinThreads, 0, st, a, kr);
   if (e != cudaSuccess || weights_out == nullptr) return e;
   const unsigned blocks = static_cast<unsigned>((c.max_pages * kB + kWeightKeys - 1) / kWeightKeys);
   return launch_dependent(weights_kernel, dim3(blocks, static_cast<unsigned>(c.hkv), static_cast<unsigned>(c.batch)),
-                          kWeightThreads, st, a, weights_in, weights_out);
+                          kWeightThreads, 0, st, a, weights_in, weights_out);
 }
 
 }  // namespace crisp

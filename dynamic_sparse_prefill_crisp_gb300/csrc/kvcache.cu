@@ -25,14 +25,10 @@ constexpr int kPasses = kB / kRowsAtOnce;         // 4
 
 __device__ __forceinline__ float block_max(float v, float* red) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = warp_max(v);
   if (lane == 0) red[warp] = v;
   __syncthreads();
-  v = red[lane & (kThreads / 32 - 1)];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  return warp_max(red[lane & (kThreads / 32 - 1)]);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -45,6 +41,29 @@ __device__ __forceinline__ float finite_abs(float x) {
 // The code of x at inv = 1 / scale; a non-finite x becomes NaN.
 __device__ __forceinline__ float scaled(float x, float inv) {
   return fabsf(x) <= 3.402823466e38f ? x * inv : __int_as_float(0x7fffffff);
+}
+// The larger magnitudes of two bf16 pairs (as 16-bit integers they order the
+// same way; infinities and NaN are 0x7f80 and above).
+constexpr uint32_t kBf16Inf = 0x7f80u;
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// Eight bf16 values as codes at inv = 1 / scale, a power of two (so the product
+// is exact, or far below half the smallest code).
+template <bool kFinite>
+__device__ __forceinline__ uint2 codes8(const uint4& x, float inv) {
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = (&x.x)[e];
+    float a, b;
+    if (kFinite) {
+      fmul2(a, b, bf16_lo(w), bf16_hi(w), inv, inv);
+    } else {
+      a = scaled(bf16_lo(w), inv);
+      b = scaled(bf16_hi(w), inv);
+    }
+    c[e] = pack_e4m3x2(a, b);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // Two codes rounded again at `ratio` times their values, for a power of two
@@ -121,6 +140,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int g = blockIdx.y >> 1, b = blockIdx.z;
   const bool is_v = blockIdx.y & 1;
   const int cap = max_pages * kB;
+  grid_dep_launch();
+  grid_dep_wait();
   int len = lens[b], cnt = new_lens != nullptr ? new_lens[b] : n_new;
   const bool bad = len < 0 || len > cap || cnt < 0 || cnt > min(n_new, len);
   if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x701);
@@ -137,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int first = max(start - lo, 0), end = min(len - lo, kB);  // rows [first, end) are new, [0, first) old
   // the new values are asked for before the page is looked up
   uint4 x[kPasses][2];
-  float amax = 0.f;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int row = row0 + p * kRowsAtOnce;
@@ -158,15 +178,25 @@ __global__ void __launch_bounds__(kThreads, 4)
   float* scale = pool.scale + static_cast<int64_t>(id) * hkv + g;
   const bool held = first > 0;
   const float s_old = held ? *scale : 0.f;
+  uint32_t top = 0u;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w = (&x[p][h].x)[e];
-        amax = fmaxf(amax, fmaxf(finite_abs(bf16_lo(w)), finite_abs(bf16_hi(w))));
-      }
+      for (int e = 0; e < 4; ++e) top = max_abs2(top, (&x[p][h].x)[e]);
+  top = max(top & 0xffffu, top >> 16);
+  const bool finite = top < kBf16Inf;  // this thread's values
+  float amax = bf16_lo(top);
+  if (!finite) {
+    amax = 0.f;
+    for (int p = 0; p < kPasses; ++p)
+      for (int h = 0; h < 2; ++h)
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = (&x[p][h].x)[e];
+          amax = fmaxf(amax, fmaxf(finite_abs(bf16_lo(w)), finite_abs(bf16_hi(w))));
+        }
+  }
   amax = block_max(amax, red);
   float s = exp2_int(scale_exponent(amax));
   if (held) s = fmaxf(s, s_old);
@@ -175,14 +205,9 @@ __global__ void __launch_bounds__(kThreads, 4)
   for (int p = 0; p < kPasses; ++p) {
     const int row = row0 + p * kRowsAtOnce;
     if (row >= first && row < end) {
-      uint4 c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w0 = (&x[p][e >> 1].x)[(e & 1) * 2], w1 = (&x[p][e >> 1].x)[(e & 1) * 2 + 1];
-        (&c.x)[e] = static_cast<uint32_t>(pack_e4m3x2(scaled(bf16_lo(w0), inv), scaled(bf16_hi(w0), inv))) |
-                    static_cast<uint32_t>(pack_e4m3x2(scaled(bf16_lo(w1), inv), scaled(bf16_hi(w1), inv))) << 16;
-      }
-      *reinterpret_cast<uint4*>(codes + row * kD + col) = c;
+      const uint2 lo8 = finite ? codes8<true>(x[p][0], inv) : codes8<false>(x[p][0], inv);
+      const uint2 hi8 = finite ? codes8<true>(x[p][1], inv) : codes8<false>(x[p][1], inv);
+      *reinterpret_cast<uint4*>(codes + row * kD + col) = make_uint4(lo8.x, lo8.y, hi8.x, hi8.y);
     } else if (row < first && s != s_old) {
       uint4* at = reinterpret_cast<uint4*>(codes + row * kD + col);
       *at = rescale16(*at, s_old * inv);
@@ -262,6 +287,7 @@ __global__ void __launch_bounds__(kSelThreads, 2)
   __shared__ alignas(8) int tot[2][kAhead * kSelThreads / 32];
   __shared__ int own[2];  // this CTA's keys above the threshold, and equal to it
   grid_dep_launch();
+  grid_dep_wait();
   const int tid = threadIdx.x;
   const int part = kC > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
   const int bg = blockIdx.x / kC, b = bg / hkv;
@@ -521,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     pack_kernel(Pool sk, Pool sv, int64_t s_page, int64_t s_head, int s_max, Pool dk, Pool dv, int64_t d_page,
                 int64_t d_head, const int32_t* d_table, int d_num, int d_max, int hkv, const int32_t* lens, int keep,
                 int new_pages, int items, const int32_t* list, int64_t list_stride, DevStatus* status) {
+  grid_dep_launch();
   extern __shared__ uint8_t smem_raw[];
   PackStage* stages = reinterpret_cast<PackStage*>(smem_raw);
   __shared__ float red[2][2][kThreads / 32];
@@ -625,10 +652,10 @@ Pool v_pool(const crisp_kv_cache& c) { return {static_cast<uint8_t*>(c.v), c.v_s
 cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
                              const int32_t* new_lens, DevStatus* status, cudaStream_t st) {
   const unsigned reach = static_cast<unsigned>((n_new + kB - 2) / kB + 1);  // pages n_new tokens can touch
-  append_kernel<<<dim3(reach, 2 * c.hkv, c.batch), kThreads, 0, st>>>(
-      k_pool(c), v_pool(c), c.page_stride, c.head_stride, c.hkv, c.num_pages, c.max_pages, c.table, c.lens, new_lens,
-      n_new, k_new, v_new, status);
-  return cudaGetLastError();
+  return launch_dependent(append_kernel, dim3(reach, static_cast<unsigned>(2 * c.hkv), static_cast<unsigned>(c.batch)),
+                          kThreads, 0, st, k_pool(c), v_pool(c), c.page_stride, c.head_stride, c.hkv, c.num_pages,
+                          c.max_pages, c.table, static_cast<const int32_t*>(c.lens), new_lens, n_new, k_new, v_new,
+                          status);
 }
 
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
@@ -638,39 +665,36 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   const int64_t new_cap = static_cast<int64_t>(dst.max_pages) * kB;
   const bool wide = cap >= kClusterLen;
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.stream = st;
-  cfg.attrs = &attr;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
   cfg.blockDim = dim3(kSelThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(src.batch * src.hkv * (wide ? kCluster : 1)));
+  cudaError_t e;
   if (wide) {
-    cudaError_t e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kCluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = kCluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? select_kernel<kCluster> : select_kernel<1>, weights,
-                                     static_cast<const int32_t*>(src.lens), dst.lens, src.hkv, cap, keep, sink, recent,
-                                     src.table, src.num_pages, new_weights, new_cap, kept, new_cap, list, list_stride,
-                                     status);
+  e = cudaLaunchKernelEx(&cfg, wide ? select_kernel<kCluster> : select_kernel<1>, weights,
+                         static_cast<const int32_t*>(src.lens), dst.lens, src.hkv, cap, keep, sink, recent, src.table,
+                         src.num_pages, new_weights, new_cap, kept, new_cap, list, list_stride, status);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(pack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPackSmem));
   if (e != cudaSuccess) return e;
   const int new_pages = (min(keep, cap) + kB - 1) / kB;
   const int items = src.batch * src.hkv * new_pages;
-  attr = cudaLaunchAttribute{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>(min(items, 2 * sms)));
-  cfg.dynamicSmemBytes = kPackSmem;
-  return cudaLaunchKernelEx(&cfg, pack_kernel, k_pool(src), v_pool(src), src.page_stride, src.head_stride,
-                            src.max_pages, k_pool(dst), v_pool(dst), dst.page_stride, dst.head_stride, dst.table,
-                            dst.num_pages, dst.max_pages, src.hkv, static_cast<const int32_t*>(src.lens), keep,
-                            new_pages, items, static_cast<const int32_t*>(list), list_stride, status);
+  return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(min(items, 2 * sms))), kThreads, kPackSmem, st,
+                          k_pool(src), v_pool(src), src.page_stride, src.head_stride, src.max_pages, k_pool(dst),
+                          v_pool(dst), dst.page_stride, dst.head_stride, dst.table, dst.num_pages, dst.max_pages,
+                          src.hkv, static_cast<const int32_t*>(src.lens), keep, new_pages, items,
+                          static_cast<const int32_t*>(list), list_stride, status);
 }
 
 }  // namespace crisp
