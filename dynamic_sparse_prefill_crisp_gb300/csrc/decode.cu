@@ -222,6 +222,52 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// Q' of kRows rows from rb on of a chunk whose first row is r0, by one warp: four
+// features a lane. All rows are asked for before the first is made.
+template <int kRows>
+__device__ __forceinline__ void make_q(const Args& a, uint8_t* dst, float* qs, int b, int g, int r0, int rb) {
+  const int lane = threadIdx.x & 31;
+  uint2 w[kRows];
+#pragma unroll
+  for (int rr = 0; rr < kRows; ++rr) {
+    const int row = r0 + rb + rr;
+    w[rr] = make_uint2(0u, 0u);
+    if (row < a.rows) {
+      const int i = a.q_len == 1 ? 0 : row / a.group, h = g * a.group + row - i * a.group;
+      w[rr] = *reinterpret_cast<const uint2*>(a.q + b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
+    }
+  }
+#pragma unroll
+  for (int rr = 0; rr < kRows; ++rr) {
+    const int r = rb + rr;
+    float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
+                  __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
+      amax = fmaxf(amax, fabsf(v[e]));                          // passes over NaN
+    }
+    const int e2 = scale_exponent(warp_max(amax));
+    const float inv = exp2_int(-e2);
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
+      const uint16_t h2 = pack_e4m3x2(y0, y1);
+      float h0, h1;
+      unpack_e4m3x2(h2, h0, h1);
+      hi |= static_cast<uint32_t>(h2) << (8 * e);
+      lo |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
+    }
+    // rows 16 (r / 8) + r % 8 and 8 further on; 16-byte chunks are swizzled by the row's low 3 bits
+    const uint32_t at = (r / 8 * 16 + r % 8) * 128 + (((lane >> 2) ^ (r % 8)) << 4) + (lane & 3) * 4;
+    *reinterpret_cast<uint32_t*>(dst + at) = hi;
+    *reinterpret_cast<uint32_t*>(dst + 8 * 128 + at) = lo;
+    if (lane == 0) qs[r] = exp2_int(e2) * a.c;
+  }
+}
+
 template <int kWG, bool kScores>
 __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -249,7 +295,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       mbar_init(&sh.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.q_full[s], C::workers);
       mbar_init(&sh.q_empty[s], 1 + kWG);  // the last score product of the item; the softmax groups' end of it
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.p_full[s], C::workers * 32);
@@ -360,80 +406,77 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         mbar_wait(&sh.v_full[q % C::v_slots], (q / C::v_slots) & 1, &never);
     }
   } else if (n > 0 && warp == kMmaWarp) {
-    constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, C::N, false, false);
-    constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, C::N, true, true);
-    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dp = sdesc_mn8(smem_u32(sP), 128, kB * 16);
-    bool go = true;
-    Walk x;  // of the score products, up to two steps ahead of the others
-    x.begin(pre, a, t_lo, n);
-    int ik = 0, iv = 0, item = -1, sk = 0;  // tiles taken, items begun, steps of scores issued
-    bool begins = true;
-    int size[3];                            // tiles of the steps in flight, by step % 3
-    // S of the next step; false when the run has no more (or on abort: go)
-    auto issue_qk = [&]() {
-      if (ik == n) return;
-      if (begins) {
-        ++item;
-        if (!warp_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) go = false;
-      }
-      const int m = min(kStep, x.left), buf = sk & 1;
-      for (int j = 0; go && j < m; ++j, ++ik) {
-        const int s = ik % C::k_slots;
-        if (!warp_wait(&sh.k_full[s], (ik / C::k_slots) & 1, &sh.abort)) go = false;
-        if (!go) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dk = sdesc_sw128(smem_u32(sK + s * kPage), 16, 1024);
-          const uint64_t dqi = dq + (item & 1) * (C::op >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 features a step
-            umma_f8_ss(tmem + (buf * kStep + j) * C::N, dk + 2 * kk, dqi + 2 * kk, idesc_qk, kk > 0);
-          umma_commit(&sh.k_empty[s]);
-        }
-        __syncwarp();
-      }
-      if (!go) return;
-      x.left -= m;
-      begins = x.left == 0;
-      if (lane == 0) {
-        umma_commit(&sh.s_full[buf]);
-        if (begins) umma_commit(&sh.q_empty[item & 1]);
-      }
-      __syncwarp();
-      if (begins && ik < n) x.next(pre, a, n - ik);
-      if (sk % 3 == 0) size[0] = m;
-      else if (sk % 3 == 1) size[1] = m;
-      else size[2] = m;
-      ++sk;
-    };
-    issue_qk();
-    if (go) issue_qk();
-    for (int st = 0; go && iv < n; ++st) {
-      const int ob = st % C::bufs;
-      if (!warp_wait(&sh.p_full[ob], (st / C::bufs) & 1, &sh.abort)) go = false;
-      const int m = st % 3 == 0 ? size[0] : st % 3 == 1 ? size[1] : size[2];
-      for (int j = 0; go && j < m; ++j, ++iv) {
-        const int s = iv % C::v_slots;
-        if (!warp_wait(&sh.v_full[s], (iv / C::v_slots) & 1, &sh.abort)) go = false;
-        if (!go) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t dv = sdesc_sw128(smem_u32(sV + s * kPage), 1024, 1024);
-          const uint64_t dpj = dp + (ob * kStep + j) * (C::op >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 keys a step: 4096 bytes of V, 512 of P'
-            umma_f8_ss(tmem + C::o_col + (ob * kStep + j) * C::N, dv + 256 * kk, dpj + 32 * kk, idesc_pv, kk > 0);
-          umma_commit(&sh.v_empty[s]);
-        }
-        __syncwarp();
-      }
-      if (!go) break;
-      if (lane == 0) umma_commit(&sh.o_full[ob]);
-      __syncwarp();
-      issue_qk();
-    }
     if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_e4m3_f32(128, C::N, false, false);
+      constexpr uint32_t idesc_pv = idesc_e4m3_f32(128, C::N, true, true);
+      const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024), dv0 = sdesc_sw128(smem_u32(sV), 1024, 1024);
+      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dp = sdesc_mn8(smem_u32(sP), 128, kB * 16);
+      bool go = true;
+      Walk x;  // of the score products, up to two steps ahead of the others
+      x.begin(pre, a, t_lo, n);
+      int ik = 0, iv = 0, item = -1, sk = 0;  // tiles taken, items begun, steps of scores issued
+      int ks = 0, kph = 0, vs = 0, vph = 0;   // page slots and their phases
+      bool begins = true;
+      int size[3];                            // tiles of the steps in flight, by step % 3
+      auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(bar, parity, &sh.abort); };
+      // S of the next step, if the run has one more; false on abort
+      auto issue_qk = [&]() -> bool {
+        if (ik == n) return true;
+        if (begins) {
+          ++item;
+          if (!wait(&sh.q_full[item & 1], (item >> 1) & 1)) return false;
+        }
+        const int m = min(kStep, x.left), buf = sk & 1;
+        const uint64_t dqi = dq + (item & 1) * (C::op >> 4);
+        for (int j = 0; j < m; ++j) {
+          if (!wait(&sh.k_full[ks], kph)) return false;
+          tc_fence_after();
+          // 32 features a product
+          umma_f8_x4<2, 2>(tmem + (buf * kStep + j) * C::N, dk0 + ks * (kPage >> 4), dqi, idesc_qk);
+          umma_commit(&sh.k_empty[ks]);
+          if (++ks == C::k_slots) {
+            ks = 0;
+            kph ^= 1;
+          }
+        }
+        ik += m;
+        x.left -= m;
+        begins = x.left == 0;
+        umma_commit(&sh.s_full[buf]);
+        if (begins) {
+          umma_commit(&sh.q_empty[item & 1]);
+          if (ik < n) x.next(pre, a, n - ik);
+        }
+        if (sk % 3 == 0) size[0] = m;
+        else if (sk % 3 == 1) size[1] = m;
+        else size[2] = m;
+        ++sk;
+        return true;
+      };
+      go = issue_qk() && issue_qk();
+      for (int st = 0; go && iv < n; ++st) {
+        const int ob = st % C::bufs, m = st % 3 == 0 ? size[0] : st % 3 == 1 ? size[1] : size[2];
+        if (!wait(&sh.p_full[ob], (st / C::bufs) & 1)) go = false;
+        for (int j = 0; go && j < m; ++j) {
+          if (!wait(&sh.v_full[vs], vph)) {
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          // 32 keys a product: 4096 bytes of V, 512 of P'
+          umma_f8_x4<256, 32>(tmem + C::o_col + (ob * kStep + j) * C::N, dv0 + vs * (kPage >> 4),
+                              dp + (ob * kStep + j) * (C::op >> 4), idesc_pv);
+          umma_commit(&sh.v_empty[vs]);
+          if (++vs == C::v_slots) {
+            vs = 0;
+            vph ^= 1;
+          }
+        }
+        if (!go) break;
+        umma_commit(&sh.o_full[ob]);
+        iv += m;
+        go = issue_qk();
+      }
       if (!go) fail(&sh.abort, a.status, 0x611);
       // Every product has completed before TMEM is released (bounded, ignores the abort flag).
       umma_commit(&sh.drain);
@@ -441,64 +484,24 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       if (!mbar_wait(&sh.drain, 0, &never)) fail(&sh.abort, a.status, 0x612);
     }
   } else if (n > 0 && warp == kQWarp) {
-    // Q' of each item of the run: one row at a time, four features a lane.
+    // Q' of the items of the run but the first, which the softmax warps make
+    // while they wait for its scores.
     Walk x;
     x.begin(pre, a, t_lo, n);
-    for (int t = 0, item = 0; t < n; ++item) {
+    int t = x.left;
+    for (int item = 1; t < n; ++item) {
+      x.next(pre, a, n - t);
       const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc - g * a.chunks) * kR;
       if (!warp_wait(&sh.q_empty[buf], ((item >> 1) & 1) ^ 1, &sh.abort)) {
         if (lane == 0) fail(&sh.abort, a.status, 0x613);
         break;
       }
-      uint8_t* dst = sQ + buf * C::op;
-      constexpr int kAtOnce = kR < 16 ? kR : 16;  // rows asked for together
-#pragma unroll 1
-      for (int rb = 0; rb < kR; rb += kAtOnce) {
-        uint2 w[kAtOnce];
-#pragma unroll
-        for (int rr = 0; rr < kAtOnce; ++rr) {
-          const int row = r0 + rb + rr;
-          w[rr] = make_uint2(0u, 0u);
-          if (row < a.rows) {
-            const int i = a.q_len == 1 ? 0 : row / a.group, h = g * a.group + row - i * a.group;
-            w[rr] = *reinterpret_cast<const uint2*>(a.q + x.b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
-          }
-        }
-#pragma unroll
-        for (int rr = 0; rr < kAtOnce; ++rr) {
-          const int r = rb + rr;
-          float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
-                        __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
-          float amax = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
-            amax = fmaxf(amax, fabsf(v[e]));                          // passes over NaN
-          }
-          const int e2 = scale_exponent(warp_max(amax));
-          const float inv = exp2_int(-e2);
-          uint32_t hi = 0, lo = 0;
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
-            const uint16_t h2 = pack_e4m3x2(y0, y1);
-            float h0, h1;
-            unpack_e4m3x2(h2, h0, h1);
-            hi |= static_cast<uint32_t>(h2) << (8 * e);
-            lo |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
-          }
-          // rows 16 (r / 8) + r % 8 and 8 further on; 16-byte chunks are swizzled by the row's low 3 bits
-          const uint32_t at = (r / 8 * 16 + r % 8) * 128 + (((lane >> 2) ^ (r % 8)) << 4) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(dst + at) = hi;
-          *reinterpret_cast<uint32_t*>(dst + 8 * 128 + at) = lo;
-          if (lane == 0) sh.qs[buf][r] = exp2_int(e2) * a.c;
-        }
-      }
+      constexpr int kAtOnce = kR < 16 ? kR : 16;
+      for (int rb = 0; rb < kR; rb += kAtOnce) make_q<kAtOnce>(a, sQ + buf * C::op, sh.qs[buf], x.b, g, r0, rb);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+      if (lane == 0) mbar_arrive_n(&sh.q_full[buf], C::workers);
       t += x.left;
-      if (t < n) x.next(pre, a, n - t);
     }
   } else if (n > 0 && warp < C::workers) {
     const int wg = warp >> 2, quarter = warp & 3;
@@ -534,6 +537,14 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     };
     Walk x;
     x.begin(pre, a, t_lo, n);
+    {
+      // the first item's Q', two rows a warp
+      const int g0 = x.gc / a.chunks;
+      make_q<2>(a, sQ, sh.qs[0], x.b, g0, (x.gc - g0 * a.chunks) * kR, warp * 2);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[0]);
+    }
     look_up(0);
     int item = 0, i = 0, steps = 0, len = 0, g = 0, r0 = 0, toks_r0 = -1;
     uint32_t toks = 0;

@@ -36,6 +36,9 @@ __device__ __forceinline__ void fence_mbar_init() {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
                : "memory");
@@ -142,15 +145,24 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem] over 8-bit operands (K = 32 elements a step);
-// issued by one thread.
-__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// D[tmem] = A[smem] * B[smem] over 128 elements of 8-bit operands, as four K =
+// 32 products in one asm block (descriptors advanced by kA and kB 16-byte
+// units: formed apart from the products, each product took 120 to 200 cycles
+// to issue); issued by one thread.
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void umma_f8_x4(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred f, t;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 f, %3, %3;\n\t"
+      "setp.eq.b32 t, %3, %3;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 a, %1, %4;\n\tadd.s64 b, %2, %5;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 2 * %4;\n\tadd.s64 b, %2, 2 * %5;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+      "add.s64 a, %1, 3 * %4;\n\tadd.s64 b, %2, 3 * %5;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t}\n" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "n"(kA), "n"(kB)
       : "memory");
 }
 // Arrives once on *bar when every tcgen05 operation previously issued by this
