@@ -53,7 +53,7 @@ template <int kWG>
 struct Cfg {
   static constexpr int rows = kWG * kWgRows;
   static constexpr int workers = kWG * 4;                   // softmax warps
-  static constexpr int threads = (workers + 3) * 32;
+  static constexpr int threads = (workers + 4) * 32;
   static constexpr int per_sm = kWG == 1 ? 2 : 1;
   static constexpr int k_slots = kWG == 1 ? 3 : 5;
   static constexpr int v_slots = kWG == 1 ? 3 : 5;
@@ -71,10 +71,10 @@ template <int kWG>
 struct Shared {
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], v_start, drain;
   uint32_t tmem_base;
   int abort;
-  int warp_sum[kWG * 4 + 3];
+  int warp_sum[kWG * 4 + 4];
   alignas(16) float qs[2][kWG * kWgRows];           // q scale * scale * log2(e) per row
   alignas(16) float red[2][kWG][4][kWgRows];        // warps' row maxima
   float sum[kWG][4][kWgRows];                       // and, at an item's end, their row sums
@@ -116,15 +116,26 @@ __device__ __forceinline__ int clamped_len(const Args& a, int b, bool& bad) {
   return min(max(n, 0), cap);
 }
 
-// The CTAs that share `total` tiles: every one of them gets a tile.
-__device__ __forceinline__ int sharing(long long total, int ctas) {
-  return static_cast<int>(total < ctas ? total : ctas);
-}
-// First tile of run c of `runs`, and the run that holds tile t.
-__device__ __forceinline__ long long run_begin(long long total, int c, int runs) { return total * c / runs; }
-__device__ __forceinline__ int run_of(long long total, long long t, int runs) {
-  return static_cast<int>(((t + 1) * runs - 1) / total);
-}
+// `runs` CTAs share `total` tiles (every one of them gets one): run c begins at
+// floor(total c / runs).
+struct Shares {
+  int total, runs, each, rest;  // each = total / runs, rest = total % runs
+  __device__ __forceinline__ Shares(int total_, int ctas) {
+    total = total_;
+    runs = min(total, ctas);
+    each = runs > 0 ? total / runs : 0;
+    rest = total - each * runs;
+  }
+  __device__ __forceinline__ int begin(int c) const { return each * c + rest * c / runs; }  // rest, c < runs <= 304
+  // The run that holds tile t.
+  __device__ __forceinline__ int of(int t) const {
+    int c = static_cast<int>((static_cast<float>(t) + 0.5f) * static_cast<float>(runs) / static_cast<float>(total));
+    c = min(max(c, 0), runs - 1);
+    while (c > 0 && begin(c) > t) --c;
+    while (c + 1 < runs && begin(c + 1) <= t) ++c;
+    return c;
+  }
+};
 
 template <class T>
 __device__ __forceinline__ T bcast(T v, int lane) {
@@ -147,17 +158,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
 // many of the item's tiles the run still has from it on.
 struct Walk {
   int b, gc, page, pages, left;
-  __device__ __forceinline__ void begin(const int* pre, const Args& a, long long t, int n) {
+  __device__ __forceinline__ void begin(const int* pre, const Args& a, int t, int n) {
     const int hc = a.hkv * a.chunks;
     int lo = 0, hi = a.batch - 1;  // the last b with pre[b] * hc <= t that has pages: pre[b + 1] * hc > t
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (static_cast<long long>(pre[mid + 1]) * hc > t) hi = mid;
+      if (pre[mid + 1] * hc > t) hi = mid;
       else lo = mid + 1;
     }
     b = lo;
     pages = pre[lo + 1] - pre[lo];
-    const int rem = static_cast<int>(t - static_cast<long long>(pre[lo]) * hc);
+    const int rem = t - pre[lo] * hc;
     gc = rem / pages;
     page = rem - gc * pages;
     left = min(pages - page, n);
@@ -273,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const __grid_constant__ Args a) {
   using C = Cfg<kWG>;
-  constexpr int kR = C::rows, kTmaWarp = C::workers, kMmaWarp = C::workers + 1, kQWarp = C::workers + 2;
+  constexpr int kR = C::rows, kKWarp = C::workers, kVWarp = C::workers + 1, kMmaWarp = C::workers + 2, kQWarp = C::workers + 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = base;
@@ -301,6 +312,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       mbar_init(&sh.p_full[s], C::workers * 32);
       mbar_init(&sh.o_full[s], 1);
     }
+    mbar_init(&sh.v_start, 1);
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
@@ -308,10 +320,10 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     tmem_alloc(&sh.tmem_base, C::tmem);
     tmem_relinquish();
   }
-  if (warp == kTmaWarp && lane == 0) {
-    prefetch_tmap(&tk);
-    prefetch_tmap(&tv);
-  }
+  if (lane == 0 && (warp == kKWarp || warp == kVWarp)) prefetch_tmap(warp == kKWarp ? &tk : &tv);
+  // Each CTA asks for a line of the page table: what of it is used is known two reads from here.
+  if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) * 32 < a.batch * a.max_pages)
+    prefetch_l2(a.table + static_cast<int>(blockIdx.x) * 32);
   // From here on what earlier kernels of the stream wrote is read, and results are written.
   grid_dep_wait();
   // Pages before each sequence (an inclusive scan over the batch, a block of sequences at a time).
@@ -343,67 +355,65 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
   tc_fence_after();
   grid_dep_launch();
   const uint32_t tmem = sh.tmem_base;
-  const long long total = static_cast<long long>(before) * a.hkv * a.chunks;
-  const int runs = sharing(total, a.ctas), run = static_cast<int>(blockIdx.x);
-  const long long t_lo = run < runs ? run_begin(total, run, runs) : 0;
-  const int n = run < runs ? static_cast<int>(run_begin(total, run + 1, runs) - t_lo) : 0;
+  // (the host has seen to it that the tiles a full table holds are an int's worth)
+  const Shares shares(before * a.hkv * a.chunks, a.ctas);
+  const int run = static_cast<int>(blockIdx.x);
+  const int t_lo = run < shares.runs ? shares.begin(run) : 0;
+  const int n = run < shares.runs ? shares.begin(run + 1) - t_lo : 0;
 
-  if (n > 0 && warp == kTmaWarp) {
-    // Tiles by 32: each lane looks up one tile's page, lane 0 issues the
-    // copies: K(0) .. K(3), then V(i - 3) behind K(i), as the products take them.
-    constexpr int kLead = 2 * kStep - 1;
+  if (n > 0 && (warp == kKWarp || warp == kVWarp)) {
+    // The K pages, or the V pages, of the run in order: each lane looks up one of
+    // 32 tiles, lane 0 issues the copies.
+    const bool is_k = warp == kKWarp;
+    const CUtensorMap* map = is_k ? &tk : &tv;
+    uint8_t* slots = is_k ? sK : sV;
+    uint64_t *full = is_k ? sh.k_full : sh.v_full, *empty = is_k ? sh.k_empty : sh.v_empty;
+    const int count = is_k ? C::k_slots : C::v_slots;
+    constexpr int kFirst = kWG == 1 ? kStep : 2 * kStep;  // at most a K slot each
+    int slot = 0, phase = 1, issued = 0;
     bool go = true;
-    auto load = [&](uint8_t* slots, uint64_t* full, uint64_t* empty, int count, const CUtensorMap* map, int i, int z,
-                    int g) {
-      const int s = i % count;
-      if (!mbar_wait(&empty[s], ((i / count) & 1) ^ 1, &sh.abort)) {
-        fail(&sh.abort, a.status, 0x610);
-        go = false;
-        return;
+    if (!is_k && !warp_wait(&sh.v_start, 0, &sh.abort)) {
+      go = false;
+      if (lane == 0) fail(&sh.abort, a.status, 0x615);
+    }
+    for (int i0 = 0; go && i0 < n; i0 += 32) {
+      int z = -1, g = 0;
+      if (i0 + lane < n) {
+        Walk x;
+        x.begin(pre, a, t_lo + i0 + lane, n);
+        z = page_id(a, x.b, x.page);
+        g = a.chunks == 1 ? x.gc : x.gc / a.chunks;
+        if (z < 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x602);
       }
-      if (z >= 0) {
-        mbar_arrive_expect_tx(&full[s], kPage);
-        tma_load_4d(slots + s * kPage, map, &full[s], 0, 0, g, z);
-      } else {
-        mbar_arrive(&full[s]);  // a bad page id: nothing is copied, and the tile counts as empty
-      }
-    };
-    int kn = 0, vn = 0;                  // copies issued
-    int z = -1, g = 0, z_old = -1, g_old = 0;  // lanes' tiles of this window of 32 and of the one before
-    for (int i = 0; i < n + kLead; ++i) {
-      if ((i & 31) == 0) {
-        z_old = z;
-        g_old = g;
-        z = -1;
-        if (i + lane < n) {
-          Walk x;
-          x.begin(pre, a, t_lo + i + lane, n);
-          z = page_id(a, x.b, x.page);
-          g = x.gc / a.chunks;
-          if (z < 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x602);
+      const int m = min(32, n - i0);
+      for (int k = 0; k < m; ++k) {
+        const int zt = bcast(z, k), gt = bcast(g, k);
+        if (lane == 0 && go) {
+          go = mbar_wait(&empty[slot], phase, &sh.abort);
+          if (!go) {
+            fail(&sh.abort, a.status, 0x610);
+          } else if (zt >= 0) {
+            mbar_arrive_expect_tx(&full[slot], kPage);
+            tma_load_4d(slots + slot * kPage, map, &full[slot], 0, 0, gt, zt);
+          } else {
+            mbar_arrive(&full[slot]);  // a bad page id: nothing is copied, and the tile counts as empty
+          }
+          issued += go;
+          // the first scores' K pages go ahead of any V page
+          if (is_k && issued == min(kFirst, n)) mbar_arrive(&sh.v_start);
+          if (++slot == count) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-      const int v = i - kLead;  // the V tile of this turn
-      const bool same = v >= (i & ~31);
-      const int zk = bcast(z, i & 31), gk = bcast(g, i & 31);
-      const int zv = bcast(same ? z : z_old, v & 31), gv = bcast(same ? g : g_old, v & 31);
-      if (lane == 0 && go && i < n) {
-        load(sK, sh.k_full, sh.k_empty, C::k_slots, &tk, i, zk, gk);
-        kn += go;
-      }
-      if (lane == 0 && go && v >= 0) {
-        load(sV, sh.v_full, sh.v_empty, C::v_slots, &tv, v, zv, gv);
-        vn += go;
-      }
+      go = bcast(static_cast<int>(go), 0) != 0;
     }
     if (lane == 0) {
       // Every copy issued has landed before the CTA ends (bounded waits that
       // ignore the abort flag).
       const int never = 0;
-      for (int q = max(0, kn - C::k_slots); q < kn; ++q)
-        mbar_wait(&sh.k_full[q % C::k_slots], (q / C::k_slots) & 1, &never);
-      for (int q = max(0, vn - C::v_slots); q < vn; ++q)
-        mbar_wait(&sh.v_full[q % C::v_slots], (q / C::v_slots) & 1, &never);
+      for (int q = max(0, issued - count); q < issued; ++q) mbar_wait(&full[q % count], (q / count) & 1, &never);
     }
   } else if (n > 0 && warp == kMmaWarp) {
     if (lane == 0) {
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       const float wsum = warp_rows<kWgRows, false>(l);
       if ((lane & 3) == 0) sh.sum[wg][quarter][lane >> 2] = wsum;
       named_bar_sync(bar, 128);
-      const long long t_item = t_lo + i_end - of.end;  // the item's first tile
+      const int t_item = t_lo + i_end - of.end;  // the item's first tile
       const bool whole = t_item >= t_lo && of.end == of.pages;
       const int slot = 2 * run + (t_item < t_lo ? 0 : 1);
       const int nr = min(kWgRows, a.rows - of.r0);
@@ -643,7 +653,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       if (i_end == n && threadIdx.x == 0) {
         // an item that begins here and goes on is joined under this CTA's number
         const bool goes_on = t_item >= t_lo && of.end < of.pages;
-        a.split[run] = Split{goes_on ? of.b : -1, of.gc, run_of(total, t_item + of.pages - 1, runs), 0};
+        a.split[run] = Split{goes_on ? of.b : -1, of.gc, shares.of(t_item + of.pages - 1), 0};
       }
     };
 

@@ -92,6 +92,11 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Asks for the L2 line of p (no data is taken from it).
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // ------------------------------------------------- programmatic dependent launch
 // Lets the next kernel of the stream, when launched as a dependent, be
 // scheduled before this one ends; that kernel reads nothing of this one's
