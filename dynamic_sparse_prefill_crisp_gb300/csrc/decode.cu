@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     uint8_t* slots = is_k ? sK : sV;
     uint64_t *full = is_k ? sh.k_full : sh.v_full, *empty = is_k ? sh.k_empty : sh.v_empty;
     const int count = is_k ? C::k_slots : C::v_slots;
+    // Scores are read back by weights_kernel: the pages, which are not, leave L2 first.
+    const uint64_t policy = kScores ? policy_evict_first() : 0;
     constexpr int kFirst = kWG == 1 ? kStep : 2 * kStep;  // at most a K slot each
     int slot = 0, phase = 1, issued = 0;
     bool go = true;
@@ -394,7 +396,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
             fail(&sh.abort, a.status, 0x610);
           } else if (zt >= 0) {
             mbar_arrive_expect_tx(&full[slot], kPage);
-            tma_load_4d(slots + slot * kPage, map, &full[slot], 0, 0, gt, zt);
+            if (kScores) tma_load_4d_hint(slots + slot * kPage, map, &full[slot], 0, 0, gt, zt, policy);
+            else tma_load_4d(slots + slot * kPage, map, &full[slot], 0, 0, gt, zt);
           } else {
             mbar_arrive(&full[slot]);  // a bad page id: nothing is copied, and the tile counts as empty
           }
