@@ -952,11 +952,6 @@ crisp_status make_page_map(CUtensorMap* m, const void* ptr, const crisp_kv_cache
   return r == CUDA_SUCCESS ? CRISP_OK : CRISP_ERR_ALIGN;
 }
 
-size_t evict_list_offset() { return align_up(sizeof(DevStatus)); }
-size_t evict_bytes(const crisp_kv_cache& c, int keep) {
-  return align_up(evict_list_offset() + static_cast<size_t>(c.batch) * c.hkv * align_up(static_cast<size_t>(keep) * 4));
-}
-
 }  // namespace
 }  // namespace crisp
 
@@ -988,7 +983,7 @@ crisp_status crisp_kv_evict_workspace_size(const crisp_kv_cache* cache, int32_t 
     crisp_status st = check_cache(cache);
     if (st != CRISP_OK) return st;
     if (!bytes || keep < 1 || keep > kMaxSeq) return CRISP_ERR_INVALID_ARG;
-    *bytes = evict_bytes(*cache, keep);
+    *bytes = evict_layout(*cache, keep).total;
     return CRISP_OK;
   });
 }
@@ -1049,13 +1044,11 @@ crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst
     if (!weights || weights == new_weights) return CRISP_ERR_INVALID_ARG;
     if (src->table == dst->table || src->lens == dst->lens) return CRISP_ERR_INVALID_ARG;  // written while read
     if (!aligned16(weights) || !aligned16(new_weights) || !aligned(kept, 4)) return CRISP_ERR_ALIGN;
-    if ((st = check_cache_ws(ws, ws_bytes, evict_bytes(*src, keep))) != CRISP_OK) return st;
+    if ((st = check_cache_ws(ws, ws_bytes, evict_layout(*src, keep).total)) != CRISP_OK) return st;
     int sms = 0;
     if ((st = check_device(&sms)) != CRISP_OK) return st;
-    auto* list = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + evict_list_offset());
-    const int64_t stride = static_cast<int64_t>(align_up(static_cast<size_t>(keep) * 4) / 4);
-    return from_cuda(launch_kv_evict(*src, *dst, weights, keep, sink, recent, new_weights, kept, list, stride,
-                                     status_of(ws), sms, stream));
+    return from_cuda(launch_kv_evict(*src, *dst, weights, keep, sink, recent, new_weights, kept,
+                                     static_cast<char*>(ws), sms, stream));
   });
 }
 

@@ -137,6 +137,15 @@ struct DecodeLayout {
   size_t scores;   // fp32 [batch][hkv][rows][128 max_pages]  scores in base 2 (weights only)
   size_t total;
 };
+// Workspace of crisp_kv_evict (the status word comes first).
+struct EvictLayout {
+  size_t list;         // int32 [batch][hkv][list_stride]  where the kept tokens' codes are (page * 128 + row)
+  size_t list_stride;  // entries
+  size_t hist, state;  // long caches: the chunks' histograms, and what their CTAs know
+  size_t total;
+};
+EvictLayout evict_layout(const crisp_kv_cache& src, int keep);
+
 DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights);
 int decode_row_chunks(int rows);  // row chunks of a (sequence, kv head)
 
@@ -190,9 +199,8 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
                           char* ws, int sms, cudaStream_t st);
 cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
                              const int32_t* new_lens, DevStatus* status, cudaStream_t st);
-// list: int32 [batch][hkv][list_stride], where the kept tokens' codes are (page * 128 + row)
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
-                            int sink, int recent, float* new_weights, int32_t* kept, int32_t* list,
-                            int64_t list_stride, DevStatus* status, int sms, cudaStream_t st);
+                            int sink, int recent, float* new_weights, int32_t* kept, char* ws, int sms,
+                            cudaStream_t st);
 
 }  // namespace crisp

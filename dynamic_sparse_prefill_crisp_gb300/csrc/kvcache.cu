@@ -6,15 +6,14 @@
 // page of one head per CTA: 8 threads hold a row (16 codes each), 32 rows at a
 // time, the whole page in registers between its maximum and its codes, so
 // every value is read once. They are bound by HBM.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
 
 namespace crisp {
 using namespace ptx;
-namespace cg = cooperative_groups;
 
 namespace {
 
@@ -222,35 +221,89 @@ __global__ void __launch_bounds__(kThreads, 4)
 // number), tokens that always stay above all. The keep-th largest key is found
 // digit by digit from the top (11 + 11 + 10 bits): a histogram of the keys that
 // match the digits found so far, then the digit in which the keep-th falls. A
-// last pass writes the kept positions in order. The keys are read four times,
-// from L2 after the first; a long sequence takes a cluster of 16 CTAs with a
-// contiguous part each, which read each other's histograms through
-// distributed shared memory (512k tokens: one CTA would read 2 MB a pass).
+// last pass writes the kept positions in order.
+//
+// A cache of up to kChunk positions takes one CTA per sequence and kv head and
+// one launch (2175 tokens: 5.7 us, of it 3 in barriers and scans; the keys stay
+// in registers up to 8192). A longer one is cut into chunks of kChunk, a CTA
+// each and a launch per pass, so that a few long rows fill the chip: every
+// chunk's histogram goes to the workspace, and every CTA of the next pass adds
+// up its row's (3.5 us for 32 chunks). 8 rows of 512k tokens take 39 us this
+// way, 48 with a cluster of 16 CTAs per row (8 such clusters fill half the SMs).
 constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kClusterLen = 16384;  // capacities from which a cluster is used
-constexpr int kCluster = 16;
-constexpr int kAhead = 4;           // loads of four keys a thread has in flight
+constexpr int kPer = kBins / kSelThreads;  // bins of a thread
+constexpr int kAhead = 4;                  // loads of four keys a thread has in flight
+constexpr int kTurn = kSelThreads * 4;     // positions the block takes with one load a thread
+constexpr int kChunk = 2 * kAhead * kTurn;
+__host__ __device__ constexpr int digit_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+__host__ __device__ constexpr uint32_t digit_mask(int pass) { return pass == 2 ? 1023u : 2047u; }
+
+// What a chunk's CTA knows: the digits found, how many of the keys that match
+// them are still wanted, and how many keys above stand in earlier chunks.
+struct SelState {
+  uint32_t found;
+  int want, before, pad;
+};
+
+struct SelArgs {
+  const float* weights;
+  const int32_t* lens;
+  int32_t* new_lens;
+  const int32_t* table;
+  float* new_weights;   // or null
+  int32_t* kept;        // or null
+  int32_t* list;
+  int64_t new_cap, list_stride;
+  int hkv, cap, keep, sink, recent, num_pages;
+  uint16_t* hist;       // [2][batch hkv][chunks][kBins]  (long caches)
+  SelState* state;      // [batch hkv][chunks]
+  int chunks, rows;     // rows: batch hkv
+  DevStatus* status;
+};
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   // + 0 makes one zero of both and one NaN of all (0x7fffffff)
   const int u = __float_as_int(w + 0.f);
   return min(static_cast<uint32_t>(u ^ (u >> 31 | INT32_MIN)), 0xfffffffeu);
 }
-// Keys of the four weights from position i on; those at or past n do not count
-// (0, which is no weight's key).
-__device__ __forceinline__ void weight_keys(const float4& w, int i, int sink, int tail, int n, uint32_t (&key)[4]) {
-  key[0] = weight_key(w.x);
-  key[1] = weight_key(w.y);
-  key[2] = weight_key(w.z);
-  key[3] = weight_key(w.w);
-  if (i < sink || i + 4 > tail) {
+
+// One sequence and kv head.
+struct SelRow {
+  int n, sink, tail;
+  const float* w;
+  const int32_t* pages;
+  __device__ __forceinline__ SelRow(const SelArgs& a, int b, int bg) {
+    n = min(max(a.lens[b], 0), a.cap);
+    sink = a.sink;
+    tail = n - a.recent;
+    w = a.weights + static_cast<int64_t>(bg) * a.cap;
+    pages = a.table + static_cast<int64_t>(b) * (a.cap / kB);
+  }
+  // rows are 512-byte aligned and cap is a multiple of 128: whole groups of four are there
+  __device__ __forceinline__ float4 load4(int i) const { return *reinterpret_cast<const float4*>(w + i); }
+  // Keys of the four weights from position i on; those at or past n do not
+  // count (0, which is no weight's key).
+  __device__ __forceinline__ void keys(const float4& x, int i, uint32_t (&key)[4]) const {
+    key[0] = weight_key(x.x);
+    key[1] = weight_key(x.y);
+    key[2] = weight_key(x.z);
+    key[3] = weight_key(x.w);
+    if (i < sink || i + 4 > tail) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (i + e < sink || i + e >= tail) key[e] = 0xffffffffu;
-      if (i + e >= n) key[e] = 0u;
+      for (int e = 0; e < 4; ++e) {
+        if (i + e < sink || i + e >= tail) key[e] = 0xffffffffu;
+        if (i + e >= n) key[e] = 0u;
+      }
     }
   }
+};
+
+// Position i is kept in place `at`: where its codes are (-1: on no page), and what it carries along.
+__device__ __forceinline__ void emit(const SelArgs& a, int bg, int at, int i, int id, float weight) {
+  a.list[bg * a.list_stride + at] = id >= 0 && id < a.num_pages ? id * kB + i % kB : -1;
+  if (a.kept != nullptr) a.kept[bg * a.new_cap + at] = i;
+  if (a.new_weights != nullptr) a.new_weights[bg * a.new_cap + at] = weight;
 }
 
 // Inclusive scan over the block of one value a thread; returns it and the total.
@@ -275,168 +328,85 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int& total) {
   return v + before;
 }
 
-template <int kC>
-__global__ void __launch_bounds__(kSelThreads, 2)
-    select_kernel(const float* weights, const int32_t* lens, int32_t* new_lens, int hkv, int cap, int keep, int sink,
-                  int recent, const int32_t* table, int num_pages, float* new_weights, int64_t new_cap, int32_t* kept,
-                  int64_t kept_stride, int32_t* list, int64_t list_stride, DevStatus* status) {
-  __shared__ alignas(8) int hist[2][kBins];
-  __shared__ int bin_total[2][kC > 1 ? kBins / kC : 1];
-  __shared__ int warp_tot[kSelThreads / 32];
-  __shared__ int digit, above_digit;
-  __shared__ alignas(8) int tot[2][kAhead * kSelThreads / 32];
-  __shared__ int own[2];  // this CTA's keys above the threshold, and equal to it
-  grid_dep_launch();
-  grid_dep_wait();
-  const int tid = threadIdx.x;
-  const int part = kC > 1 ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
-  const int bg = blockIdx.x / kC, b = bg / hkv;
-  int n = lens[b];
-  if (bg % hkv == 0 && part == 0 && tid == 0) {
-    if (n < 0 || n > cap) report_error(status, CRISP_ERR_BOUNDS, 0x711);
-    new_lens[b] = min(min(max(n, 0), cap), keep);
-  }
-  n = min(max(n, 0), cap);
-  const float* w = weights + static_cast<int64_t>(bg) * cap;
-  int32_t* dst = list + bg * list_stride;
-  float* dst_w = new_weights != nullptr ? new_weights + bg * new_cap : nullptr;
-  int32_t* dst_pos = kept != nullptr ? kept + bg * kept_stride : nullptr;
-  const int32_t* pages = table + static_cast<int64_t>(b) * (cap / kB);
-  // Position i is kept in place `at`: where its codes are (-1: on no page), and what it carries along.
-  auto emit = [&](int at, int i, int id, float weight) {
-    dst[at] = id >= 0 && id < num_pages ? id * kB + i % kB : -1;
-    if (dst_pos) dst_pos[at] = i;
-    if (dst_w) dst_w[at] = weight;
-  };
-  // this CTA's part of the positions, whole groups of four
-  const int quads = (n + 3) / 4;
-  const int lo = static_cast<int>(static_cast<int64_t>(quads) * part / kC) * 4;
-  const int hi = min(static_cast<int>(static_cast<int64_t>(quads) * (part + 1) / kC) * 4, n);
-  if (n <= keep) {  // uniform over the cluster
-    for (int i = lo + tid; i < hi; i += kSelThreads) emit(i, i, pages[i / kB], w[i]);
-    return;
-  }
-  const int tail = n - recent;
-  // rows are 512-byte aligned and cap is a multiple of 128: whole groups of four are there
-  auto load4 = [&](int i) { return *reinterpret_cast<const float4*>(w + i); };
+struct SelShared {
+  alignas(8) int hist[2][kBins];  // (and, in the last pass, a turn's kept positions)
+  alignas(8) int tot[2][kAhead * kSelThreads / 32];
+  int warp_tot[kSelThreads / 32];
+  int digit, above, equal_before;
+};
 
-  constexpr int kTurn = kSelThreads * 4;  // positions the block takes with one load a thread
-  float4 v[kAhead];                       // a part of one turn is read once
-  auto load_first = [&]() {
+// The first turn's keys of [lo, hi).
+__device__ __forceinline__ void load_first(const SelRow& r, int lo, int hi, float4 (&v)[kAhead]) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (lo + u * kTurn + tid * 4 < hi) v[u] = load4(lo + u * kTurn + tid * 4);
-  };
+  for (int u = 0; u < kAhead; ++u) {
+    const int i = lo + u * kTurn + static_cast<int>(threadIdx.x) * 4;
+    if (i < hi) v[u] = r.load4(i);
+  }
+}
 
-  uint32_t found = 0;   // the digits found, in place
-  int want = keep;      // the threshold is the want-th largest of the keys that match them
-  int above_own = 0;    // this CTA's keys above (this thread's part)
-  constexpr int kShift[3] = {21, 10, 0};
-  constexpr uint32_t kMask[3] = {2047u, 2047u, 1023u};
+// Adds the keys of [lo, hi) that match `found` above digit `pass` to the
+// histogram h of that digit; v: the first turn's. Ends with a barrier.
+template <int pass>
+__device__ __forceinline__ void count(const SelRow& r, int lo, int hi, uint32_t found, int* h, float4 (&v)[kAhead]) {
+  for (int x = threadIdx.x; x < kBins; x += kSelThreads) h[x] = 0;
+  __syncthreads();
+  constexpr uint32_t fixed = pass == 0 ? 0u : ~0u << digit_shift(pass - 1);
+  for (int i0 = lo + static_cast<int>(threadIdx.x) * 4; i0 < hi; i0 += kTurn * kAhead) {
 #pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    int* h = hist[pass & 1];
-    for (int x = tid; x < kBins; x += kSelThreads) h[x] = 0;
-    __syncthreads();
-    const uint32_t fixed = pass == 0 ? 0u : ~0u << kShift[pass - 1];
-    if (pass == 0 || hi - lo > kTurn * kAhead) load_first();
-    for (int i0 = lo + tid * 4; i0 < hi; i0 += kTurn * kAhead) {
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * kTurn;
+      if (i >= hi) break;
+      uint32_t key[4];
+      r.keys(v[u], i, key);
+      if (i + kTurn * kAhead < hi) v[u] = r.load4(i + kTurn * kAhead);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u * kTurn;
-        if (i >= hi) break;
-        uint32_t key[4];
-        weight_keys(v[u], i, sink, tail, n, key);
-        if (i + kTurn * kAhead < hi) v[u] = load4(i + kTurn * kAhead);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // a key of 0 counts only in the first pass, in bin 0, where no weight's key falls (-inf is in bin 3)
-          if (pass == 0 || ((key[e] ^ found) & fixed) == 0u)
-            atomicAdd(&h[pass == 0 ? key[e] >> kShift[0] : (key[e] >> kShift[pass]) & kMask[pass]], 1);
-        }
-      }
-    }
-    if (kC > 1) cg::this_cluster().sync();
-    else __syncthreads();
-    // thread t takes kPer bins of the whole sequence, the largest first
-    constexpr int kPer = kBins / kSelThreads;
-    const int top = kBins - 1 - kPer * tid;
-    int c[kPer], sum = 0;
-    if constexpr (kC > 1) {
-      // CTA r adds up bins r * kOwn .. of all CTAs; everyone then reads the sums
-      // from their owners (reading every CTA's whole histogram instead made
-      // all CTAs queue at one after the other: 40 us a pass against 3)
-      constexpr int kOwn = kBins / kC, kSplit = kSelThreads / kOwn;
-      int* total = bin_total[pass & 1];
-      if (tid < kOwn) total[tid] = 0;
-      __syncthreads();
-      int part_sum = 0;
-#pragma unroll
-      for (int u = 0; u < kC / kSplit; ++u)
-        part_sum += cg::this_cluster().map_shared_rank(h, tid / kOwn * (kC / kSplit) + u)[part * kOwn + tid % kOwn];
-      if (part_sum) atomicAdd(&total[tid % kOwn], part_sum);
-      cg::this_cluster().sync();
-#pragma unroll
-      for (int u = 0; u < kPer; ++u)
-        c[u] = cg::this_cluster().map_shared_rank(total, (top - u) / kOwn)[(top - u) % kOwn];
-    } else {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) c[u] = h[top - u];
-    }
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) sum += c[u];
-    int all;
-    const int incl = block_scan(sum, warp_tot, all);
-    int before = incl - sum;
-    if (before < want && want <= incl) {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        if (before < want && want <= before + c[u]) {
-          digit = top - u;
-          above_digit = before;
-        }
-        before += c[u];
-      }
-    }
-    __syncthreads();
-    const int d = digit;
-    want -= above_digit;
-    found |= static_cast<uint32_t>(d) << kShift[pass];
-    // this CTA's own keys above the digit
-    int mine = 0;
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) mine += top - u > d ? h[top - u] : 0;
-    above_own += mine;
-    if (kC > 1 && pass == 2) {
-      int own_above;
-      block_scan(above_own, warp_tot, own_above);
-      if (tid == 0) {
-        own[0] = own_above;
-        own[1] = h[d];
+      for (int e = 0; e < 4; ++e) {
+        // a key of 0 counts only in the first pass, in bin 0, where no weight's key falls (-inf is in bin 3)
+        if (pass == 0 || ((key[e] ^ found) & fixed) == 0u)
+          atomicAdd(&h[(key[e] >> digit_shift(pass)) & digit_mask(pass)], 1);
       }
     }
   }
-  // Kept before this CTA's part: all keys above the threshold `found`, and the
-  // first `want` equal to it.
-  int gt = 0, eq = 0;
-  if (kC > 1) {
-    cg::this_cluster().sync();
-    if ((tid & 31) < part) {
-      const int* o = cg::this_cluster().map_shared_rank(own, tid & 31);
-      gt = o[0];
-      eq = o[1];
+  __syncthreads();
+}
+
+// The digit in which the want-th largest key falls; c: this thread's kPer bins
+// of the row's histogram, the largest (kBins - 1 - kPer * thread) first.
+__device__ __forceinline__ void pick(SelShared& sh, const int (&c)[kPer], int pass, uint32_t& found, int& want) {
+  const int top = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
+  int sum = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) sum += c[u];
+  int all;
+  const int incl = block_scan(sum, sh.warp_tot, all);
+  int before = incl - sum;
+  if (before < want && want <= incl) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      if (before < want && want <= before + c[u]) {
+        sh.digit = top - u;
+        sh.above = before;
+      }
+      before += c[u];
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    cg::this_cluster().sync();  // nobody's shared memory goes away while it is read
   }
-  // A turn's kept positions are first put in order in shared memory (where the
-  // histograms were), then written out by neighbouring threads.
+  __syncthreads();
+  want -= sh.above;
+  found |= static_cast<uint32_t>(sh.digit) << digit_shift(pass);
+}
+
+// Writes the kept positions of [lo, hi): keys above `found`, and those equal to
+// it while fewer than `want` of them came before; gt, eq: the row's keys above
+// and equal before lo; v: the first turn's keys. A turn's kept positions are
+// first put in order in shared memory (where the histograms were), then
+// written out by neighbouring threads.
+__device__ __forceinline__ void write_kept(const SelArgs& a, const SelRow& r, SelShared& sh, int bg, int lo, int hi,
+                                           uint32_t found, int want, int gt, int eq, float4 (&v)[kAhead]) {
   constexpr int kWarps = kSelThreads / 32;
-  const int warp = tid >> 5, lane = tid & 31;
-  static_assert(sizeof(hist) >= 2 * kTurn * kAhead, "a turn's offsets fit the histograms");
-  uint16_t* order = reinterpret_cast<uint16_t*>(hist);
-  if (hi - lo > kTurn * kAhead) load_first();
+  static_assert(sizeof(sh.hist) >= 2 * kTurn * kAhead, "a turn's offsets fit the histograms");
+  static_assert(kAhead * kWarps == 64, "two totals a lane");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint16_t* order = reinterpret_cast<uint16_t*>(sh.hist);
   for (int i0 = lo, turn = 0; i0 < hi; i0 += kTurn * kAhead, ++turn) {
     // counts before this thread: keys above in the high half, equal in the low
     // (at most 8192 of either in a turn)
@@ -448,8 +418,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       int mine = 0;
       if (i < hi) {
         uint32_t key[4];
-        weight_keys(v[u], i, sink, tail, n, key);
-        if (i + kTurn * kAhead < hi) v[u] = load4(i + kTurn * kAhead);
+        r.keys(v[u], i, key);
+        if (i + kTurn * kAhead < hi) v[u] = r.load4(i + kTurn * kAhead);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           above |= (key[e] > found ? 1u : 0u) << (4 * u + e);
@@ -464,12 +434,11 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         if (lane >= o) incl += x;
       }
       before[u] = incl - mine;
-      if (lane == 31) tot[turn & 1][u * kWarps + warp] = incl;
+      if (lane == 31) sh.tot[turn & 1][u * kWarps + warp] = incl;
     }
     __syncthreads();
     // the kAhead * kWarps totals in order, two a lane
-    static_assert(kAhead * kWarps == 64, "two totals a lane");
-    const int2 pair = *reinterpret_cast<const int2*>(&tot[turn & 1][2 * lane]);
+    const int2 pair = *reinterpret_cast<const int2*>(&sh.tot[turn & 1][2 * lane]);
     int incl = pair.x + pair.y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -486,30 +455,149 @@ __global__ void __launch_bounds__(kSelThreads, 2)
       int g1 = gt + (base >> 16) - begin, e1 = eq + (base & 0xffff);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool a = above >> (4 * u + e) & 1u, t = tie >> (4 * u + e) & 1u;
-        if (a || (t && e1 < want)) order[g1 + min(e1, want)] = static_cast<uint16_t>(u * kTurn + tid * 4 + e);
-        g1 += a;
-        e1 += t;
+        const bool is_above = above >> (4 * u + e) & 1u, is_tie = tie >> (4 * u + e) & 1u;
+        if (is_above || (is_tie && e1 < want))
+          order[g1 + min(e1, want)] = static_cast<uint16_t>(u * kTurn + tid * 4 + e);
+        g1 += is_above;
+        e1 += is_tie;
       }
     }
     gt += all >> 16;
     eq += all & 0xffff;
-    const int count = gt + min(eq, want) - begin;
+    const int total = gt + min(eq, want) - begin;
     __syncthreads();
-    for (int j0 = tid; j0 < count; j0 += kSelThreads * 4) {
+    for (int j0 = tid; j0 < total; j0 += kSelThreads * 4) {
       int i[4], id[4];
       float f[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        i[u] = j0 + u * kSelThreads < count ? i0 + order[j0 + u * kSelThreads] : i0;
-        id[u] = pages[i[u] / kB];
-        f[u] = dst_w ? w[i[u]] : 0.f;
+        i[u] = j0 + u * kSelThreads < total ? i0 + order[j0 + u * kSelThreads] : i0;
+        id[u] = r.pages[i[u] / kB];
+        f[u] = a.new_weights != nullptr ? r.w[i[u]] : 0.f;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (j0 + u * kSelThreads < count) emit(begin + j0 + u * kSelThreads, i[u], id[u], f[u]);
+        if (j0 + u * kSelThreads < total) emit(a, bg, begin + j0 + u * kSelThreads, i[u], id[u], f[u]);
     }
   }
+}
+
+__device__ __forceinline__ void write_len(const SelArgs& a, int b) {
+  const int n = a.lens[b];
+  if (n < 0 || n > a.cap) report_error(a.status, CRISP_ERR_BOUNDS, 0x711);
+  a.new_lens[b] = min(min(max(n, 0), a.cap), a.keep);
+}
+
+// All passes of a row in one CTA.
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ SelShared sh;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int tid = threadIdx.x, bg = blockIdx.x, b = bg / a.hkv;
+  if (bg % a.hkv == 0 && tid == 0) write_len(a, b);
+  const SelRow r(a, b, bg);
+  if (r.n <= a.keep) {
+    for (int i = tid; i < r.n; i += kSelThreads) emit(a, bg, i, i, r.pages[i / kB], r.w[i]);
+    return;
+  }
+  float4 v[kAhead];
+  const bool once = r.n <= kTurn * kAhead;  // one turn: its keys stay in registers
+  uint32_t found = 0;
+  int want = a.keep;
+  const int top = kBins - 1 - kPer * tid;
+  int c[kPer];
+  auto pass = [&](auto which) {
+    constexpr int p = decltype(which)::value;
+    if (p == 0 || !once) load_first(r, 0, r.n, v);
+    count<p>(r, 0, r.n, found, sh.hist[p & 1], v);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) c[u] = sh.hist[p & 1][top - u];
+    pick(sh, c, p, found, want);
+  };
+  pass(std::integral_constant<int, 0>());
+  pass(std::integral_constant<int, 1>());
+  pass(std::integral_constant<int, 2>());
+  if (!once) load_first(r, 0, r.n, v);
+  write_kept(a, r, sh, bg, 0, r.n, found, want, 0, 0, v);
+}
+
+// From the histograms of digit `pass` of all chunks of a row: the digit, and
+// how many keys above it (and equal to it, in sh.equal_before) stand before `chunk`.
+__device__ __forceinline__ void digest(const SelArgs& a, SelShared& sh, int bg, int n, int chunk, int pass,
+                                       SelState& st) {
+  const int tid = threadIdx.x, top = kBins - 1 - kPer * tid, chunks = (n + kChunk - 1) / kChunk;
+  const uint16_t* h = a.hist + (static_cast<int64_t>((pass & 1) * a.rows + bg) * a.chunks) * kBins + top - (kPer - 1);
+  int c[kPer] = {0, 0, 0, 0}, before[kPer] = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int x = 0; x < chunks; ++x) {
+    const uint2 q = *reinterpret_cast<const uint2*>(h + static_cast<int64_t>(x) * kBins);
+    const int y[kPer] = {static_cast<int>(q.y >> 16), static_cast<int>(q.y & 0xffffu), static_cast<int>(q.x >> 16),
+                         static_cast<int>(q.x & 0xffffu)};
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      c[u] += y[u];
+      before[u] += x < chunk ? y[u] : 0;
+    }
+  }
+  pick(sh, c, pass, st.found, st.want);
+  int mine = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    if (top - u > sh.digit) mine += before[u];
+    if (top - u == sh.digit) sh.equal_before = before[u];
+  }
+  int sum;
+  block_scan(mine, sh.warp_tot, sum);
+  st.before += sum;
+}
+
+// Digit `pass` of one chunk.
+template <int pass>
+__global__ void __launch_bounds__(kSelThreads, 2) chunk_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ SelShared sh;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
+  const SelRow r(a, b, bg);
+  const int lo = chunk * kChunk, hi = min(lo + kChunk, r.n);
+  if (r.n <= a.keep || lo >= r.n) return;
+  float4 v[kAhead];
+  load_first(r, lo, hi, v);
+  SelState st{0u, a.keep, 0, 0};
+  if (pass > 0) {
+    SelState* keep = a.state + static_cast<int64_t>(bg) * a.chunks + chunk;
+    if (pass > 1) st = *keep;
+    __syncthreads();  // all have read it
+    digest(a, sh, bg, r.n, chunk, pass - 1, st);
+    if (threadIdx.x == 0) *keep = st;
+  }
+  count<pass>(r, lo, hi, st.found, sh.hist[0], v);
+  uint16_t* out = a.hist + (static_cast<int64_t>((pass & 1) * a.rows + bg) * a.chunks + chunk) * kBins;
+  const int4 x = *reinterpret_cast<const int4*>(&sh.hist[0][kPer * threadIdx.x]);
+  *reinterpret_cast<uint2*>(out + kPer * threadIdx.x) =
+      make_uint2(static_cast<uint32_t>(x.x) | static_cast<uint32_t>(x.y) << 16,
+                 static_cast<uint32_t>(x.z) | static_cast<uint32_t>(x.w) << 16);
+}
+
+// The kept positions of one chunk.
+__global__ void __launch_bounds__(kSelThreads, 2) chunk_kept_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ SelShared sh;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
+  if (chunk == 0 && blockIdx.y == 0 && threadIdx.x == 0) write_len(a, b);
+  const SelRow r(a, b, bg);
+  const int lo = chunk * kChunk, hi = min(lo + kChunk, r.n);
+  if (r.n <= a.keep) {
+    for (int i = lo + threadIdx.x; i < hi; i += kSelThreads) emit(a, bg, i, i, r.pages[i / kB], r.w[i]);
+    return;
+  }
+  if (lo >= r.n) return;
+  float4 v[kAhead];
+  load_first(r, lo, hi, v);
+  SelState st = a.state[static_cast<int64_t>(bg) * a.chunks + chunk];
+  digest(a, sh, bg, r.n, chunk, 2, st);
+  write_kept(a, r, sh, bg, lo, hi, st.found, st.want, st.before, sh.equal_before, v);
 }
 
 // Asynchronous copies of 16 or 4 bytes to shared memory; nothing is read and
@@ -658,43 +746,64 @@ cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new,
                           status);
 }
 
+EvictLayout evict_layout(const crisp_kv_cache& src, int keep) {
+  const size_t rows = static_cast<size_t>(src.batch) * src.hkv;
+  const size_t chunks = src.max_pages * kB > kChunk ? (src.max_pages * kB + kChunk - 1) / kChunk : 0;
+  EvictLayout L{};
+  size_t o = align_up(sizeof(DevStatus));
+  L.list_stride = align_up(static_cast<size_t>(keep) * 4) / 4;
+  L.list = o;  o = align_up(o + rows * L.list_stride * 4);
+  L.hist = o;  o = align_up(o + 2 * rows * chunks * kBins * sizeof(uint16_t));
+  L.state = o; o = align_up(o + rows * chunks * sizeof(SelState));
+  L.total = o;
+  return L;
+}
+
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
-                            int sink, int recent, float* new_weights, int32_t* kept, int32_t* list,
-                            int64_t list_stride, DevStatus* status, int sms, cudaStream_t st) {
-  const int cap = src.max_pages * kB;
-  const int64_t new_cap = static_cast<int64_t>(dst.max_pages) * kB;
-  const bool wide = cap >= kClusterLen;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attrs[2] = {};
-  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attrs[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.stream = st;
-  cfg.attrs = attrs;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>(src.batch * src.hkv * (wide ? kCluster : 1)));
+                            int sink, int recent, float* new_weights, int32_t* kept, char* ws, int sms,
+                            cudaStream_t st) {
+  const EvictLayout L = evict_layout(src, keep);
+  SelArgs a{};
+  a.weights = weights;
+  a.lens = src.lens;
+  a.new_lens = dst.lens;
+  a.table = src.table;
+  a.new_weights = new_weights;
+  a.kept = kept;
+  a.list = reinterpret_cast<int32_t*>(ws + L.list);
+  a.new_cap = static_cast<int64_t>(dst.max_pages) * kB;
+  a.list_stride = static_cast<int64_t>(L.list_stride);
+  a.hkv = src.hkv;
+  a.cap = src.max_pages * kB;
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.num_pages = src.num_pages;
+  a.hist = reinterpret_cast<uint16_t*>(ws + L.hist);
+  a.state = reinterpret_cast<SelState*>(ws + L.state);
+  a.chunks = (a.cap + kChunk - 1) / kChunk;
+  a.rows = src.batch * src.hkv;
+  a.status = reinterpret_cast<DevStatus*>(ws);
   cudaError_t e;
-  if (wide) {
-    e = cudaFuncSetAttribute(select_kernel<kCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = kCluster;
-    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+  if (a.chunks == 1) {
+    e = launch_dependent(select_kernel, dim3(static_cast<unsigned>(a.rows)), kSelThreads, 0, st, a);
+  } else {
+    const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.hkv), static_cast<unsigned>(src.batch));
+    e = launch_dependent(chunk_kernel<0>, grid, kSelThreads, 0, st, a);
+    if (e == cudaSuccess) e = launch_dependent(chunk_kernel<1>, grid, kSelThreads, 0, st, a);
+    if (e == cudaSuccess) e = launch_dependent(chunk_kernel<2>, grid, kSelThreads, 0, st, a);
+    if (e == cudaSuccess) e = launch_dependent(chunk_kept_kernel, grid, kSelThreads, 0, st, a);
   }
-  e = cudaLaunchKernelEx(&cfg, wide ? select_kernel<kCluster> : select_kernel<1>, weights,
-                         static_cast<const int32_t*>(src.lens), dst.lens, src.hkv, cap, keep, sink, recent, src.table,
-                         src.num_pages, new_weights, new_cap, kept, new_cap, list, list_stride, status);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(pack_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPackSmem));
   if (e != cudaSuccess) return e;
-  const int new_pages = (min(keep, cap) + kB - 1) / kB;
-  const int items = src.batch * src.hkv * new_pages;
+  const int new_pages = (min(keep, a.cap) + kB - 1) / kB;
+  const int items = a.rows * new_pages;
   return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(min(items, 2 * sms))), kThreads, kPackSmem, st,
                           k_pool(src), v_pool(src), src.page_stride, src.head_stride, src.max_pages, k_pool(dst),
                           v_pool(dst), dst.page_stride, dst.head_stride, dst.table, dst.num_pages, dst.max_pages,
                           src.hkv, static_cast<const int32_t*>(src.lens), keep, new_pages, items,
-                          static_cast<const int32_t*>(list), list_stride, status);
+                          static_cast<const int32_t*>(a.list), a.list_stride, a.status);
 }
 
 }  // namespace crisp
