@@ -1109,7 +1109,11 @@ const char* crisp_status_string(crisp_status status) {
     case CRISP_ERR_CUDA: return "CUDA runtime error";
     case CRISP_ERR_TIMEOUT: return "device wait timed out";
     case CRISP_ERR_DEVICE: return "device is not sm_103";
+#ifdef CRISP_DEBUG
     case CRISP_ERR_BOUNDS: return "device index outside its buffer (bounds-checking build)";
+#else
+    case CRISP_ERR_BOUNDS: return "device index outside its buffer";
+#endif
   }
   return "unknown status";
 }

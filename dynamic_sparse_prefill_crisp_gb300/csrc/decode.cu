@@ -9,16 +9,23 @@
 //   acc = acc 2^(m - m') + O^T vs 2^(m_t - m')      fp32 registers, m' = max(m, m_t)
 // K and V go from HBM by TMA to shared memory and into the tensor cores as
 // they are: nothing dequantises them. The other operand is made of two e4m3
-// pieces, x = hi + lo / 16 (columns r and 8 + r of 16 for eight rows): a bf16 q at a power-of-two
-// row scale is exactly that sum down to 2^-14 of the row's largest element;
-// p (scaled to 256 at the step's maximum) is off by at most 2^-8 of itself, as
-// a bf16 p would be. O^T is read back every tile, so that page scales and the
-// running maximum act in fp32 and a tile of small p is as exact as any other.
+// pieces, x = hi + lo / 16 (for eight rows, columns r and 8 + r of 16). A bf16 q
+// at a power-of-two row scale is exactly that sum, down to 2^-14 of the row's
+// largest element. p, scaled to 256 at the step's maximum, goes through fp16:
+// it is off by at most 2^-11 of itself for that and 2^-9 for the pieces, less
+// than a bf16 p. O^T is read back every tile, so that page scales and the
+// running maximum act in fp32, and a tile of small p is as exact as any other.
 //
-// Two tiles of an item make a step. What bounds a step is the chain of waits
-// from its scores to its P', not arithmetic: one tile at a time took 2300
-// cycles (2800 with weights; 44.7 bytes per ns and SM leave 2800 for two CTAs'
-// tiles), so a step shares the waits, the maximum and the fence between two.
+// Two tiles of an item make a step: what takes time between a step's scores and
+// its P' is a chain of waits (one tile at a time took 2300 cycles, where the
+// memory gives a CTA a tile every 2800), and two tiles share it. Then the
+// memory bounds all but short calls: 512k tokens of 8 heads in 160 us (6.7 TB/s
+// of K and V; a copy does 6.8). What it comes to elsewhere: 5 us before the
+// first product (launch, lengths, page table, first pages), 4 us behind the
+// last (the joining kernel), and a few waits at every item's end (1000
+// sequences of up to 1000 tokens: 250 us, 153 at the copy rate). With 17 to 32
+// rows one CTA of four groups has the SM; its chain of 1850 cycles a tile is
+// longer than the memory's 1400 (28 rows, 128k tokens, 4 heads: 41 us against 20).
 //
 // The work is the list of all tiles of the batch, item (sequence, kv head, row
 // chunk) by item; every CTA takes an equal run of it, so ragged batches stay
@@ -27,8 +34,12 @@
 // join_kernel adds them in CTA order: results do not depend on timing.
 //
 // Warps: kWG groups of four for softmax and accumulation, eight rows each
-// (thread t of a group: key t of a tile, feature t of the output), then TMA, MMA
-// issue (and TMEM), and the Q' operand.
+// (thread t of a group: key t of a tile, feature t of the output), then K copies,
+// V copies, MMA issue (and TMEM), and the Q' operand.
+//
+// Every launch may start while the kernel before it ends (3 us a call saved);
+// each waits (grid_dep_wait) before it touches anything of another's, and no
+// thread returns without that, so that a kernel's end is its predecessors' too.
 #include <algorithm>
 #include <utility>
 #include <cuda_bf16.h>

@@ -461,8 +461,8 @@ CRISP_API crisp_status crisp_prefill_layer_host(crisp_host_pipeline* pipeline, c
  * lens[b] counts the tokens held, the ones being appended or asked about
  * included: advance it, then append, then attend. Rows of a page at or past
  * lens[b] may hold anything. batch <= 1024, max_pages <= 8192, num_pages <
- * 2^24. Pointers are device pointers: k and v (and the strides) 16-byte aligned, the others
- * 4-byte aligned. */
+ * 2^24, batch * hkv * max_pages < 2^31 (else CRISP_ERR_SHAPE). k and v and
+ * their strides are 16-byte aligned, the other pointers 4-byte aligned. */
 typedef struct crisp_kv_cache {
   int32_t batch;        /* sequences */
   int32_t hkv;          /* key/value heads */
@@ -519,7 +519,10 @@ CRISP_API crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_
  * q, out: bf16 [batch][hq][q_len][128], 1 <= q_len <= 16, hq % hkv == 0;
  * weights: fp32 [batch][hkv][128 * max_pages], contiguous, 16-byte aligned.
  * Precision: q is held as two e4m3 pieces (exact down to 2^-14 of the row's
- * largest element), p as two (2^-8 of itself); products and sums are fp32. */
+ * largest element), p as two (off by less than 2^-8 of itself); products and
+ * sums are fp32. Limits: (hq / hkv) * q_len <= 1024, and batch * hkv * max_pages
+ * * ceil((hq / hkv) * q_len / 32) < 2^31 (else CRISP_ERR_SHAPE). The result does
+ * not depend on timing: the same call gives the same bits. */
 CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32_t hq, int32_t q_len, float scale,
                                               const crisp_tokens* q, const crisp_tokens* out,
                                               const float* weights_in, float* weights_out, void* ws, size_t ws_bytes,

@@ -72,6 +72,9 @@ DECODE = [
     ("drafted-edges", 4, 2, 3, [0, 1, 2, 3, 128, 129, 130, 131]),
     ("drafted-16", 2, 1, 16, [7, 16, 135, 400]),
     ("drafted-gqa16", 16, 1, 5, [260, 4]),
+    ("drafted-gqa7", 14, 2, 2, [300, 129, 2, 1]),
+    ("rows-24", 12, 1, 2, [513]),
+    ("batch-limit", 2, 1, 1, [i % 3 * 70 for i in range(1024)]),
     ("many-short", 4, 1, 1, [(37 * i) % 200 for i in range(300)]),
     ("one-long", 4, 1, 1, [45000]),
 ]
@@ -432,10 +435,11 @@ EVICT = [
     ("ties", 2, [700, 650], 333, 10, 50, "few"),
     ("all-equal", 1, [1000], 257, 1, 1, "equal"),
     ("odd-values", 1, [900], 300, 2, 3, "odd"),
-    ("longer-than-a-chunk", 1, [9001, 4096, 4097], 4097, 128, 128, "random"),
-    ("cluster", 2, [16390, 20000, 300], 9000, 128, 1024, "random"),
-    ("cluster-ties", 1, [40000], 20001, 7, 9, "few"),
-    ("cluster-short", 1, [30000, 5], 29999, 0, 1, "equal"),
+    ("longer-than-a-turn", 1, [9001, 4096, 4097], 4097, 128, 128, "random"),
+    ("chunks", 2, [16390, 20000, 300], 9000, 128, 1024, "random"),
+    ("chunks-ties", 1, [40000], 20001, 7, 9, "few"),
+    ("chunks-short", 1, [30000, 5], 29999, 0, 1, "equal"),
+    ("chunks-odd-values", 1, [33000], 20000, 5, 7, "odd"),
 ]
 
 
