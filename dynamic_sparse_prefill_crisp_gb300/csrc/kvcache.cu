@@ -637,51 +637,55 @@ constexpr size_t kPackSmem = kStages * sizeof(PackStage);
 
 __global__ void __launch_bounds__(kThreads, 2)
     pack_kernel(Pool sk, Pool sv, int64_t s_page, int64_t s_head, int s_max, Pool dk, Pool dv, int64_t d_page,
-                int64_t d_head, const int32_t* d_table, int d_num, int d_max, int hkv, const int32_t* lens, int keep,
-                int new_pages, int items, const int32_t* list, int64_t list_stride, DevStatus* status) {
+                int64_t d_head, const int32_t* d_table, int d_num, int d_max, int batch, int hkv, const int32_t* lens,
+                int keep, int new_pages, int items, const int32_t* list, int64_t list_stride, DevStatus* status) {
   grid_dep_launch();
   extern __shared__ uint8_t smem_raw[];
   PackStage* stages = reinterpret_cast<PackStage*>(smem_raw);
   __shared__ float red[2][2][kThreads / 32];
+  __shared__ int held[kMaxBatch];  // what each sequence keeps
   const int tid = threadIdx.x;
   const int col = (tid & (kRowThreads - 1)) * 16, row0 = tid / kRowThreads;
   grid_dep_wait();
+  for (int b = tid; b < batch; b += kThreads) held[b] = min(min(max(lens[b], 0), s_max * kB), keep);
+  __syncthreads();
 
-  // The next item of this CTA that has rows: its head, rows, and page (-1: none left).
-  struct Item {
-    int g, rows, id;
+  // An item of this CTA (a page that gets rows): its head and rows (0: there are
+  // no more), its page, and where the rows of this thread come from.
+  struct Look {
+    int g, rows, id, src[kPasses];
   };
   int at = static_cast<int>(blockIdx.x);
-  auto start = [&](PackStage& st) -> Item {
-    Item it{0, 0, -1};
-    for (; at < items; at += static_cast<int>(gridDim.x)) {
+  // The lookups of the next item; what they read is not needed before copy().
+  auto look = [&]() -> Look {
+    Look l{};
+    for (; at < items && l.rows <= 0; at += static_cast<int>(gridDim.x)) {
       const int page = at % new_pages, bg = at / new_pages, b = bg / hkv;
-      const int n = min(min(max(lens[b], 0), s_max * kB), keep);
-      if (n <= page * kB) continue;
-      it.g = bg - b * hkv;
-      it.rows = min(n - page * kB, kB);
-      it.id = d_table[static_cast<int64_t>(b) * d_max + page];
-      if (it.id < 0 || it.id >= d_num) {
-        if (tid == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
-        it.id = -1;
-        continue;
-      }
+      l.rows = min(held[b] - page * kB, kB);
+      if (l.rows <= 0) continue;
+      l.g = bg - b * hkv;
+      l.id = d_table[static_cast<int64_t>(b) * d_max + page];
       const int32_t* where = list + bg * list_stride + page * kB;
-      int src[kPasses];
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const int row = row0 + p * kRowsAtOnce;
-        src[p] = row < it.rows ? where[row] : 0;
+        l.src[p] = row < l.rows ? where[row] : 0;
       }
+    }
+    l.rows = max(l.rows, 0);
+    return l;
+  };
+  // Starts the copies of an item.
+  auto copy = [&](const Look& l, PackStage& st) {
+    if (l.rows > 0) {
+      if ((l.id < 0 || l.id >= d_num) && tid == 0) report_error(status, CRISP_ERR_BOUNDS, 0x712);
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
-        const bool there = row0 + p * kRowsAtOnce < it.rows && src[p] >= 0;
-        if (src[p] < 0) {
-          report_error(status, CRISP_ERR_BOUNDS, 0x713);
-          src[p] = 0;
-        }
-        const int64_t from = src[p] / kB * s_page + it.g * s_head + (src[p] % kB) * kD + col;
-        const int64_t sat = static_cast<int64_t>(src[p] / kB) * hkv + it.g;
+        if (l.src[p] < 0) report_error(status, CRISP_ERR_BOUNDS, 0x713);
+        const int src = max(l.src[p], 0);
+        const bool there = row0 + p * kRowsAtOnce < l.rows && l.src[p] >= 0;
+        const int64_t from = src / kB * s_page + l.g * s_head + (src % kB) * kD + col;
+        const int64_t sat = static_cast<int64_t>(src / kB) * hkv + l.g;
         copy16(&st.codes[0][p][tid], sk.codes + from, there);
         copy16(&st.codes[1][p][tid], sv.codes + from, there);
         if (col == 0) {
@@ -689,16 +693,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           copy4(&st.scale[1][p][row0], sv.scale + sat, there);
         }
       }
-      at += static_cast<int>(gridDim.x);
-      break;
     }
     copies_commit();
-    return it;
   };
 
-  Item now = start(stages[0]), next = start(stages[1]);
-  for (int k = 0; now.id >= 0; ++k) {
-    const Item after = start(stages[(k + 2) % kStages]);
+  Look now = look();
+  copy(now, stages[0]);
+  Look next = look();
+  copy(next, stages[1]);
+  Look after = look();
+  for (int k = 0; now.rows > 0; ++k) {
+    copy(after, stages[(k + 2) % kStages]);
+    const Look later = look();
     copies_wait<2>();
     const PackStage& st = stages[k % kStages];
     float amax[2] = {0.f, 0.f}, s[2][kPasses];
@@ -718,20 +724,23 @@ __global__ void __launch_bounds__(kThreads, 2)
       rd[1][tid >> 5] = amax[1];
     }
     __syncthreads();
+    if (now.id >= 0 && now.id < d_num) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float sn = exp2_int(scale_exponent(warp_max(rd[x][tid & (kThreads / 32 - 1)]))), inv = 1.f / sn;
-      uint8_t* codes = (x ? dv : dk).codes + now.id * d_page + now.g * d_head;
+      for (int x = 0; x < 2; ++x) {
+        const float sn = exp2_int(scale_exponent(warp_max(rd[x][tid & (kThreads / 32 - 1)]))), inv = 1.f / sn;
+        uint8_t* codes = (x ? dv : dk).codes + now.id * d_page + now.g * d_head;
 #pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int row = row0 + p * kRowsAtOnce;
-        if (row >= now.rows) continue;
-        *reinterpret_cast<uint4*>(codes + row * kD + col) = rescale16(st.codes[x][p][tid], s[x][p] * inv);
+        for (int p = 0; p < kPasses; ++p) {
+          const int row = row0 + p * kRowsAtOnce;
+          if (row >= now.rows) continue;
+          *reinterpret_cast<uint4*>(codes + row * kD + col) = rescale16(st.codes[x][p][tid], s[x][p] * inv);
+        }
+        if (tid == 0) (x ? dv : dk).scale[static_cast<int64_t>(now.id) * hkv + now.g] = sn;
       }
-      if (tid == 0) (x ? dv : dk).scale[static_cast<int64_t>(now.id) * hkv + now.g] = sn;
     }
     now = next;
     next = after;
+    after = later;
   }
   copies_wait<0>();
 }
@@ -806,7 +815,7 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(min(items, 2 * sms))), kThreads, kPackSmem, st,
                           k_pool(src), v_pool(src), src.page_stride, src.head_stride, src.max_pages, k_pool(dst),
                           v_pool(dst), dst.page_stride, dst.head_stride, dst.table, dst.num_pages, dst.max_pages,
-                          src.hkv, static_cast<const int32_t*>(src.lens), keep, new_pages, items,
+                          src.batch, src.hkv, static_cast<const int32_t*>(src.lens), keep, new_pages, items,
                           static_cast<const int32_t*>(a.list), a.list_stride, a.status);
 }
 
