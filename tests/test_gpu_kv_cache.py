@@ -551,6 +551,98 @@ def test_evict_keeps_non_finite_values_and_reports_bad_pages():
     assert np.array_equal(have[:78], want[0][np.r_[0:30, 80:128]])
 
 
+def test_evict_replays_from_a_cuda_graph():
+    # short and long caches (one launch and a launch per digit); the weights and
+    # lengths may change between replays
+    for lens, keep in (([3000, 900], 1000), ([20000, 17000], 9000)):
+        pools, cache, table, rng = make(lens, 1, 33)
+        new_pages = -(-keep // B)
+        dst = Pools(2 * new_pages, 1)
+        new_cache = dst.cache(np.arange(2 * new_pages).reshape(2, new_pages).tolist(), [0, 0])
+        cap = cache.max_pages * B
+        w = torch.zeros((2, 1, cap), device="cuda")
+        kept = torch.full((2, 1, new_pages * B), -7, dtype=torch.int32, device="cuda")
+        ws = workspace(crisp.kv_evict_workspace_size(cache, keep))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            crisp.kv_evict(cache, new_cache, w, ws, keep=keep, sink=3, recent=50, kept=kept)
+        for step in range(2):
+            wn = rng.random((2, 1, cap)).astype(np.float32)
+            w.copy_(torch.from_numpy(wn))
+            n = [x - 100 * step for x in lens]
+            pools.lens.copy_(torch.tensor(n, dtype=torch.int32))
+            g.replay()
+            assert crisp.read_status(ws) == 0
+            assert new_cache.tensors[5].tolist() == [min(x, keep) for x in n]
+            for b in range(2):
+                m = min(n[b], keep)
+                pos = evict_reference(wn[b, 0], n[b], keep, 3, 50)
+                assert np.array_equal(kept[b, 0, :m].cpu().numpy(), pos)
+                want = tokens_of(pools.host(), table[b], n[b], 0)
+                have = tokens_of(dst.host(), list(range(b * new_pages, (b + 1) * new_pages)), m, 0)
+                for x, y in zip(want, have):
+                    assert (np.abs(x[pos] - y) <= 2.0 ** -10 * 2.0 ** -3).all()  # subnormal codes may round again
+
+
+# ------------------------------------------------------------- sizes and edges
+def test_offsets_past_32_bits():
+    # A pool of 5.2 GB for K and as much for V: pages on both sides of 2^32
+    # bytes, written by an append, read by attention, packed to the last pages.
+    hkv, num = 8, 40000
+    k, v = (torch.empty((num, hkv, B, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty((num, hkv), device="cuda") for _ in range(2))
+    table = torch.tensor([[5, 32767, 32768, 39990], [39999, 1, 20000, 39000]], dtype=torch.int32).cuda()
+    lens = torch.tensor([400, 300], dtype=torch.int32).cuda()
+    cache = crisp.make_kv_cache(k, v, ks, vs, table, lens)
+    rng = np.random.default_rng(51)
+    x = {m: bf16(rng.standard_normal((2, hkv, 400, D))) for m in "kv"}
+    ws = workspace(max(crisp.decode_workspace_size(cache, 16, 1, True), crisp.kv_evict_workspace_size(cache, 200)))
+    crisp.kv_append(cache, x["k"].cuda(), x["v"].cuda(), ws, new_lens=lens)
+    q = bf16(rng.standard_normal((2, 16, 1, D)))
+    out, weights = torch.empty_like(q.cuda()), torch.zeros((2, hkv, 4 * B), device="cuda")
+    crisp.decode_attention(cache, q.cuda(), out, ws, None, weights)
+    new_table = torch.tensor([[39998, 32769], [2, 39997]], dtype=torch.int32).cuda()
+    new_lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    new_cache = crisp.make_kv_cache(k, v, ks, vs, new_table, new_lens)
+    out2 = torch.empty_like(out)
+    crisp.kv_evict(cache, new_cache, weights, ws, keep=200, sink=10, recent=20)
+    crisp.decode_attention(new_cache, q.cuda(), out2, ws)
+    assert crisp.read_status(ws) == 0
+
+    def read(tab):  # the touched pages only, renumbered
+        ids = torch.tensor(sorted({int(i) for i in tab.flatten()}))
+        at = {int(p): j for j, p in enumerate(ids)}
+        host = tuple(t[ids.cuda()].cpu().numpy() for t in (k, v, ks, vs))
+        return host, [[at[int(p)] for p in row] for row in tab.cpu()]
+    host, tab = read(table)
+    for b, n in enumerate((400, 300)):
+        for g in range(hkv):
+            for y, m in zip(tokens_of(host, tab[b], n, g), "kv"):
+                want = x[m][b, g, :n].double().numpy()
+                assert np.abs(y - want).max() <= np.abs(want).max() * 2.0 ** -4
+    want, tol, _, _ = attention(host, tab, [400, 300], q.double().numpy())
+    check(out, want, tol)
+    host, tab = read(new_table)
+    want, tol, _, _ = attention(host, tab, [200, 200], q.double().numpy())
+    check(out2, want, tol)
+
+
+def test_a_batch_of_no_sequences_is_nothing_to_do():
+    pools = Pools(2, 1)
+    cache = pools.cache(torch.zeros((0, 3), dtype=torch.int32), torch.zeros(0, dtype=torch.int32))
+    host = pools.host()
+    ws = workspace(max(crisp.kv_append_workspace_size(cache), crisp.decode_workspace_size(cache, 4),
+                       crisp.kv_evict_workspace_size(cache, 5)))
+    x = torch.zeros((0, 1, 7, D), dtype=torch.bfloat16, device="cuda")
+    crisp.kv_append(cache, x, x, ws)
+    q = torch.zeros((0, 4, 1, D), dtype=torch.bfloat16, device="cuda")
+    crisp.decode_attention(cache, q, torch.empty_like(q), ws)
+    other = Pools(2, 1).cache(torch.zeros((0, 1), dtype=torch.int32), torch.zeros(0, dtype=torch.int32))
+    crisp.kv_evict(cache, other, torch.zeros((0, 1, 3 * B), device="cuda"), ws, keep=5)
+    assert crisp.read_status(ws) == 0
+    assert_same_pools(pools, host)
+
+
 # ------------------------------------------------------------------ together
 def test_prefill_store_decode_evict_decode():
     """As a program runs them: a layer is prefilled, its K and V are stored, tokens
