@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     for (int w = 0; w < warp; ++w) add += sh.warp_sum[w];
     if (b < a.batch) pre[b + 1] = n + add;
     for (int w = 0; w < C::threads / 32; ++w) before += sh.warp_sum[w];
-    __syncthreads();
+    if (b0 + C::threads < a.batch) __syncthreads();  // warp_sum is written again
   }
   tc_fence_before();
   __syncthreads();
@@ -527,6 +527,12 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       if (lane == 0) mbar_arrive_n(&sh.q_full[buf], C::workers);
       t += x.left;
     }
+    // If the run's last item begins here and goes on, it is joined under this CTA's number.
+    if (lane == 0) {
+      const int rest = x.pages - x.page - x.left;  // its pages behind this run
+      const bool goes_on = x.page == 0 && rest > 0;
+      a.split[run] = Split{goes_on ? x.b : -1, x.gc, goes_on ? shares.of(t_lo + n - 1 + rest) : run, 0};
+    }
   } else if (n > 0 && warp < C::workers) {
     const int wg = warp >> 2, quarter = warp & 3;
     const int tid = threadIdx.x & 127;              // key of a tile, feature of the output
@@ -663,11 +669,6 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         for (int r = 0; r < kWgRows; ++r)
           if (r < nr) to[r * kD] = acc[r];
         if (tid < nr) a.part_ml[slot * kR + row0 + tid] = make_float2(m, ls);
-      }
-      if (i_end == n && threadIdx.x == 0) {
-        // an item that begins here and goes on is joined under this CTA's number
-        const bool goes_on = t_item >= t_lo && of.end < of.pages;
-        a.split[run] = Split{goes_on ? of.b : -1, of.gc, shares.of(t_item + of.pages - 1), 0};
       }
     };
 
@@ -864,10 +865,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       if (ok && add_o(steps - 1, prev)) finish(n, prev);
       else ok = false;
     }
-    if (!ok) {
-      if (lane == 0) fail(&sh.abort, a.status, 0x614);
-      if (threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
-    }
+    if (!ok && lane == 0) fail(&sh.abort, a.status, 0x614);
   }
   if (n == 0 && threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
   // Sequences without a page have no tile: their rows of the output are zeros.
@@ -904,22 +902,35 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (sp.b < 0 || row >= a.rows) return;
   const int nc = sp.last - c0 + 1;
   auto slot_of = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
-  float m = -INFINITY;
-  for (int x = tid; x < nc; x += kJoinThreads) m = fmaxf(m, a.part_ml[slot_of(x) * kr + r].x);
+  auto part_of = [&](int x) {
+    return *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(slot_of(x)) * kr + r) * kD + lane * 4);
+  };
+  // this warp's first accumulators are asked for together with the statistics
+  constexpr int kFirst = 4;
+  float4 first[kFirst];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int u = 0; u < kFirst; ++u) first[u] = warp + u * kWarps < nc ? part_of(warp + u * kWarps) : make_float4(0, 0, 0, 0);
+  static_assert(kMaxDecodeCtas <= 2 * kJoinThreads, "two CTAs' statistics a thread");
+  float2 ml[2];
+  float m = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int x = tid + u * kJoinThreads;
+    ml[u] = x < nc ? a.part_ml[slot_of(x) * kr + r] : make_float2(-INFINITY, 0.f);
+    m = fmaxf(m, ml[u].x);
+  }
+  m = warp_max(m);
   if (lane == 0) red_m[warp] = m;
   __syncthreads();
-  m = red_m[lane & (kWarps - 1)];
-#pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_max(red_m[lane & (kWarps - 1)]);
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  for (int x = tid; x < nc; x += kJoinThreads) {
-    const float2 ml = a.part_ml[slot_of(x) * kr + r];
-    const float fx = ex2_approx(ml.x - base);
-    f[x] = fx;
-    l = fmaf(fx, ml.y, l);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int x = tid + u * kJoinThreads;
+    const float fx = ex2_approx(ml[u].x - base);
+    if (x < nc) f[x] = fx;
+    l = fmaf(fx, ml[u].y, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -928,15 +939,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   l = 0.f;
   for (int w = 0; w < kWarps; ++w) l += red_l[w];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float fx, const float4& v) {
+    acc.x = fmaf(fx, v.x, acc.x);
+    acc.y = fmaf(fx, v.y, acc.y);
+    acc.z = fmaf(fx, v.z, acc.z);
+    acc.w = fmaf(fx, v.w, acc.w);
+  };
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u)
+    if (warp + u * kWarps < nc) add(f[warp + u * kWarps], first[u]);
 #pragma unroll 4
-  for (int x = warp; x < nc; x += kWarps) {
-    const float4 v = *reinterpret_cast<const float4*>(
-        a.part + (static_cast<int64_t>(slot_of(x)) * kr + r) * kD + lane * 4);
-    acc.x = fmaf(f[x], v.x, acc.x);
-    acc.y = fmaf(f[x], v.y, acc.y);
-    acc.z = fmaf(f[x], v.z, acc.z);
-    acc.w = fmaf(f[x], v.w, acc.w);
-  }
+  for (int x = warp + kFirst * kWarps; x < nc; x += kWarps) add(f[x], part_of(x));
   red[warp][lane] = acc;
   __syncthreads();
   if (warp == 0) {
