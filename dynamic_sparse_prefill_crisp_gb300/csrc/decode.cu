@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     tmem_relinquish();
   }
   if (lane == 0 && (warp == kKWarp || warp == kVWarp)) prefetch_tmap(warp == kKWarp ? &tk : &tv);
-  // Each CTA asks for a line of the page table: what of it is used is known two reads from here.
+  // The lengths, and a line of the page table by each CTA, are asked for: what
+  // of the table is used is known two reads from here.
+  if (warp == 1 && lane * 32 < a.batch) prefetch_l2(a.lens + lane * 32);
   if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) * 32 < a.batch * a.max_pages)
     prefetch_l2(a.table + static_cast<int>(blockIdx.x) * 32);
   // From here on what earlier kernels of the stream wrote is read, and results are written.
@@ -385,10 +387,6 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     constexpr int kFirst = kWG == 1 ? kStep : 2 * kStep;  // at most a K slot each
     int slot = 0, phase = 1, issued = 0;
     bool go = true;
-    if (!is_k && !warp_wait(&sh.v_start, 0, &sh.abort)) {
-      go = false;
-      if (lane == 0) fail(&sh.abort, a.status, 0x615);
-    }
     for (int i0 = 0; go && i0 < n; i0 += 32) {
       int z = -1, g = 0;
       if (i0 + lane < n) {
@@ -399,6 +397,10 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         if (z < 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x602);
       }
       const int m = min(32, n - i0);
+      if (!is_k && i0 == 0 && !warp_wait(&sh.v_start, 0, &sh.abort)) {
+        go = false;
+        if (lane == 0) fail(&sh.abort, a.status, 0x615);
+      }
       for (int k = 0; k < m; ++k) {
         const int zt = bcast(z, k), gt = bcast(g, k);
         if (lane == 0 && go) {
@@ -548,23 +550,33 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     // tiles by 32: lane L looks up tile win + L (its page, scales, and sequence's length)
     int win = 0, z = -1, ln = 0;
     float ks = 0.f, vs = 0.f;
-    auto look_up = [&](int i) {
+    int id = -1, id_head = 0;  // as asked for
+    auto ask = [&](int i) {
       win = i;
-      z = -1;
-      ks = vs = 0.f;
+      id = -1;
       if (i + lane < n) {
         Walk y;
         y.begin(pre, a, t_lo + i + lane, n);
-        z = page_id(a, y.b, y.page);
+        id = a.table[static_cast<int64_t>(y.b) * a.max_pages + y.page];
+        id_head = a.chunks == 1 ? y.gc : y.gc / a.chunks;
         bool bad;
         ln = clamped_len(a, y.b, bad);
-        if (z >= 0) {
-          const int64_t at = static_cast<int64_t>(z) * a.hkv + y.gc / a.chunks;
-          ks = a.k_scale[at];
-          vs = a.v_scale[at];
-        }
       }
     };
+    auto take = [&]() {
+      z = id >= 0 && id < a.num_pages ? id : -1;
+      ks = vs = 0.f;
+      if (z >= 0) {
+        const int64_t at = static_cast<int64_t>(z) * a.hkv + id_head;
+        ks = a.k_scale[at];
+        vs = a.v_scale[at];
+      }
+    };
+    auto look_up = [&](int i) {
+      ask(i);
+      take();
+    };
+    ask(0);
     Walk x;
     x.begin(pre, a, t_lo, n);
     {
@@ -575,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[0]);
     }
-    look_up(0);
+    take();
     int item = 0, i = 0, steps = 0, len = 0, g = 0, r0 = 0, toks_r0 = -1;
     uint32_t toks = 0;
     auto tok_of = [&](int r) { return static_cast<int>(toks >> (4 * r) & 15u); };
