@@ -990,16 +990,18 @@ __global__ void __launch_bounds__(kWeightThreads)
   __shared__ float lse[kMaxGroupRows];
   const int g = blockIdx.y, b = blockIdx.z;
   grid_dep_launch();
-  bool bad;
-  const int len = clamped_len(a, b, bad);
   const int key = blockIdx.x * kWeightKeys + threadIdx.x * 4;
   const int64_t cap = static_cast<int64_t>(a.max_pages) * kB, bg = static_cast<int64_t>(b) * a.hkv + g;
   const int64_t at = bg * cap + key;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  // rows of weights and scores end at a multiple of 128: whole groups of four are there
-  if (w_in != nullptr && key < len) w = *reinterpret_cast<const float4*>(w_in + at);
+  // Rows of weights and scores end at a multiple of 128: whole groups of four are
+  // there. What came before this call has ended when its first kernel lets the
+  // next ones start, so w_in is read at once (from L2).
+  if (w_in != nullptr && key < cap) w = __ldcg(reinterpret_cast<const float4*>(w_in + at));
   // before any return: this kernel may not end before the ones it depends on
   grid_dep_wait();
+  bool bad;
+  const int len = clamped_len(a, b, bad);
   if (static_cast<int>(blockIdx.x) * kWeightKeys >= len) return;
   for (int r = threadIdx.x; r < a.rows; r += kWeightThreads) lse[r] = a.lse[bg * a.rows + r];
   __syncthreads();
