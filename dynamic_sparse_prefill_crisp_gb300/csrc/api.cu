@@ -1042,7 +1042,10 @@ crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst
       return CRISP_ERR_INVALID_ARG;
     if (src->batch == 0) return CRISP_OK;
     if (!weights || weights == new_weights) return CRISP_ERR_INVALID_ARG;
-    if (src->table == dst->table || src->lens == dst->lens) return CRISP_ERR_INVALID_ARG;  // written while read
+    // read while written: the lengths, or pages that both caches hold
+    const bool one_pool =
+        src->k == dst->k || src->v == dst->v || src->k_scale == dst->k_scale || src->v_scale == dst->v_scale;
+    if (src->lens == dst->lens || (one_pool && src->table == dst->table)) return CRISP_ERR_INVALID_ARG;
     if (!aligned16(weights) || !aligned16(new_weights) || !aligned(kept, 4)) return CRISP_ERR_ALIGN;
     if ((st = check_cache_ws(ws, ws_bytes, evict_layout(*src, keep).total)) != CRISP_OK) return st;
     int sms = 0;

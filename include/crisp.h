@@ -535,8 +535,8 @@ CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32
  * position; NaN counts as larger than any number). The kept tokens go, in their
  * order, to positions 0, 1, .. of dst: each of its pages gets the scale its
  * values need, codes rounded again where that differs. dst->lens[b] = min(n,
- * keep). dst may share the pools with src (k, v, scales), but its table's pages
- * must not stand in any src table. new_weights fp32 [batch][hkv][128 *
+ * keep). dst->lens is not src->lens. dst may share the pools with src (k, v,
+ * scales); its table's pages must then not stand in any src table. new_weights fp32 [batch][hkv][128 *
  * dst->max_pages] (16-byte aligned) and kept int32 [batch][hkv][128 *
  * dst->max_pages] (each kept token's old position) are written below the new
  * length; either may be NULL. 1 <= keep <= 128 * dst->max_pages, sink + recent

@@ -507,6 +507,18 @@ def test_evict_keeps_and_packs_what_the_definition_says(name, hkv, lens, keep, s
                     scales[new_table[b][p], g] = e
                     codes[new_table[b][p], g, :len(rows)] = round_codes(rows / e)
     assert_same_pools(dst, dhost)
+    if not shared:  # into pages of the same ids, by the same table
+        alike = Pools(num, hkv)
+        cache2 = crisp.make_kv_cache(alike.k, alike.v, alike.ks, alike.vs, cache.tensors[4],
+                                     torch.full((batch,), -1, dtype=torch.int32, device="cuda"))
+        if keep <= cache2.max_pages * B:
+            crisp.kv_evict(cache, cache2, wd, ws, keep=keep, sink=sink, recent=recent)
+            assert crisp.read_status(ws) == 0
+            for b, n in enumerate(lens):
+                m = min(n, keep)
+                for g in range(hkv):
+                    for a, c in zip(tokens_of(alike.host(), table[b], m, g), tokens_of(dst.host(), new_table[b], m, g)):
+                        assert np.array_equal(a, c, equal_nan=True)
     # without the optional outputs: the same cache
     again = Pools(num, hkv)
     cache2 = Pools.cache(again, cut(new_table, [min(n, keep) for n in lens]), [-1] * batch)

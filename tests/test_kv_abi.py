@@ -141,6 +141,11 @@ def test_evict_refusals(L):
         assert evict(L, c, d, keep=keep, sink=sink, recent=recent) == INVALID
     assert evict(L, c, d, weights=None) == INVALID and evict(L, c, d, new_w=vp(512)) == INVALID
     assert evict(L, c, other(table=256)) == INVALID and evict(L, c, other(lens=256)) == INVALID
+    # the same table is refused over any shared pool, and taken over pools of its own (here up to the workspace)
+    apart = {"k": 768, "v": 768, "k_scale": 768, "v_scale": 768}
+    for field in apart:
+        assert evict(L, c, other(table=256, **{**apart, field: 256})) == INVALID
+    assert evict(L, c, other(table=256, **apart), nbytes=0) == WORKSPACE
     assert evict(L, c, d, weights=vp(520)) == ALIGN and evict(L, c, d, new_w=vp(260)) == ALIGN
     assert evict(L, c, d, kept=vp(258)) == ALIGN
     n = ctypes.c_size_t()
