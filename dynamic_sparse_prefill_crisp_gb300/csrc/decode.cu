@@ -546,7 +546,19 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     const int my_row = lane & (kWgRows - 1);        // row of the lane-held maximum
     float acc[kWgRows], l[kWgRows];
     float m = -INFINITY;                            // running maximum of row my_row, base 2
-    bool ok = true;
+    // A wait that gives up lets its warp go on, and so does every wait after it:
+    // all warps of a group take every step of the run, so none is left behind in
+    // a named barrier. What is computed then goes to the call's own buffers, and
+    // the status says that it is worth nothing.
+    auto await = [&](uint64_t* b, int parity) {
+      bool done = mbar_try_wait(b, parity);
+      if (__all_sync(0xffffffffu, done)) return;
+      const volatile int* abort = &sh.abort;
+      const unsigned long long t0 = globaltimer_ns();
+      while (!done && !*abort && globaltimer_ns() - t0 <= kWaitLimitNs) done = mbar_try_wait(b, parity);
+      if (!done) fail(&sh.abort, a.status, 0x614);
+      __syncwarp();
+    };
     // tiles by 32: lane L looks up tile win + L (its page, scales, and sequence's length)
     int win = 0, z = -1, ln = 0;
     float ks = 0.f, vs = 0.f;
@@ -611,9 +623,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       end = min(max(len - page * kB, 0), kB);
     };
 
-    auto add_o = [&](int st, const Item& of) -> bool {
+    auto add_o = [&](int st, const Item& of) {
       const int ob = st % C::bufs;
-      if (!warp_wait(&sh.o_full[ob], (st / C::bufs) & 1, &sh.abort)) return false;
+      await(&sh.o_full[ob], (st / C::bufs) & 1);
       tc_fence_after();
       float wl[kWgRows];
       load8(sh.wl[warp][ob], wl);
@@ -648,7 +660,6 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
           ffma2(acc[r], acc[r + 1], v[r], v[r + 1], w0, w1, acc[r], acc[r + 1]);
         }
       }
-      return true;
     };
 
     // The end of an item in this run; i_end: tiles of the run up to it.
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       }
     };
 
-    for (int st = 0; ok && i < n; ++st) {
+    for (int st = 0; i < n; ++st) {
       const int mt_tiles = min(kStep, x.left), buf = st & 1;
       if (i + kStep > win + 32) look_up(i);
       if (begins) {
@@ -697,15 +708,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
           const int tok = a.q_len == 1 ? 0 : min((r0 + my_row) / a.group, kMaxQLen - 1);
           toks = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(tok) << (4 * my_row));
         }
-        if (!warp_wait(&sh.q_full[item & 1], (item >> 1) & 1, &sh.abort)) {
-          ok = false;
-          break;
-        }
+        await(&sh.q_full[item & 1], (item >> 1) & 1);
       }
-      if (!warp_wait(&sh.s_full[buf], (st >> 1) & 1, &sh.abort)) {
-        ok = false;
-        break;
-      }
+      await(&sh.s_full[buf], (st >> 1) & 1);
       tc_fence_after();
       // Row r's token sees the keys below len - (q_len - 1) + its number.
       float s[kStep][kWgRows], t[kWgRows], vst[kStep];
@@ -747,10 +752,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         red[1] = make_float4(t[4], t[5], t[6], t[7]);
       }
       // The step before: its product has run meanwhile.
-      if (C::bufs == 1 && st > 0 && !add_o(st - 1, prev)) {
-        ok = false;
-        break;
-      }
+      if (C::bufs == 1 && st > 0) add_o(st - 1, prev);
       if (begins) {
         if (C::bufs == 1 && st > 0) finish(i, prev);
 #pragma unroll
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
             // V rows that not every row sees become zeros: p = 0 there, and what
             // the page holds (anything past the end) must not matter
             const int sl = (i + j) % C::v_slots;
-            if (!warp_wait(&sh.v_full[sl], ((i + j) / C::v_slots) & 1, &sh.abort)) ok = false;
+            await(&sh.v_full[sl], ((i + j) / C::v_slots) & 1);
             if (tid >= lo) {
               uint4* rowp = reinterpret_cast<uint4*>(sV + sl * kPage + tid * 128);
 #pragma unroll
@@ -828,7 +830,6 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         *reinterpret_cast<uint4*>(p_at + (st % C::bufs * kStep + j) * C::op) = make_uint4(
             hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
-      if (!ok) break;
       fence_async_shared();
       tc_fence_before();
       mbar_arrive(&sh.p_full[st % C::bufs]);
@@ -845,10 +846,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
         }
       }
       const Item now{x.b, x.gc, g, r0, x.page + mt_tiles, x.pages, len, toks};
-      if (C::bufs == 2 && !begins && !add_o(st - 1, now)) {
-        ok = false;
-        break;
-      }
+      if (C::bufs == 2 && !begins) add_o(st - 1, now);
       o.tiles = mt_tiles;
       o.page = x.page;
       o.vs[0] = vst[0];
@@ -863,10 +861,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       begins = x.left == 0;
       if (begins) {
         if (C::bufs == 2) {
-          if (!add_o(st, now)) {
-            ok = false;
-            break;
-          }
+          add_o(st, now);
           finish(i, now);
         }
         ++item;
@@ -874,10 +869,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       }
     }
     if (C::bufs == 1) {
-      if (ok && add_o(steps - 1, prev)) finish(n, prev);
-      else ok = false;
+      add_o(steps - 1, prev);
+      finish(n, prev);
     }
-    if (!ok && lane == 0) fail(&sh.abort, a.status, 0x614);
   }
   if (n == 0 && threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
   // Sequences without a page have no tile: their rows of the output are zeros.
