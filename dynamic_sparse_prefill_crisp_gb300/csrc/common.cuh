@@ -132,7 +132,7 @@ inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 struct DecodeLayout {
   size_t part;     // fp32 [2 CTAs][rows of a chunk][128]  unfinished accumulators
   size_t part_ml;  // float2 [2 CTAs][rows of a chunk]     their running maximum and sum
-  size_t split;    // [CTAs] which item begins there and goes on
+  size_t split;    // [CTAs] items that go on from one CTA to another
   size_t lse;      // fp32 [batch][hkv][rows]              log2 of the sums (weights only)
   size_t scores;   // fp32 [batch][hkv][rows][128 max_pages]  scores in base 2 (weights only)
   size_t total;

@@ -95,15 +95,19 @@ struct Shared {
   float tail[2][kWG * kWgRows][kMaxTail + 1];       // p of keys that only some rows see
 };
 
-// A split item, by the CTA in which it begins.
+// A split item, recorded by the CTA in which it begins: under the CTA's number
+// (one item at most begins in it and goes on), or, with more than eight rows and
+// no more items than CTAs, under the item's: then the joining kernel has a block
+// a row for every item and not for every CTA (28 rows, 4 heads: 112 and not
+// 4256, 39.1 us and not 40.6; with eight rows or fewer it gains nothing).
 struct Split {
-  int b, gc;   // sequence (-1: no item begins here and goes on); kv head * chunks + row chunk
-  int last;    // the CTA in which it ends
-  int pad;
+  int b, gc;        // sequence (-1: no such item); kv head * chunks + row chunk
+  int first, last;  // the CTAs in which it begins and ends
 };
 
 struct Args {
   int batch, hkv, group, q_len, rows, chunks, num_pages, max_pages, ctas;
+  int records;                         // joining blocks a row: ctas, or the number of items
   const float *k_scale, *v_scale;
   const int32_t *table, *lens;
   const uint8_t* v;                    // for the tail keys
@@ -115,7 +119,7 @@ struct Args {
   float c;                             // scale * log2(e)
   float* part;                         // [2 ctas][rows of a chunk][128]
   float2* part_ml;                     // [2 ctas][rows of a chunk]  (m, l)
-  Split* split;                        // [ctas]
+  Split* split;                        // [records]
   float* lse;                          // [batch][hkv][rows]  log2 sum of 2^s, +inf for a row without keys; or null
   float* scores;                       // [batch][hkv][rows][128 max_pages] or null
   DevStatus* status;
@@ -371,6 +375,7 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
   // (the host has seen to it that the tiles a full table holds are an int's worth)
   const Shares shares(before * a.hkv * a.chunks, a.ctas);
   const int run = static_cast<int>(blockIdx.x);
+  const bool by_item = kWG > 1 && a.records < a.ctas;
   const int t_lo = run < shares.runs ? shares.begin(run) : 0;
   const int n = run < shares.runs ? shares.begin(run + 1) - t_lo : 0;
 
@@ -514,27 +519,36 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     // while they wait for its scores.
     Walk x;
     x.begin(pre, a, t_lo, n);
-    int t = x.left;
-    for (int item = 1; t < n; ++item) {
-      x.next(pre, a, n - t);
-      const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc - g * a.chunks) * kR;
-      if (!warp_wait(&sh.q_empty[buf], ((item >> 1) & 1) ^ 1, &sh.abort)) {
-        if (lane == 0) fail(&sh.abort, a.status, 0x613);
-        break;
+    // whether the item begins here and goes on behind the run
+    auto record = [&](bool ends_run) {
+      const int rest = x.pages - x.page - x.left;  // its pages behind this run
+      const bool goes_on = x.page == 0 && rest > 0;
+      const Split sp{goes_on ? x.b : -1, x.gc, run, goes_on ? shares.of(t_lo + n - 1 + rest) : run};
+      if (!by_item) {
+        if (ends_run) a.split[run] = sp;
+      } else if (x.page == 0) {
+        a.split[x.b * a.hkv * a.chunks + x.gc] = sp;
       }
+    };
+    int t = x.left;
+    bool ok = true;
+    for (int item = 1; t < n; ++item) {
+      if (by_item && lane == 0) record(false);
+      x.next(pre, a, n - t);
+      t += x.left;
+      const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc - g * a.chunks) * kR;
+      if (ok && !warp_wait(&sh.q_empty[buf], ((item >> 1) & 1) ^ 1, &sh.abort)) {
+        if (lane == 0) fail(&sh.abort, a.status, 0x613);
+        ok = false;
+      }
+      if (!ok) continue;  // every item is recorded all the same
       constexpr int kAtOnce = kR < 16 ? kR : 16;
       for (int rb = 0; rb < kR; rb += kAtOnce) make_q<kAtOnce>(a, sQ + buf * C::op, sh.qs[buf], x.b, g, r0, rb);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_n(&sh.q_full[buf], C::workers);
-      t += x.left;
     }
-    // If the run's last item begins here and goes on, it is joined under this CTA's number.
-    if (lane == 0) {
-      const int rest = x.pages - x.page - x.left;  // its pages behind this run
-      const bool goes_on = x.page == 0 && rest > 0;
-      a.split[run] = Split{goes_on ? x.b : -1, x.gc, goes_on ? shares.of(t_lo + n - 1 + rest) : run, 0};
-    }
+    if (lane == 0) record(true);
   } else if (n > 0 && warp < C::workers) {
     const int wg = warp >> 2, quarter = warp & 3;
     const int tid = threadIdx.x & 127;              // key of a tile, feature of the output
@@ -873,10 +887,12 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       finish(n, prev);
     }
   }
-  if (n == 0 && threadIdx.x == 0) a.split[run] = Split{-1, 0, 0, 0};
+  if (n == 0 && threadIdx.x == 0 && !by_item) a.split[run] = Split{-1, 0, 0, 0};
   // Sequences without a page have no tile: their rows of the output are zeros.
   for (int b = run; b < a.batch; b += a.ctas) {
     if (pre[b + 1] != pre[b]) continue;
+    if (by_item)
+      for (int e = threadIdx.x; e < a.hkv * a.chunks; e += C::threads) a.split[b * a.hkv * a.chunks + e] = Split{-1, 0, 0, 0};
     for (int e = threadIdx.x; e < a.hkv * a.rows * kD; e += C::threads) {
       const int d = e % kD, row = e / kD % a.rows, g = e / kD / a.rows;
       a.out[b * a.o_b + (g * a.group + row % a.group) * a.o_h + row / a.group * a.o_t + d] = __float2bfloat16_rn(0.f);
@@ -891,8 +907,8 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
 
 constexpr int kJoinThreads = 256;
 
-// Joins the items that several CTAs worked on: block (c, r) takes row r of the
-// item that begins in CTA c and goes on. Eight warps share the CTAs of the
+// Joins the items that several CTAs worked on: block (j, r) takes row r of the
+// item of record j. Eight warps share the CTAs of the
 // item, a lane has four features; the sums run in a fixed order.
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a, int kr) {
   constexpr int kWarps = kJoinThreads / 32;
@@ -900,10 +916,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   __shared__ float red_m[kWarps], red_l[kWarps];
   __shared__ float4 red[kWarps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c0 = blockIdx.x, r = blockIdx.y;
+  const int r = blockIdx.y;
   grid_dep_launch();
   grid_dep_wait();
-  const Split sp = a.split[c0];
+  const Split sp = a.split[blockIdx.x];
+  const int c0 = sp.first;
   const int g = sp.gc / a.chunks, row = (sp.gc - g * a.chunks) * kr + r;
   if (sp.b < 0 || row >= a.rows) return;
   const int nc = sp.last - c0 + 1;
@@ -1079,6 +1096,7 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
   // what the chip holds at once, and no more than the table can hold tiles
   const long long most = static_cast<long long>(c.batch) * c.max_pages * c.hkv * a.chunks;
   a.ctas = static_cast<int>(std::min<long long>(std::min((wg >= 2 ? 1 : 2) * sms, kMaxDecodeCtas), most));
+  a.records = wg > 1 ? static_cast<int>(std::min<long long>(a.ctas, most / c.max_pages)) : a.ctas;
   a.k_scale = c.k_scale;
   a.v_scale = c.v_scale;
   a.table = c.table;
@@ -1105,7 +1123,7 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
                                                                     : launch_groups<4>(maps, a, st);
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(std::min(kr, a.rows));
-  e = launch_dependent(join_kernel, dim3(static_cast<unsigned>(a.ctas), rows), kJoinThreads, 0, st, a, kr);
+  e = launch_dependent(join_kernel, dim3(static_cast<unsigned>(a.records), rows), kJoinThreads, 0, st, a, kr);
   if (e != cudaSuccess || weights_out == nullptr) return e;
   const unsigned blocks = static_cast<unsigned>((c.max_pages * kB + kWeightKeys - 1) / kWeightKeys);
   return launch_dependent(weights_kernel, dim3(blocks, static_cast<unsigned>(c.hkv), static_cast<unsigned>(c.batch)),
