@@ -86,6 +86,8 @@ struct Shared {
   uint32_t tmem_base;
   int abort;
   int warp_sum[kWG * 4 + 4];
+  uint32_t odd[kMaxBatch / 32];                     // sequences with an odd number of pages
+  int odd_before[kMaxBatch / 32], cut[2];           // how many before these 32; the run's bounds
   alignas(16) float qs[2][kWG * kWgRows];           // q scale * scale * log2(e) per row
   alignas(16) float red[2][kWG][4][kWgRows];        // warps' row maxima
   float sum[kWG][4][kWgRows];                       // and, at an item's end, their row sums
@@ -131,8 +133,8 @@ __device__ __forceinline__ int clamped_len(const Args& a, int b, bool& bad) {
   return min(max(n, 0), cap);
 }
 
-// `runs` CTAs share `total` tiles (every one of them gets one): run c begins at
-// floor(total c / runs).
+// `runs` CTAs share `total` tiles or steps (every one of them gets one): run c
+// begins at floor(total c / runs).
 struct Shares {
   int total, runs, each, rest;  // each = total / runs, rest = total % runs
   __device__ __forceinline__ Shares(int total_, int ctas) {
@@ -142,7 +144,7 @@ struct Shares {
     rest = total - each * runs;
   }
   __device__ __forceinline__ int begin(int c) const { return each * c + rest * c / runs; }  // rest, c < runs <= 304
-  // The run that holds tile t.
+  // The run that holds tile (or step) t.
   __device__ __forceinline__ int of(int t) const {
     int c = static_cast<int>((static_cast<float>(t) + 0.5f) * static_cast<float>(runs) / static_cast<float>(total));
     c = min(max(c, 0), runs - 1);
@@ -354,12 +356,15 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       n = (clamped_len(a, b, bad) + kB - 1) / kB;
       if (bad && blockIdx.x == 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x601);
     }
+    const int own = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, n, o);
       if (lane >= o) n += up;
     }
     if (lane == 31) sh.warp_sum[warp] = n;
+    const uint32_t odd = __ballot_sync(0xffffffffu, own & 1);
+    if (lane == 0 && b < a.batch) sh.odd[b / 32] = odd;
     __syncthreads();
     int add = before;
     for (int w = 0; w < warp; ++w) add += sh.warp_sum[w];
@@ -373,11 +378,50 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
   grid_dep_launch();
   const uint32_t tmem = sh.tmem_base;
   // (the host has seen to it that the tiles a full table holds are an int's worth)
-  const Shares shares(before * a.hkv * a.chunks, a.ctas);
-  const int run = static_cast<int>(blockIdx.x);
+  const int hc = a.hkv * a.chunks, run = static_cast<int>(blockIdx.x);
   const bool by_item = kWG > 1 && a.records < a.ctas;
-  const int t_lo = run < shares.runs ? shares.begin(run) : 0;
-  const int n = run < shares.runs ? shares.begin(run + 1) - t_lo : 0;
+  // Many short items are shared out by steps, not by tiles: the step of an odd
+  // last tile takes as long as another (1000 sequences of up to 1000 tokens, 8
+  // heads: 243 us, 257 by tiles). Longer items gain nothing.
+  const bool by_step = before <= 16 * a.batch && before * hc >= 4 * a.ctas;
+  int odds = 0;  // sequences with an odd number of pages
+  if (by_step) {
+    int c = lane < (a.batch + 31) / 32 ? __popc(sh.odd[lane]) : 0;
+    const int mine = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += up;
+    }
+    if (warp == 0) sh.odd_before[lane] = c - mine;
+    odds = __shfl_sync(0xffffffffu, c, 31);
+  }
+  const Shares shares(by_step ? (before + odds) / 2 * hc : before * hc, a.ctas);
+  int t_lo = run < shares.runs ? shares.begin(run) : 0;
+  int n = run < shares.runs ? shares.begin(run + 1) - t_lo : 0;
+  // steps of a head before sequence b
+  auto steps_before = [&](int b) {
+    return (pre[b] + sh.odd_before[b >> 5] + __popc(sh.odd[b >> 5] & ((1u << (b & 31)) - 1u))) / 2;
+  };
+  if (by_step) {
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+      // the first tile of the run, and the one behind its last
+      const int t = warp == 0 ? t_lo : t_lo + n;
+      int lo = 0, hi = a.batch;  // the last sequence whose first step is not behind t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (steps_before(mid) * hc <= t) lo = mid;
+        else hi = mid;
+      }
+      const int pages = pre[lo + 1] - pre[lo], each = (pages + 1) / 2;
+      const int rem = t - steps_before(lo) * hc, gc = each > 0 ? rem / each : 0;  // (hc behind the last sequence)
+      sh.cut[warp] = pre[lo] * hc + gc * pages + 2 * (rem - gc * each);
+    }
+    __syncthreads();
+    t_lo = sh.cut[0];
+    n = sh.cut[1] - t_lo;
+  }
 
   if (n > 0 && (warp == kKWarp || warp == kVWarp)) {
     // The K pages, or the V pages, of the run in order: each lane looks up one of
@@ -523,7 +567,10 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     auto record = [&](bool ends_run) {
       const int rest = x.pages - x.page - x.left;  // its pages behind this run
       const bool goes_on = x.page == 0 && rest > 0;
-      const Split sp{goes_on ? x.b : -1, x.gc, run, goes_on ? shares.of(t_lo + n - 1 + rest) : run};
+      int ends_in = run;
+      if (goes_on)
+        ends_in = shares.of(by_step ? steps_before(x.b) * hc + (x.gc + 1) * ((x.pages + 1) / 2) - 1 : t_lo + n - 1 + rest);
+      const Split sp{goes_on ? x.b : -1, x.gc, run, ends_in};
       if (!by_item) {
         if (ends_run) a.split[run] = sp;
       } else if (x.page == 0) {

@@ -77,6 +77,13 @@ DECODE = [
     ("batch-limit", 2, 1, 1, [i % 3 * 70 for i in range(1024)]),
     ("many-short", 4, 1, 1, [(37 * i) % 200 for i in range(300)]),
     ("one-long", 4, 1, 1, [45000]),
+    ("rows-limit", 1024, 1, 1, [300, 3]),
+    ("rows-limit-drafted", 64, 1, 16, [300, 20, 0]),
+    # many short sequences, of no page, of an odd and of an even number of pages
+    ("short-items", 8, 4, 1, [97 * i % 520 for i in range(160)]),
+    ("short-items-12-rows", 12, 1, 1, [0, 0] + [61 * i % 520 for i in range(300)] + [0]),
+    ("short-items-two-chunks", 40, 1, 1, [97 * i % 520 // 128 * 128 for i in range(40)] + [300] * 130),
+    ("short-items-drafted", 4, 1, 4, [1 + 61 * i % 380 for i in range(330)]),
 ]
 
 
@@ -210,6 +217,29 @@ def test_decode_bad_pages_and_lengths_are_reported_and_hold_nothing():
     pools.lens.copy_(torch.tensor([-3, 300, 200], dtype=torch.int32))
     out = decode(cache, q, status=CRISP_ERR_BOUNDS)
     assert (out[0] == 0).all() and torch.equal(out[1:], good[1:])
+
+
+def test_decode_on_several_streams_at_once():
+    # each stream with a workspace of its own, and inputs made there just before
+    lens = [1000, 300, 17, 900]
+    pools, cache, table, rng = make(lens, 4, 15)
+    qs = [bf16(rng.standard_normal((4, 28, 2, D))).cuda() for _ in range(4)]
+    want = [decode(cache, q.cpu()) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [workspace(crisp.decode_workspace_size(cache, 28, 2)) for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        for s, ws in zip(streams, spaces):
+            with torch.cuda.stream(s):
+                q = qs[i % 4].clone()
+                out = torch.empty_like(q)
+                crisp.decode_attention(cache, q, out, ws)
+                got.append((i % 4, q, out, out.clone()))
+    torch.cuda.synchronize()
+    assert all(crisp.read_status(ws) == 0 for ws in spaces)
+    assert all(torch.equal(want[i], seen) for i, _, _, seen in got)
 
 
 def test_decode_shared_pages_streams_graphs_and_in_place_weights():
