@@ -23,9 +23,9 @@
 // of K and V; a copy does 6.8). What it comes to elsewhere: 5 us before the
 // first product (launch, lengths, page table, first pages), 4 us behind the
 // last (the joining kernel), and a few waits at every item's end (1000
-// sequences of up to 1000 tokens: 250 us, 153 at the copy rate). With 17 to 32
+// sequences of up to 1000 tokens: 243 us, 153 at the copy rate). With 17 to 32
 // rows one CTA of four groups has the SM; its chain of 1850 cycles a tile is
-// longer than the memory's 1400 (28 rows, 128k tokens, 4 heads: 41 us against 20).
+// longer than the memory's 1400 (28 rows, 128k tokens, 4 heads: 39 us against 20).
 //
 // The work is the list of all tiles of the batch, item (sequence, kv head, row
 // chunk) by item; every CTA takes an equal run of it, so ragged batches stay

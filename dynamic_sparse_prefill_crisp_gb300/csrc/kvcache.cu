@@ -625,7 +625,7 @@ __device__ __forceinline__ void copies_wait() {
 // found through the list, so a page is three dependent reads and a write: the
 // copies of the next two pages are under way while one is packed (each thread
 // copies what it packs itself, so nothing but the maximum is shared). 512k ->
-// 128k tokens of 8 heads: 95 us, 79 at the copy rate (a kept row is 128 bytes
+// 128k tokens of 8 heads: 91 us, 79 at the copy rate (a kept row is 128 bytes
 // somewhere in its page); with four plain CTAs on an SM 105 us, and 120 us with
 // the codes scaled in fp32.
 constexpr int kStages = 3;
