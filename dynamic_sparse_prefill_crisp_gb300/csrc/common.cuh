@@ -141,7 +141,7 @@ struct DecodeLayout {
 struct EvictLayout {
   size_t list;         // int32 [batch][hkv][list_stride]  where the kept tokens' codes are (page * 128 + row)
   size_t list_stride;  // entries
-  size_t hist, state;  // long caches: the chunks' histograms, and what their CTAs know
+  size_t hist, from, total_bins, state;  // long caches: the chunks' and rows' histograms, and what the CTAs know
   size_t total;
 };
 EvictLayout evict_layout(const crisp_kv_cache& src, int keep);

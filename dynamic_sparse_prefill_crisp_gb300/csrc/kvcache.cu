@@ -222,31 +222,36 @@ __global__ void __launch_bounds__(kThreads, 4)
 // Which tokens stay: the `keep` largest of n keys, equal keys by lowest
 // position. Keys order as the weights do (32-bit integers; NaN above every
 // number), tokens that always stay above all. The keep-th largest key is found
-// digit by digit from the top (11 + 11 + 10 bits): a histogram of the keys that
+// digit by digit from the top (10 + 11 + 11 bits): a histogram of the keys that
 // match the digits found so far, then the digit in which the keep-th falls. A
 // last pass writes the kept positions in order.
 //
 // A cache of up to kChunk positions takes one CTA per sequence and kv head and
 // one launch (2175 tokens: 5.7 us, of it 3 in barriers and scans; the keys stay
 // in registers up to 8192). A longer one is cut into chunks of kChunk, a CTA
-// each and a launch per pass, so that a few long rows fill the chip: every
-// chunk's histogram goes to the workspace, and every CTA of the next pass adds
-// up its row's (3.5 us for 32 chunks). 8 rows of 512k tokens take 39 us this
-// way, 48 with a cluster of 16 CTAs per row (8 such clusters fill half the SMs).
+// each and a launch per pass, so that a few long rows fill the chip. The chunks'
+// first histograms go to the workspace and every CTA of the next pass adds up
+// its row's; the later ones, mostly zeros, are added to the row's totals, which
+// the first pass clears. The last pass needs to know what stands in the chunks
+// before its own: each leaves, for every last digit, how many of its keys are at
+// or above it. 8 rows of 512k tokens take TODO us this way, 39 when every pass
+// adds up all histograms, 48 with a cluster of 16 CTAs per row (8 such clusters
+// fill half the SMs).
 constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kPer = kBins / kSelThreads;  // bins of a thread
 constexpr int kAhead = 4;                  // loads of four keys a thread has in flight
 constexpr int kTurn = kSelThreads * 4;     // positions the block takes with one load a thread
 constexpr int kChunk = 2 * kAhead * kTurn;
-__host__ __device__ constexpr int digit_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
-__host__ __device__ constexpr uint32_t digit_mask(int pass) { return pass == 2 ? 1023u : 2047u; }
+constexpr int kFirstBins = 1024;           // of the first digit
+__host__ __device__ constexpr int digit_shift(int pass) { return pass == 0 ? 22 : pass == 1 ? 11 : 0; }
+__host__ __device__ constexpr uint32_t digit_mask(int pass) { return pass == 0 ? kFirstBins - 1u : kBins - 1u; }
 
 // What a chunk's CTA knows: the digits found, how many of the keys that match
-// them are still wanted, and how many keys above stand in earlier chunks.
+// them are still wanted, and how many of the chunk's keys are above them.
 struct SelState {
   uint32_t found;
-  int want, before, pad;
+  int want, above, pad;
 };
 
 struct SelArgs {
@@ -259,7 +264,9 @@ struct SelArgs {
   int32_t* list;
   int64_t new_cap, list_stride;
   int hkv, cap, keep, sink, recent, num_pages;
-  uint16_t* hist;       // [2][batch hkv][chunks][kBins]  (long caches)
+  uint16_t* hist;       // [batch hkv][chunks][kFirstBins]  (long caches)
+  uint16_t* from;       // [batch hkv][chunks][kBins]  keys whose last digit is that or above
+  int* total;           // [2][batch hkv][kBins]  the rows' second and third histograms
   SelState* state;      // [batch hkv][chunks]
   int chunks, rows;     // rows: batch hkv
   DevStatus* status;
@@ -335,7 +342,7 @@ struct SelShared {
   alignas(8) int hist[2][kBins];  // (and, in the last pass, a turn's kept positions)
   alignas(8) int tot[2][kAhead * kSelThreads / 32];
   int warp_tot[kSelThreads / 32];
-  int digit, above, equal_before;
+  int digit, above;
 };
 
 // The first turn's keys of [lo, hi).
@@ -348,12 +355,14 @@ __device__ __forceinline__ void load_first(const SelRow& r, int lo, int hi, floa
 }
 
 // Adds the keys of [lo, hi) that match `found` above digit `pass` to the
-// histogram h of that digit; v: the first turn's. Ends with a barrier.
+// histogram h of that digit; v: the first turn's. Ends with a barrier. Returns,
+// in the last pass, how many of this thread's keys are above those that match.
 template <int pass>
-__device__ __forceinline__ void count(const SelRow& r, int lo, int hi, uint32_t found, int* h, float4 (&v)[kAhead]) {
+__device__ __forceinline__ int count(const SelRow& r, int lo, int hi, uint32_t found, int* h, float4 (&v)[kAhead]) {
   for (int x = threadIdx.x; x < kBins; x += kSelThreads) h[x] = 0;
   __syncthreads();
   constexpr uint32_t fixed = pass == 0 ? 0u : ~0u << digit_shift(pass - 1);
+  int above = 0;
   for (int i0 = lo + static_cast<int>(threadIdx.x) * 4; i0 < hi; i0 += kTurn * kAhead) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -364,13 +373,15 @@ __device__ __forceinline__ void count(const SelRow& r, int lo, int hi, uint32_t 
       if (i + kTurn * kAhead < hi) v[u] = r.load4(i + kTurn * kAhead);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // a key of 0 counts only in the first pass, in bin 0, where no weight's key falls (-inf is in bin 3)
+        // a key of 0 counts only in the first pass, in bin 0, where no weight's key falls (-inf is in bin 1)
         if (pass == 0 || ((key[e] ^ found) & fixed) == 0u)
           atomicAdd(&h[(key[e] >> digit_shift(pass)) & digit_mask(pass)], 1);
+        if (pass == 2) above += key[e] > (found | ~fixed);
       }
     }
   }
   __syncthreads();
+  return above;
 }
 
 // The digit in which the want-th largest key falls; c: this thread's kPer bins
@@ -524,34 +535,39 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const __grid_con
   write_kept(a, r, sh, bg, 0, r.n, found, want, 0, 0, v);
 }
 
-// From the histograms of digit `pass` of all chunks of a row: the digit, and
-// how many keys above it (and equal to it, in sh.equal_before) stand before `chunk`.
-__device__ __forceinline__ void digest(const SelArgs& a, SelShared& sh, int bg, int n, int chunk, int pass,
-                                       SelState& st) {
-  const int tid = threadIdx.x, top = kBins - 1 - kPer * tid, chunks = (n + kChunk - 1) / kChunk;
-  const uint16_t* h = a.hist + (static_cast<int64_t>((pass & 1) * a.rows + bg) * a.chunks) * kBins + top - (kPer - 1);
-  int c[kPer] = {0, 0, 0, 0}, before[kPer] = {0, 0, 0, 0};
+// The first digit, from the histograms of all chunks of a row; two halves of
+// the block take every second chunk.
+__device__ __forceinline__ void digest_first(const SelArgs& a, SelShared& sh, int bg, int n, SelState& st) {
+  constexpr int kHalf = kSelThreads / 2;
+  static_assert(kFirstBins == kPer * kHalf && 2 * kFirstBins == kBins, "a half's threads have the bins among them");
+  const int tid = threadIdx.x, half = tid / kHalf, bin = kPer * (tid % kHalf), chunks = (n + kChunk - 1) / kChunk;
+  const uint16_t* h = a.hist + static_cast<int64_t>(bg) * a.chunks * kFirstBins + bin;
+  int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 8
-  for (int x = 0; x < chunks; ++x) {
-    const uint2 q = *reinterpret_cast<const uint2*>(h + static_cast<int64_t>(x) * kBins);
-    const int y[kPer] = {static_cast<int>(q.y >> 16), static_cast<int>(q.y & 0xffffu), static_cast<int>(q.x >> 16),
-                         static_cast<int>(q.x & 0xffffu)};
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      c[u] += y[u];
-      before[u] += x < chunk ? y[u] : 0;
-    }
+  for (int x = half; x < chunks; x += 2) {
+    const uint2 q = *reinterpret_cast<const uint2*>(h + static_cast<int64_t>(x) * kFirstBins);
+    sum.x += q.x & 0xffffu;
+    sum.y += q.x >> 16;
+    sum.z += q.y & 0xffffu;
+    sum.w += q.y >> 16;
   }
+  *reinterpret_cast<int4*>(&sh.hist[1][half * kFirstBins + bin]) = sum;
+  __syncthreads();
+  const int top = kBins - 1 - kPer * tid;
+  int c[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    c[u] = top < kFirstBins ? sh.hist[1][top - u] + sh.hist[1][kFirstBins + top - u] : 0;
+  pick(sh, c, 0, st.found, st.want);
+}
+
+// The second or third digit, from the row's totals.
+__device__ __forceinline__ void digest_total(const SelArgs& a, SelShared& sh, int bg, int pass, SelState& st) {
+  const int top = kBins - 1 - kPer * static_cast<int>(threadIdx.x);
+  const int4 q = *reinterpret_cast<const int4*>(a.total + (static_cast<int64_t>(pass - 1) * a.rows + bg) * kBins +
+                                                top - (kPer - 1));
+  const int c[kPer] = {q.w, q.z, q.y, q.x};
   pick(sh, c, pass, st.found, st.want);
-  int mine = 0;
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    if (top - u > sh.digit) mine += before[u];
-    if (top - u == sh.digit) sh.equal_before = before[u];
-  }
-  int sum;
-  block_scan(mine, sh.warp_tot, sum);
-  st.before += sum;
 }
 
 // Digit `pass` of one chunk.
@@ -560,26 +576,50 @@ __global__ void __launch_bounds__(kSelThreads, 2) chunk_kernel(const __grid_cons
   __shared__ SelShared sh;
   grid_dep_launch();
   grid_dep_wait();
-  const int chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
+  const int tid = threadIdx.x, chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
   const SelRow r(a, b, bg);
   const int lo = chunk * kChunk, hi = min(lo + kChunk, r.n);
   if (r.n <= a.keep || lo >= r.n) return;
   float4 v[kAhead];
   load_first(r, lo, hi, v);
+  const int64_t at = static_cast<int64_t>(bg) * a.chunks + chunk;
   SelState st{0u, a.keep, 0, 0};
-  if (pass > 0) {
-    SelState* keep = a.state + static_cast<int64_t>(bg) * a.chunks + chunk;
-    if (pass > 1) st = *keep;
-    __syncthreads();  // all have read it
-    digest(a, sh, bg, r.n, chunk, pass - 1, st);
-    if (threadIdx.x == 0) *keep = st;
+  if (pass == 0 && chunk == 0) {  // every row that goes on has a first chunk
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      *reinterpret_cast<int4*>(a.total + (static_cast<int64_t>(p) * a.rows + bg) * kBins + kPer * tid) =
+          make_int4(0, 0, 0, 0);
   }
-  count<pass>(r, lo, hi, st.found, sh.hist[0], v);
-  uint16_t* out = a.hist + (static_cast<int64_t>((pass & 1) * a.rows + bg) * a.chunks + chunk) * kBins;
-  const int4 x = *reinterpret_cast<const int4*>(&sh.hist[0][kPer * threadIdx.x]);
-  *reinterpret_cast<uint2*>(out + kPer * threadIdx.x) =
-      make_uint2(static_cast<uint32_t>(x.x) | static_cast<uint32_t>(x.y) << 16,
-                 static_cast<uint32_t>(x.z) | static_cast<uint32_t>(x.w) << 16);
+  if (pass == 1) digest_first(a, sh, bg, r.n, st);
+  if (pass == 2) {
+    st = a.state[at];
+    digest_total(a, sh, bg, 1, st);
+  }
+  const int above = count<pass>(r, lo, hi, st.found, sh.hist[0], v);
+  const int4 x = *reinterpret_cast<const int4*>(&sh.hist[0][kPer * tid]);
+  if (pass == 0) {
+    if (tid < kFirstBins / kPer)
+      *reinterpret_cast<uint2*>(a.hist + at * kFirstBins + kPer * tid) =
+          make_uint2(static_cast<uint32_t>(x.x) | static_cast<uint32_t>(x.y) << 16,
+                     static_cast<uint32_t>(x.z) | static_cast<uint32_t>(x.w) << 16);
+    return;
+  }
+  int* total = a.total + (static_cast<int64_t>(pass - 1) * a.rows + bg) * kBins + kPer * tid;
+  if (x.x != 0) atomicAdd(total, x.x);
+  if (x.y != 0) atomicAdd(total + 1, x.y);
+  if (x.z != 0) atomicAdd(total + 2, x.z);
+  if (x.w != 0) atomicAdd(total + 3, x.w);
+  if (pass == 2) {
+    const int sum = x.x + x.y + x.z + x.w;
+    int all;
+    const int from = sum - block_scan(sum, sh.warp_tot, all);  // minus what stands in the bins below
+    const int f0 = from + all, f1 = f0 - x.x, f2 = f1 - x.y, f3 = f2 - x.z;
+    *reinterpret_cast<uint2*>(a.from + at * kBins + kPer * tid) =
+        make_uint2(static_cast<uint32_t>(f0) | static_cast<uint32_t>(f1) << 16,
+                   static_cast<uint32_t>(f2) | static_cast<uint32_t>(f3) << 16);
+    block_scan(above, sh.warp_tot, st.above);
+  }
+  if (tid == 0) a.state[at] = st;
 }
 
 // The kept positions of one chunk.
@@ -587,20 +627,33 @@ __global__ void __launch_bounds__(kSelThreads, 2) chunk_kept_kernel(const __grid
   __shared__ SelShared sh;
   grid_dep_launch();
   grid_dep_wait();
-  const int chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
-  if (chunk == 0 && blockIdx.y == 0 && threadIdx.x == 0) write_len(a, b);
+  const int tid = threadIdx.x, chunk = blockIdx.x, b = blockIdx.z, bg = b * a.hkv + blockIdx.y;
+  if (chunk == 0 && blockIdx.y == 0 && tid == 0) write_len(a, b);
   const SelRow r(a, b, bg);
   const int lo = chunk * kChunk, hi = min(lo + kChunk, r.n);
   if (r.n <= a.keep) {
-    for (int i = lo + threadIdx.x; i < hi; i += kSelThreads) emit(a, bg, i, i, r.pages[i / kB], r.w[i]);
+    for (int i = lo + tid; i < hi; i += kSelThreads) emit(a, bg, i, i, r.pages[i / kB], r.w[i]);
     return;
   }
   if (lo >= r.n) return;
   float4 v[kAhead];
   load_first(r, lo, hi, v);
-  SelState st = a.state[static_cast<int64_t>(bg) * a.chunks + chunk];
-  digest(a, sh, bg, r.n, chunk, 2, st);
-  write_kept(a, r, sh, bg, lo, hi, st.found, st.want, st.before, sh.equal_before, v);
+  const int64_t row = static_cast<int64_t>(bg) * a.chunks;
+  SelState st = a.state[row + chunk];
+  digest_total(a, sh, bg, 2, st);
+  // keys above, and equal, in the chunks before: a thread each (64 at most)
+  static_assert(kMaxSeq / kChunk <= kSelThreads, "a thread for every chunk");
+  int gt = 0, eq = 0;
+  if (tid < chunk) {
+    const uint16_t* from = a.from + (row + tid) * kBins + sh.digit;
+    const int next = sh.digit + 1 < kBins ? from[1] : 0;
+    gt = a.state[row + tid].above + next;
+    eq = from[0] - next;
+  }
+  int all_gt, all_eq;
+  block_scan(gt, sh.warp_tot, all_gt);
+  block_scan(eq, sh.warp_tot, all_eq);
+  write_kept(a, r, sh, bg, lo, hi, st.found, st.want, all_gt, all_eq, v);
 }
 
 // Asynchronous copies of 16 or 4 bytes to shared memory; nothing is read and
@@ -766,7 +819,9 @@ EvictLayout evict_layout(const crisp_kv_cache& src, int keep) {
   size_t o = align_up(sizeof(DevStatus));
   L.list_stride = align_up(static_cast<size_t>(keep) * 4) / 4;
   L.list = o;  o = align_up(o + rows * L.list_stride * 4);
-  L.hist = o;  o = align_up(o + 2 * rows * chunks * kBins * sizeof(uint16_t));
+  L.hist = o;  o = align_up(o + rows * chunks * kFirstBins * sizeof(uint16_t));
+  L.from = o;  o = align_up(o + rows * chunks * kBins * sizeof(uint16_t));
+  L.total_bins = o; o = align_up(o + (chunks > 0 ? 2 * rows * kBins * sizeof(int) : 0));
   L.state = o; o = align_up(o + rows * chunks * sizeof(SelState));
   L.total = o;
   return L;
@@ -793,6 +848,8 @@ cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst
   a.recent = recent;
   a.num_pages = src.num_pages;
   a.hist = reinterpret_cast<uint16_t*>(ws + L.hist);
+  a.from = reinterpret_cast<uint16_t*>(ws + L.from);
+  a.total = reinterpret_cast<int*>(ws + L.total_bins);
   a.state = reinterpret_cast<SelState*>(ws + L.state);
   a.chunks = (a.cap + kChunk - 1) / kChunk;
   a.rows = src.batch * src.hkv;
