@@ -251,50 +251,64 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 }
 
 // Q' of kRows rows from rb on of a chunk whose first row is r0, by one warp: four
-// features a lane. All rows are asked for before the first is made.
+// features a lane, first in registers. All rows are asked for before the first
+// is made.
 template <int kRows>
-__device__ __forceinline__ void make_q(const Args& a, uint8_t* dst, float* qs, int b, int g, int r0, int rb) {
-  const int lane = threadIdx.x & 31;
-  uint2 w[kRows];
+struct QRows {
+  uint32_t hi[kRows], lo[kRows];
+  float scale;  // lane r: of row r, with scale * log2(e)
+
+  __device__ __forceinline__ void make(const Args& a, int b, int g, int r0, int rb) {
+    const int lane = threadIdx.x & 31;
+    uint2 w[kRows];
 #pragma unroll
-  for (int rr = 0; rr < kRows; ++rr) {
-    const int row = r0 + rb + rr;
-    w[rr] = make_uint2(0u, 0u);
-    if (row < a.rows) {
-      const int i = a.q_len == 1 ? 0 : row / a.group, h = g * a.group + row - i * a.group;
-      w[rr] = *reinterpret_cast<const uint2*>(a.q + b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
+    for (int rr = 0; rr < kRows; ++rr) {
+      const int row = r0 + rb + rr;
+      w[rr] = make_uint2(0u, 0u);
+      if (row < a.rows) {
+        const int i = a.q_len == 1 ? 0 : row / a.group, h = g * a.group + row - i * a.group;
+        w[rr] = *reinterpret_cast<const uint2*>(a.q + b * a.q_b + h * a.q_h + i * a.q_t + lane * 4);
+      }
+    }
+    scale = 0.f;
+#pragma unroll
+    for (int rr = 0; rr < kRows; ++rr) {
+      float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
+                    __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
+        amax = fmaxf(amax, fabsf(v[e]));                          // passes over NaN
+      }
+      const int e2 = scale_exponent(warp_max(amax));
+      const float inv = exp2_int(-e2);
+      hi[rr] = lo[rr] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
+        const uint16_t h2 = pack_e4m3x2(y0, y1);
+        float h0, h1;
+        unpack_e4m3x2(h2, h0, h1);
+        hi[rr] |= static_cast<uint32_t>(h2) << (8 * e);
+        lo[rr] |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
+      }
+      if (lane == rr) scale = exp2_int(e2) * a.c;
     }
   }
+  __device__ __forceinline__ void store(uint8_t* dst, float* qs, int rb) const {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int rr = 0; rr < kRows; ++rr) {
-    const int r = rb + rr;
-    float v[4] = {__uint_as_float(w[rr].x << 16), __uint_as_float(w[rr].x & 0xffff0000u),
-                  __uint_as_float(w[rr].y << 16), __uint_as_float(w[rr].y & 0xffff0000u)};
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (!isfinite(v[e])) v[e] = __int_as_float(0x7fffffff);  // the row's scores become NaN
-      amax = fmaxf(amax, fabsf(v[e]));                          // passes over NaN
+    for (int rr = 0; rr < kRows; ++rr) {
+      const int r = rb + rr;
+      // rows 16 (r / 8) + r % 8 and 8 further on; 16-byte chunks are swizzled by the row's low 3 bits
+      const uint32_t at = (r / 8 * 16 + r % 8) * 128 + (((lane >> 2) ^ (r % 8)) << 4) + (lane & 3) * 4;
+      *reinterpret_cast<uint32_t*>(dst + at) = hi[rr];
+      *reinterpret_cast<uint32_t*>(dst + 8 * 128 + at) = lo[rr];
     }
-    const int e2 = scale_exponent(warp_max(amax));
-    const float inv = exp2_int(-e2);
-    uint32_t hi = 0, lo = 0;
-#pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const float y0 = v[e] * inv, y1 = v[e + 1] * inv;
-      const uint16_t h2 = pack_e4m3x2(y0, y1);
-      float h0, h1;
-      unpack_e4m3x2(h2, h0, h1);
-      hi |= static_cast<uint32_t>(h2) << (8 * e);
-      lo |= static_cast<uint32_t>(pack_e4m3x2((y0 - h0) * kLo, (y1 - h1) * kLo)) << (8 * e);
-    }
-    // rows 16 (r / 8) + r % 8 and 8 further on; 16-byte chunks are swizzled by the row's low 3 bits
-    const uint32_t at = (r / 8 * 16 + r % 8) * 128 + (((lane >> 2) ^ (r % 8)) << 4) + (lane & 3) * 4;
-    *reinterpret_cast<uint32_t*>(dst + at) = hi;
-    *reinterpret_cast<uint32_t*>(dst + 8 * 128 + at) = lo;
-    if (lane == 0) qs[r] = exp2_int(e2) * a.c;
+    if (lane < kRows) qs[rb + lane] = scale;
   }
-}
+};
 
 template <int kWG, bool kScores>
 __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
@@ -584,13 +598,20 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
       x.next(pre, a, n - t);
       t += x.left;
       const int buf = item & 1, g = x.gc / a.chunks, r0 = (x.gc - g * a.chunks) * kR;
+      // the first rows are made while their buffer is still in use
+      constexpr int kAtOnce = kR < 16 ? kR : 16;
+      QRows<kAtOnce> q;
+      q.make(a, x.b, g, r0, 0);
       if (ok && !warp_wait(&sh.q_empty[buf], ((item >> 1) & 1) ^ 1, &sh.abort)) {
         if (lane == 0) fail(&sh.abort, a.status, 0x613);
         ok = false;
       }
       if (!ok) continue;  // every item is recorded all the same
-      constexpr int kAtOnce = kR < 16 ? kR : 16;
-      for (int rb = 0; rb < kR; rb += kAtOnce) make_q<kAtOnce>(a, sQ + buf * C::op, sh.qs[buf], x.b, g, r0, rb);
+      q.store(sQ + buf * C::op, sh.qs[buf], 0);
+      for (int rb = kAtOnce; rb < kR; rb += kAtOnce) {
+        q.make(a, x.b, g, r0, rb);
+        q.store(sQ + buf * C::op, sh.qs[buf], rb);
+      }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_n(&sh.q_full[buf], C::workers);
@@ -655,7 +676,9 @@ __global__ void __launch_bounds__(Cfg<kWG>::threads, Cfg<kWG>::per_sm)
     {
       // the first item's Q', two rows a warp
       const int g0 = x.gc / a.chunks;
-      make_q<2>(a, sQ, sh.qs[0], x.b, g0, (x.gc - g0 * a.chunks) * kR, warp * 2);
+      QRows<2> q;
+      q.make(a, x.b, g0, (x.gc - g0 * a.chunks) * kR, warp * 2);
+      q.store(sQ, sh.qs[0], warp * 2);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full[0]);
