@@ -786,7 +786,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int p = 0; p < kPasses; ++p) {
           const int row = row0 + p * kRowsAtOnce;
           if (row >= now.rows) continue;
-          *reinterpret_cast<uint4*>(codes + row * kD + col) = rescale16(st.codes[x][p][tid], s[x][p] * inv);
+          // A row of zeros does not raise the page's scale: old over new may pass the largest float, and
+          // zeros have to stay zeros (a code of another value needs 2^18 at most: the page holds it).
+          const float up = s[x][p] * inv, ratio = up > 0x1p127f ? 0x1p127f : up;
+          *reinterpret_cast<uint4*>(codes + row * kD + col) = rescale16(st.codes[x][p][tid], ratio);
         }
         if (tid == 0) (x ? dv : dk).scale[static_cast<int64_t>(now.id) * hkv + now.g] = sn;
       }
