@@ -107,19 +107,35 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
+// A tensor map of `rank` axes (the strides are the outer ones', in bytes), boxes
+// swizzled by 128 bytes, zeros outside.
+crisp_status encode_map(CUtensorMap* m, CUtensorMapDataType type, cuuint32_t rank, const void* ptr,
+                        const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return CRISP_ERR_CUDA;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  auto encode = [&]() {
+    return enc(m, type, rank, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // A host thread that has called nothing of CUDA's has no context, and this
+    // call, unlike a launch, does not give it its device's.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return CRISP_ERR_CUDA;
+    r = encode();
+  }
+  return r == CUDA_SUCCESS ? CRISP_OK : r == CUDA_ERROR_INVALID_VALUE ? CRISP_ERR_ALIGN : CRISP_ERR_CUDA;
+}
+
 // bf16 [heads][n][128] with element strides; boxes of 64 features x `rows`
 // tokens (one 128-byte swizzle row per token).
 crisp_status make_map(CUtensorMap* m, const void* ptr, int heads, int n, int64_t hs, int64_t ts, int rows = kB) {
-  EncodeTiled enc = encode_fn();
-  if (!enc) return CRISP_ERR_CUDA;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ts) * 2, static_cast<cuuint64_t>(hs) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? CRISP_OK : CRISP_ERR_ALIGN;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ts) * 2, static_cast<cuuint64_t>(hs) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box);
 }
 
 // The attention kernel's K and V maps: boxes of 64 tokens (a sub-block).
@@ -939,17 +955,11 @@ crisp_status check_decode(const crisp_kv_cache* c, int hq, int q_len) {
 
 // Whole pages of one head: [num_pages][hkv][128][128] bytes.
 crisp_status make_page_map(CUtensorMap* m, const void* ptr, const crisp_kv_cache& c) {
-  EncodeTiled enc = encode_fn();
-  if (!enc) return CRISP_ERR_CUDA;
-  cuuint64_t dims[4] = {kD, kB, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t dims[4] = {kD, kB, static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.num_pages)};
   // a single head's stride is not used, but has to be one the map accepts
-  cuuint64_t strides[3] = {kD, static_cast<cuuint64_t>(c.head_stride), static_cast<cuuint64_t>(c.page_stride)};
-  cuuint32_t box[4] = {kD, kB, 1, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? CRISP_OK : CRISP_ERR_ALIGN;
+  const cuuint64_t strides[3] = {kD, static_cast<cuuint64_t>(c.head_stride), static_cast<cuuint64_t>(c.page_stride)};
+  const cuuint32_t box[4] = {kD, kB, 1, 1};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, ptr, dims, strides, box);
 }
 
 }  // namespace

@@ -1,10 +1,12 @@
 """The paged 8-bit cache on the GPU at the edges of its values and of its use."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 import dynamic_sparse_prefill_crisp_gb300 as crisp
-from kv_helpers import B, Pools, page_exponent, round_codes, tokens_of
+from kv_helpers import B, D, Pools, page_exponent, round_codes, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,55 @@ def test_evict_keeps_zeros_of_pages_with_any_scale(exponents, beside):
             want = round_codes(rows / e)
             sign = np.where(want & 127, 255, 127)  # -0 and 0 are one value
             assert np.array_equal(codes[page, 0, :len(rows)] & sign, want & sign)
+
+
+# ------------------------------------------------------------- host threads
+def in_threads(calls):
+    """Runs the functions at once, a fresh host thread each; raises what one of them raised."""
+    start, errors = threading.Barrier(len(calls)), []
+
+    def run(f):
+        try:
+            start.wait()
+            f()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(f,)) for f in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if errors:
+        raise errors[0]
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_the_first_call_of_a_host_thread(own_stream):
+    # Threads that have called nothing of CUDA's before: no context is current there.
+    gen = torch.Generator(device="cuda").manual_seed(63)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    pools = Pools(8, 2)
+    cache = pools.cache([[0, 3], [5, 1]], [200, 256])
+    k, v, q = rand(2, 2, 256, D), rand(2, 2, 256, D), rand(2, 8, 1, D)
+    ws = [workspace(crisp.decode_workspace_size(cache, 8)) for _ in range(2)]
+    crisp.kv_append(cache, k, v, ws[0], new_lens=cache.tensors[5])
+    want = torch.empty_like(q)
+    crisp.decode_attention(cache, q, want, ws[0])
+    lq, lk, lv = rand(4, 1000, D), rand(1, 1000, D), rand(1, 1000, D)
+    layer_want = crisp.attention(lq, lk, lv)
+    shape = crisp.make_shape(4, 1, 1000, lq, lk, lq)
+    lws = workspace(crisp.layer_workspace_size(shape))
+    layer_out, out = torch.zeros_like(lq), torch.zeros_like(q)
+    stream = torch.cuda.Stream() if own_stream else None
+    params = crisp.params_default()
+    torch.cuda.synchronize()
+    for call in (lambda: crisp.decode_attention(cache, q, out, ws[1], stream=stream),
+                 lambda: crisp.prefill_layer(shape, params, lq, lk, lv, layer_out, lws, stream=stream)):
+        in_threads([call])
+    torch.cuda.synchronize()
+    assert crisp.read_status(ws[1]) == 0 and crisp.read_status(lws) == 0
+    assert torch.equal(out, want) and torch.equal(layer_out, layer_want)
