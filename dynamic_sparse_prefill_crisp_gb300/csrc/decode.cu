@@ -1115,12 +1115,13 @@ int groups_of(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 template <int kWG, bool kScores>
 cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {
   using C = Cfg<kWG>;
-  const uint32_t smem = C::smem + (a.batch + 1) * 4;
-  cudaError_t e =
-      cudaFuncSetAttribute(decode_kernel<kWG, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit belongs to the kernel, not to the call: every call sets the same
+  // one, so that host threads with other batches do not lower it in between.
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<kWG, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::smem + (kMaxBatch + 1) * 4);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_kernel<kWG, kScores>, dim3(static_cast<unsigned>(a.ctas)), C::threads, smem, st,
-                          maps.k, maps.v, a);
+  return launch_dependent(decode_kernel<kWG, kScores>, dim3(static_cast<unsigned>(a.ctas)), C::threads,
+                          C::smem + (a.batch + 1) * 4, st, maps.k, maps.v, a);
 }
 template <int kWG>
 cudaError_t launch_groups(const KvMaps& maps, const Args& a, cudaStream_t st) {

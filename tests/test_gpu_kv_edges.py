@@ -111,3 +111,40 @@ def test_the_first_call_of_a_host_thread(own_stream):
     torch.cuda.synchronize()
     assert crisp.read_status(ws[1]) == 0 and crisp.read_status(lws) == 0
     assert torch.equal(out, want) and torch.equal(layer_out, layer_want)
+
+
+def again_and_again(f, args, times):
+    """The C call, with its arguments made beforehand: threads meet inside the library as often as they can."""
+    def run():
+        for _ in range(times):
+            rc = f(*args)
+            assert rc == 0, rc
+    return run
+
+
+def test_host_threads_decode_batches_of_any_size_at_once():
+    # Each thread has a cache, stream, workspace and outputs of its own; only the
+    # batch, and with it the shared memory that a launch asks for, differs.
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    jobs, calls = [], []
+    for hq, batch in [(2, 1), (2, 1024)] * 4 + [(16, 1), (16, 1024), (28, 1), (28, 1024)]:
+        pools = Pools(batch + 2, 1)
+        for t in (pools.k, pools.v):
+            t.copy_(torch.randint(0, 127, t.shape, generator=gen, device="cuda", dtype=torch.uint8))
+        for t in (pools.ks, pools.vs):
+            t.fill_(2.0 ** -8)
+        cache = pools.cache([[b + 1] for b in range(batch)], [77] + [0] * (batch - 2) + [5] * (batch > 1))
+        q = torch.randn((batch, hq, 1, D), generator=gen, device="cuda").to(torch.bfloat16)
+        ws = workspace(crisp.decode_workspace_size(cache, hq))
+        want, out, stream = torch.empty_like(q), torch.zeros_like(q), torch.cuda.Stream()
+        crisp.decode_attention(cache, q, want, ws)
+        qt, ot = (crisp.Tokens(t.data_ptr(), *t.stride()[:3]) for t in (q, out))
+        jobs.append((cache, q, out, ws, want, stream))
+        calls.append(again_and_again(crisp.lib().crisp_decode_attention,
+                                     (cache, hq, 1, 0.0, qt, ot, None, None, ws.data_ptr(), ws.numel(),
+                                      stream.cuda_stream), 4000))
+    torch.cuda.synchronize()
+    in_threads(calls)
+    torch.cuda.synchronize()
+    for _, _, out, ws, want, _ in jobs:
+        assert crisp.read_status(ws) == 0 and torch.equal(out, want)
