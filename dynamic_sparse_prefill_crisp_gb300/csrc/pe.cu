@@ -598,7 +598,12 @@ cudaError_t launch_select_pe(const crisp_shape& s, const crisp_params& p, const 
   const bool in_shared = nb <= kPeRowsInShared;
   const int smem = 8 * pe_warp_layout(nb, in_shared).bytes;
   auto kernel = in_shared ? select_pe_kernel<true> : select_pe_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit belongs to the kernel, not to the call: every call sets the one
+  // of the longest row, so that host threads with other lengths do not lower it
+  // in between.
+  const int longest = in_shared ? kPeRowsInShared : kMaxBlocks;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       8 * pe_warp_layout(longest, in_shared).bytes);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(s.hq) * nb;
   kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, smem, st>>>(pbar, route, s.hq, nb, p.pe_mode, p.gamma_num,

@@ -148,3 +148,29 @@ def test_host_threads_decode_batches_of_any_size_at_once():
     torch.cuda.synchronize()
     for _, _, out, ws, want, _ in jobs:
         assert crisp.read_status(ws) == 0 and torch.equal(out, want)
+
+
+def test_host_threads_select_blocks_of_any_length_at_once():
+    # The prefill's block selection, whose launches ask for shared memory by the length.
+    gen = torch.Generator(device="cuda").manual_seed(64)
+    jobs, calls, params = [], [], crisp.params_default()
+    for n in [256, 128 * 1000] * 4 + [128 * 1100, 128 * 2000]:
+        nb = n // B
+        x = torch.empty((1, n, D), dtype=torch.bfloat16, device="cuda")
+        shape = crisp.make_shape(1, 1, n, x, x, x)
+        pbar = torch.softmax(torch.randn((1, nb, nb), generator=gen, device="cuda"), -1)
+        route = torch.zeros(1, dtype=torch.uint8, device="cuda")
+        ws = workspace(crisp.workspace_size(shape))
+        bits = torch.zeros((1, nb, (nb + 31) // 32), dtype=torch.int32, device="cuda")
+        want = torch.zeros_like(bits)
+        crisp.select_pe(shape, params, pbar, route, want, ws)
+        stream = torch.cuda.Stream()
+        jobs.append((pbar, route, bits, ws, want, stream))
+        calls.append(again_and_again(crisp.lib().crisp_select_pe,
+                                     (shape, params, pbar.data_ptr(), route.data_ptr(), bits.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), stream.cuda_stream), 4000))
+    torch.cuda.synchronize()
+    in_threads(calls)
+    torch.cuda.synchronize()
+    for _, _, bits, ws, want, _ in jobs:
+        assert crisp.read_status(ws) == 0 and torch.equal(bits, want)
