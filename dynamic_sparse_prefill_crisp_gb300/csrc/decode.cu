@@ -1093,10 +1093,12 @@ __global__ void __launch_bounds__(kWeightThreads)
   for (int r = 0; r < a.rows; ++r) {
     const float4 s = __ldcs(reinterpret_cast<const float4*>(sc + r * cap));
     const float e = lse[r];
-    p.x += ex2_approx(s.x - e);
-    p.y += ex2_approx(s.y - e);
-    p.z += ex2_approx(s.z - e);
-    p.w += ex2_approx(s.w - e);
+    // a key that the row does not see (-inf) has no weight from it, even where the row's sum is NaN
+    auto weight = [&](float x) { return x == -INFINITY ? 0.f : ex2_approx(x - e); };
+    p.x += weight(s.x);
+    p.y += weight(s.y);
+    p.z += weight(s.z);
+    p.w += weight(s.w);
   }
   w.x += p.x;
   w.y += p.y;

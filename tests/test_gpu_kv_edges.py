@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dynamic_sparse_prefill_crisp_gb300 as crisp
-from kv_helpers import B, D, Pools, page_exponent, round_codes, tokens_of
+from kv_helpers import B, D, Pools, attention, fill, page_exponent, round_codes, shuffled_table, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,35 @@ def test_host_threads_select_blocks_of_any_length_at_once():
     torch.cuda.synchronize()
     for _, _, bits, ws, want, _ in jobs:
         assert crisp.read_status(ws) == 0 and torch.equal(bits, want)
+
+
+# ----------------------------------------------------------- non-finite rows
+@pytest.mark.parametrize("hq,hkv,q_len,lens", [(4, 2, 3, [130, 129, 128, 2, 1, 0]), (2, 1, 16, [300, 130, 9]),
+                                               (32, 1, 2, [257, 1]), (40, 1, 2, [200])])
+def test_weights_of_keys_that_a_non_finite_row_does_not_see(hq, hkv, q_len, lens):
+    # The first token's first head is NaN (or infinite): its softmax, and with it the
+    # weight of every key that it sees, is NaN. The last q_len - 1 keys it does not see.
+    rng = np.random.default_rng(65)
+    pages = max(1, max(-(-n // B) for n in lens))
+    table, num = shuffled_table(rng, len(lens), pages)
+    pools = Pools(num, hkv)
+    fill(pools, table, lens, rng)
+    cache = pools.cache(table, lens)
+    q = torch.from_numpy(rng.standard_normal((len(lens), hq, q_len, D))).to(torch.bfloat16)
+    _, _, w, wtol = attention(pools.host(), table, lens, q.double().numpy())
+    for bad in (float("nan"), float("inf")):
+        q[:, 0, 0, 7] = bad
+        w_in = torch.rand((len(lens), hkv, cache.max_pages * B), generator=torch.Generator().manual_seed(1)).cuda()
+        w_out = torch.full_like(w_in, -7.0)
+        qd = q.cuda()
+        ws = workspace(crisp.decode_workspace_size(cache, hq, q_len, True))
+        crisp.decode_attention(cache, qd, torch.empty_like(qd), ws, w_in, w_out)
+        assert crisp.read_status(ws) == 0
+        got, base = w_out.double().cpu().numpy(), w_in.double().cpu().numpy()
+        for b, n in enumerate(lens):
+            seen = max(n - (q_len - 1), 0)
+            assert np.isnan(got[b, 0, :seen]).all() and (got[b, :, n:] == -7.0).all()
+            for g in range(hkv):
+                lo = seen if g == 0 else 0
+                err = np.abs(got[b, g, lo:n] - base[b, g, lo:n] - w[b, g, lo:n])
+                assert (err <= wtol[b, g, lo:n] + 2.0 ** -24 * np.abs(got[b, g, lo:n])).all()
