@@ -10,11 +10,18 @@
 // K and V go from HBM by TMA to shared memory and into the tensor cores as
 // they are: nothing dequantises them. The other operand is made of two e4m3
 // pieces, x = hi + lo / 16 (for eight rows, columns r and 8 + r of 16). A bf16 q
-// at a power-of-two row scale is exactly that sum, down to 2^-14 of the row's
-// largest element. p, scaled to 256 at the step's maximum, goes through fp16:
-// it is off by at most 2^-11 of itself for that and 2^-9 for the pieces, less
-// than a bf16 p. O^T is read back every tile, so that page scales and the
-// running maximum act in fp32, and a tile of small p is as exact as any other.
+// at a power-of-two row scale is exactly that sum, down to 2^-13 of the row's
+// largest element (the smallest step of lo / 16 is 2^-13, the largest element
+// at least 224). p, scaled to 256 at the step's maximum, goes through fp16: it
+// is off by at most 2^-11 of itself for that and 2^-9 for the pieces, less than
+// a bf16 p, but by no less than half of that smallest step, 2^-22 of the
+// maximum: a p below 2^-14 of its step's largest has fewer bits in the product
+// (in l and in the weights it has them all). What that leaves out is at most
+// 2^-22 |v| a key, seen only where the large p stand before a V near zero. A
+// third piece would be 32 columns where there are 16 (M = 128 takes them by
+// 16), and 32 rows have all of TMEM in use. O^T is read back every tile, so
+// that page scales and the running maximum act in fp32, and a step of small p
+// is as exact as any other.
 //
 // Two tiles of an item make a step: what takes time between a step's scores and
 // its P' is a chain of waits (one tile at a time took 2300 cycles, where the

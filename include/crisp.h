@@ -518,8 +518,14 @@ CRISP_API crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_
  * may be the same array; entries at or past lens[b] are left as they were).
  * q, out: bf16 [batch][hq][q_len][128], 1 <= q_len <= 16, hq % hkv == 0;
  * weights: fp32 [batch][hkv][128 * max_pages], contiguous, 16-byte aligned.
- * Precision: q is held as two e4m3 pieces (exact down to 2^-14 of the row's
- * largest element), p as two (off by less than 2^-8 of itself); products and
+ * Precision: q is held as two e4m3 pieces, exact down to 2^-13 of the row's
+ * largest element and below that off by at most 2^-21 of it. p is held as two
+ * in the product with V, off by at most 2^-8 of itself or, where that is more,
+ * 2^-22 of the row's largest p among the keys of the product (256 at most, in
+ * two neighbouring pages): a p behind a neighbour that is 2^14 times as large
+ * reaches out with fewer bits, at 2^-22 of it as zero, which shows in out only
+ * where V of the large one is near zero. The sums and the weights count every p
+ * in full. Products and
  * sums are fp32. Limits: (hq / hkv) * q_len <= 1024, and batch * hkv * max_pages
  * * ceil((hq / hkv) * q_len / 32) < 2^31 (else CRISP_ERR_SHAPE). The result does
  * not depend on timing: the same call gives the same bits. */

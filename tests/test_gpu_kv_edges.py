@@ -206,3 +206,54 @@ def test_weights_of_keys_that_a_non_finite_row_does_not_see(hq, hkv, q_len, lens
                 lo = seen if g == 0 else 0
                 err = np.abs(got[b, g, lo:n] - base[b, g, lo:n] - w[b, g, lo:n])
                 assert (err <= wtol[b, g, lo:n] + 2.0 ** -24 * np.abs(got[b, g, lo:n])).all()
+
+
+# ------------------------------------------------------- small weights beside large ones
+@pytest.mark.parametrize("n", [3, 128, 200, 256, 1000])
+@pytest.mark.parametrize("sink_v", ["zero", "plain"])
+def test_decode_small_weights_beside_a_large_one(n, sink_v):
+    # Rows whose first key stands 2 to 24 nats above all others, with V = 0 there:
+    # what the row puts out comes from the small p alone.
+    # Tolerance: kv_helpers.attention's, and for each key 2^-22 of the row's largest p
+    # among the keys of its product (256 at most: within 255 positions), times |v|.
+    # That is half the smallest step of the second piece: e4m3's 2^-9, over its scale
+    # 16, over 2, over the 256 that the largest p is scaled to.
+    rng = np.random.default_rng(66)
+    gaps = [2, 6, 8, 10, 12, 13, 14, 15, 16, 17, 20, 24]
+    hq = len(gaps)
+    table, num = shuffled_table(rng, 1, -(-n // B))
+    pools = Pools(num, 1)
+    fill(pools, table, [n], rng)
+    k, v, ks, vs = pools.host()
+    first = table[0][0]
+    # feature 0 carries the gap: 64 at the first key, 0 elsewhere
+    for p in table[0]:
+        k[p, 0, :, 0] = 0
+        k[p, 0, :, 1:] = round_codes(rng.standard_normal((B, D - 1)))
+        ks[p, 0] = 0.25
+    k[first, 0, 0, 0] = round_codes(np.array([256.0]))[0]
+    k[first, 0, 0, 1:] = 0
+    if sink_v == "zero":
+        v[first, 0, 0] = 0
+    for t, a in zip((pools.k, pools.v, pools.ks, pools.vs), (k, v, ks, vs)):
+        t.copy_(torch.from_numpy(a))
+    q = rng.standard_normal((1, hq, 1, D)) * 0.25
+    q[0, :, 0, 0] = np.array(gaps) / 64.0
+    q = torch.from_numpy(q).to(torch.bfloat16)
+    cache = pools.cache(table, [n])
+    host = pools.host()
+    want, tol, w, wtol = attention(host, table, [n], q.double().numpy(), scale=1.0)
+    keys, vals = tokens_of(host, table[0], n, 0)
+    for h in range(hq):
+        s = keys @ q[0, h, 0].double().numpy()
+        p = np.exp(s - s.max()) / np.exp(s - s.max()).sum()
+        top = np.array([p[max(0, j - 255):j + 256].max() for j in range(n)])
+        tol[0, h, 0] += 2.0 ** -22 * (top @ np.abs(vals))
+    qd = q.cuda()
+    out, weights = torch.full_like(qd, float("nan")), torch.zeros((1, 1, cache.max_pages * B), device="cuda")
+    ws = workspace(crisp.decode_workspace_size(cache, hq, 1, True))
+    crisp.decode_attention(cache, qd, out, ws, None, weights, scale=1.0)
+    assert crisp.read_status(ws) == 0
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
+    got = weights.double().cpu().numpy()[:, :, :n]  # the weights have no such floor
+    assert (np.abs(got - w[:, :, :n]) <= wtol[:, :, :n] + 2.0 ** -24 * np.abs(got)).all()
