@@ -485,7 +485,8 @@ def decode_attention(cache, q, out, ws, weights_in=None, weights_out=None, scale
     """Attention of the last q_len tokens of every sequence over the cache: q,
     out bf16 [batch][hq][q_len][128]. With weights_out (fp32 [batch][hkv][128 *
     max_pages]) each key's weight, summed over the kv head's rows, is added to
-    weights_in's (None: zeros; may be the same tensor)."""
+    weights_in's (None: zeros; may be the same tensor). Entries past a length are
+    left alone: weights that accumulate start as zeros throughout."""
     _need(q.dim() == 4, "decode_attention: q must be [batch][hq][q_len][128]")
     _, hq, q_len, _ = q.shape
     qt = _tokens("decode_attention: q", q, cache, hq, q_len)
@@ -502,7 +503,8 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
     """Copies at most `keep` tokens of every sequence and kv head -- the first
     `sink`, the last `recent`, and those of largest weight -- into new_cache's
     pages, in their order, and sets its lens. new_weights (fp32) and kept (int32,
-    old positions) are [batch][hkv][128 * new_cache.max_pages]."""
+    old positions) are [batch][hkv][128 * new_cache.max_pages], written below the
+    new lengths only: new_weights that decoding goes on with start as zeros."""
     f32, i32 = cache.tensors[2].dtype, cache.tensors[5].dtype
     w = _rows("kv_evict: weights", weights, cache, f32)
     new_w = _rows("kv_evict: new_weights", new_weights, new_cache, f32)

@@ -40,9 +40,10 @@
  *    out) are recorded in the workspace status word; read it with
  *    crisp_read_status. No C++ exception crosses this boundary.
  *  - Fixed sizes: head_dim = 128, block = 128 tokens, batch 1 (a batch is a
- *    loop over calls). seq_len = n <= 2^20, any n: blocks are aligned at
- *    token 0, nb = ceil(n/128), and when 128 does not divide n the last block
- *    is short (n - 128*(nb-1) tokens). The method's steps (A1..A7) need
+ *    loop over calls; the cache calls take one). seq_len = n <= 2^20, any n:
+ *    blocks are aligned at token 0, nb = ceil(n/128), and when 128 does not
+ *    divide n the last block is short (n - 128*(nb-1) tokens). The method's
+ *    steps (A1..A7) need
  *    n >= 256 (the sink block and at least one more); attention, the whole
  *    layer and the workspace sizes take any n >= 0, and n = 0 (an empty
  *    input) launches nothing and returns CRISP_OK.
@@ -460,9 +461,9 @@ CRISP_API crisp_status crisp_prefill_layer_host(crisp_host_pipeline* pipeline, c
  *
  * lens[b] counts the tokens held, the ones being appended or asked about
  * included: advance it, then append, then attend. Rows of a page at or past
- * lens[b] may hold anything. batch <= 1024, max_pages <= 8192, num_pages <
- * 2^24, batch * hkv * max_pages < 2^31 (else CRISP_ERR_SHAPE). k and v and
- * their strides are 16-byte aligned, the other pointers 4-byte aligned. */
+ * lens[b] may hold anything. batch <= 1024, hkv <= 4096, max_pages <= 8192,
+ * num_pages < 2^24, batch * hkv * max_pages < 2^31 (else CRISP_ERR_SHAPE). k and
+ * v and their strides are 16-byte aligned, the other pointers 4-byte aligned. */
 typedef struct crisp_kv_cache {
   int32_t batch;        /* sequences */
   int32_t hkv;          /* key/value heads */
@@ -481,7 +482,8 @@ typedef struct crisp_kv_cache {
 } crisp_kv_cache;
 
 /* bf16 [batch][heads][tokens][128] with element strides (the 128 features
- * contiguous): the pointer 16-byte aligned, strides multiples of 8. */
+ * contiguous): the pointer 16-byte aligned, strides multiples of 8 and at least
+ * 128 (that of an axis of one entry is not used). */
 typedef struct crisp_tokens {
   const void* data;
   int64_t batch_stride, head_stride, tok_stride;
@@ -516,6 +518,8 @@ CRISP_API crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_
  *                g and the tokens i of softmax_j(s),     j < lens[b],
  * the second only with weights_out (weights_in NULL counts as zeros; the two
  * may be the same array; entries at or past lens[b] are left as they were).
+ * No call clears an entry: where weights accumulate from call to call, the
+ * caller sets those at or past lens[b] to zero before tokens are appended there.
  * q, out: bf16 [batch][hq][q_len][128], 1 <= q_len <= 16, hq % hkv == 0;
  * weights: fp32 [batch][hkv][128 * max_pages], contiguous, 16-byte aligned.
  * Precision: q is held as two e4m3 pieces, exact down to 2^-13 of the row's
@@ -525,10 +529,10 @@ CRISP_API crisp_status crisp_kv_append(const crisp_kv_cache* cache, const crisp_
  * two neighbouring pages): a p behind a neighbour that is 2^14 times as large
  * reaches out with fewer bits, at 2^-22 of it as zero, which shows in out only
  * where V of the large one is near zero. The sums and the weights count every p
- * in full. Products and
- * sums are fp32. Limits: (hq / hkv) * q_len <= 1024, and batch * hkv * max_pages
- * * ceil((hq / hkv) * q_len / 32) < 2^31 (else CRISP_ERR_SHAPE). The result does
- * not depend on timing: the same call gives the same bits. */
+ * in full. Products and sums are fp32. Limits: with rows = (hq / hkv) * q_len,
+ * rows <= 1024, hq <= 4096, batch * hkv * max_pages * ceil(rows / 32) < 2^31 and
+ * batch * hkv * (rows + max_pages) < 2^31 (else CRISP_ERR_SHAPE). The result
+ * does not depend on timing: the same call gives the same bits. */
 CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32_t hq, int32_t q_len, float scale,
                                               const crisp_tokens* q, const crisp_tokens* out,
                                               const float* weights_in, float* weights_out, void* ws, size_t ws_bytes,
@@ -542,10 +546,12 @@ CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32
  * order, to positions 0, 1, .. of dst: each of its pages gets the scale its
  * values need, codes rounded again where that differs. dst->lens[b] = min(n,
  * keep). dst->lens is not src->lens. dst may share the pools with src (k, v,
- * scales); its table's pages must then not stand in any src table. new_weights fp32 [batch][hkv][128 *
- * dst->max_pages] (16-byte aligned) and kept int32 [batch][hkv][128 *
- * dst->max_pages] (each kept token's old position) are written below the new
- * length; either may be NULL. 1 <= keep <= 128 * dst->max_pages, sink + recent
+ * scales); its table's pages must then not stand in any src table. new_weights
+ * fp32 [batch][hkv][128 * dst->max_pages] (16-byte aligned) and kept int32
+ * [batch][hkv][128 * dst->max_pages] (each kept token's old position) are
+ * written below the new length and left as they were from there on (so
+ * new_weights starts as zeros, if decoding goes on with it); either may be
+ * NULL. 1 <= keep <= 128 * dst->max_pages, sink + recent
  * <= keep. weights: as for crisp_decode_attention, not the same array as
  * new_weights. */
 CRISP_API crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst, const float* weights,

@@ -1,4 +1,6 @@
 """The paged 8-bit cache on the GPU at the edges of its values and of its use."""
+import os
+import re
 import threading
 
 import numpy as np
@@ -9,6 +11,8 @@ import dynamic_sparse_prefill_crisp_gb300 as crisp
 from kv_helpers import B, D, Pools, attention, fill, page_exponent, round_codes, shuffled_table, tokens_of
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def workspace(nbytes):
@@ -257,3 +261,40 @@ def test_decode_small_weights_beside_a_large_one(n, sink_v):
     assert (np.abs(out.double().cpu().numpy() - want) <= tol).all()
     got = weights.double().cpu().numpy()[:, :, :n]  # the weights have no such floor
     assert (np.abs(got - w[:, :, :n]) <= wtol[:, :, :n] + 2.0 ** -24 * np.abs(got)).all()
+
+
+# ------------------------------------------------------------------ the example
+def test_the_documented_example_of_the_cache():
+    # The two blocks of the README, as they stand there, with memory that starts as
+    # NaN; then a token over the smaller cache. Each weight is a share of a sum of 1.
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
+    blocks = [b for b in blocks if "make_kv_cache" in b]
+    assert len(blocks) == 2
+    batch, hq, hkv, n, max_pages = 2, 8, 2, 4500, 40
+    gen = torch.Generator(device="cuda").manual_seed(67)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    names = dict(torch=torch, crisp=crisp, batch=batch, hq=hq, hkv=hkv, n=n, max_pages=max_pages,
+                 pages=batch * (max_pages + 50), k=rand(batch, hkv, n, D), v=rand(batch, hkv, n, D),
+                 k_new=rand(batch, hkv, 1, D), v_new=rand(batch, hkv, 1, D), q=rand(batch, hq, 1, D))
+    names["out"] = torch.empty_like(names["q"])
+    torch.use_deterministic_algorithms(True, warn_only=True)  # fills torch.empty
+    try:
+        for b in blocks:
+            exec(b, names)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    weights, small, small_weights, ws = (names[x] for x in ("weights", "small", "small_weights", "ws"))
+    rows = hq // hkv
+    assert torch.allclose(weights.double().sum(-1), torch.full((), float(rows), dtype=torch.float64, device="cuda"), rtol=1e-5)
+    assert (weights[..., n + 1:] == 0).all() and small.tensors[5].tolist() == [4096] * batch
+    before = small_weights.double().sum(-1)
+    small.tensors[5].add_(1)
+    crisp.kv_append(small, names["k_new"], names["v_new"], ws)
+    crisp.decode_attention(small, names["q"], names["out"], ws, small_weights, small_weights)
+    assert crisp.read_status(ws) == 0 and crisp.read_status(names["ws2"]) == 0
+    assert torch.isfinite(names["out"].float()).all()
+    assert torch.allclose(small_weights.double().sum(-1), before + rows, rtol=1e-5)
+    assert (small_weights[..., 4096] > 0).all() and (small_weights[..., 4097:] == 0).all()
