@@ -265,8 +265,8 @@ def test_decode_small_weights_beside_a_large_one(n, sink_v):
 
 # ------------------------------------------------------------------ the example
 def test_the_documented_example_of_the_cache():
-    # The two blocks of the README, as they stand there, with memory that starts as
-    # NaN; then a token over the smaller cache. Each weight is a share of a sum of 1.
+    # The two blocks of the user's guide, as they stand there, with memory that starts
+    # as NaN; then a token over the smaller cache. A row's weights sum to 1.
     blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
     blocks = [b for b in blocks if "make_kv_cache" in b]
     assert len(blocks) == 2
