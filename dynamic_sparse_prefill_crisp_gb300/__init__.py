@@ -30,7 +30,7 @@ def map_ld(n: int) -> int:
 
 STATUS_NAMES = {0: "CRISP_OK", 1: "CRISP_ERR_INVALID_ARG", 2: "CRISP_ERR_SHAPE", 3: "CRISP_ERR_ALIGN",
                 4: "CRISP_ERR_WORKSPACE", 5: "CRISP_ERR_CUDA", 6: "CRISP_ERR_TIMEOUT", 7: "CRISP_ERR_DEVICE",
-                8: "CRISP_ERR_BOUNDS"}
+                8: "CRISP_ERR_BOUNDS", 9: "CRISP_ERR_PAGES"}
 PE_GAMMA, PE_NOISE = 0, 1
 ROUTE_CSTRUCT, ROUTE_JSD = 0, 1
 VS_NOISE, VS_GAMMA = 0, 1
@@ -80,6 +80,22 @@ class KVCache(ctypes.Structure):
 class Tokens(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("tok_stride", ctypes.c_int64)]
+
+
+class KVStep(ctypes.Structure):
+    """What kv_reserve finds out for a step (make_kv_step); cu_new, cu_all, slots,
+    positions, runs and all_slots are its int32 tensors."""
+    _fields_ = [("max_new", ctypes.c_int32), ("max_all", ctypes.c_int32), ("_cu_new", ctypes.c_void_p),
+                ("_cu_all", ctypes.c_void_p), ("_slots", ctypes.c_void_p), ("_positions", ctypes.c_void_p),
+                ("_runs", ctypes.c_void_p), ("_all_slots", ctypes.c_void_p)]
+
+
+class Packed(ctypes.Structure):
+    """A batch of packed sequences (make_packed); keeps its tensors alive."""
+    _fields_ = [("batch", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
+                ("max_k", ctypes.c_int32), ("scale", ctypes.c_float), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p)]
 
 
 def lib():
@@ -133,6 +149,11 @@ def load_library(path):
     L.crisp_decode_attention.argtypes = [P(KVCache), i32, i32, ctypes.c_float, P(Tokens), P(Tokens), vp, vp, vp, sz,
                                          st]
     L.crisp_kv_evict.argtypes = [P(KVCache), P(KVCache), vp, i32, i32, i32, vp, vp, vp, sz, st]
+    L.crisp_kv_reserve.argtypes = [P(KVCache), vp, vp, vp, vp, vp, P(KVStep), vp, sz, st]
+    L.crisp_kv_append_packed.argtypes = [P(KVCache), P(KVStep), P(Tokens), P(Tokens), vp, sz, st]
+    L.crisp_kv_gather.argtypes = [P(KVCache), vp, i32, vp, P(Tokens), P(Tokens), vp, sz, st]
+    L.crisp_packed_workspace_size.argtypes = [P(Packed), P(sz)]
+    L.crisp_packed_prefill.argtypes = [P(Packed), P(Tokens), P(Tokens), P(Tokens), P(Tokens), vp, sz, st]
     L.crisp_read_status.argtypes = [vp, st, P(ctypes.c_int)]
     L.crisp_status_string.argtypes = [ctypes.c_int]
     L.crisp_status_string.restype = ctypes.c_char_p
@@ -144,7 +165,9 @@ def load_library(path):
                  "crisp_layer_views_get", "crisp_prefill_layer", "crisp_read_status",
                  "crisp_host_pipeline_create", "crisp_host_pipeline_destroy", "crisp_prefill_layer_host",
                  "crisp_kv_append_workspace_size", "crisp_decode_workspace_size", "crisp_kv_evict_workspace_size",
-                 "crisp_kv_append", "crisp_decode_attention", "crisp_kv_evict", "crisp_wait_selftest"):
+                 "crisp_kv_append", "crisp_decode_attention", "crisp_kv_evict", "crisp_wait_selftest",
+                 "crisp_kv_reserve", "crisp_kv_append_packed", "crisp_kv_gather", "crisp_packed_workspace_size",
+                 "crisp_packed_prefill"):
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -512,6 +535,132 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
     st = _on_device(cache, stream, new_cache.tensors[0], weights, ws, new_weights, kept)
     _check(lib().crisp_kv_evict(ctypes.byref(cache), ctypes.byref(new_cache), w, keep, sink, recent, new_w, pos,
                                 ws.data_ptr(), _nbytes(ws), st), "crisp_kv_evict")
+
+
+def make_kv_step(cache, max_new, max_all=0) -> KVStep:
+    """Room for a step's maps (kv_reserve): at most max_new new tokens of the
+    cache's batch, and the slots of all its tokens where max_all is not 0 (the
+    most there can be). Allocates int32 tensors on the cache's device."""
+    import torch
+    _need(0 <= max_new <= 1 << 24 and 0 <= max_all <= 1 << 24, "make_kv_step: max_new and max_all must be 0 .. 2^24")
+    runs = min(max_new, max_new // B + 2 * cache.batch)
+    sizes = dict(cu_new=cache.batch + 1, cu_all=cache.batch + 1, slots=max_new, positions=max_new, runs=runs + 1,
+                 all_slots=max_all)
+    s = KVStep(max_new, max_all)
+    for name, n in sizes.items():
+        t = torch.zeros(n, dtype=torch.int32, device=cache.tensors[5].device)
+        setattr(s, name, t)
+        setattr(s, "_" + name, t.data_ptr() if n else None)
+    s.batch, s.device_index = cache.batch, cache.device_index
+    return s
+
+
+def _step_of(what, step, cache):
+    if step.batch != cache.batch or step.device_index != cache.device_index:
+        raise ValueError(f"{what}: the step was made for another batch or device")
+
+
+def _ints(what, t, n):
+    """The address of contiguous int32 [n] (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{n}]")
+    return t.data_ptr()
+
+
+def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, stream=None):
+    """Hands out pages for a step: sequence b keeps its first min(keep[b], lens[b])
+    tokens (None: all of them) and gets new_lens[b] more (None: none). Pages no
+    longer needed go back to the stack of free page ids (free_pages int32
+    [num_pages], num_free int32 [1]), missing ones come from it; the cache's table
+    and lens are brought up to date and `step` is filled (cu_new, cu_all, slots,
+    positions, runs, all_slots). If too few pages are free, or the step or a
+    sequence has no room, the status word says so and the step takes no tokens.
+    ws: kv_append_workspace_size bytes."""
+    _step_of("kv_reserve", step, cache)
+    free = _ints("kv_reserve: free_pages", free_pages, cache.num_pages)
+    num = _ints("kv_reserve: num_free", num_free, 1)
+    kept = _ints("kv_reserve: keep", keep, cache.batch)
+    new = _ints("kv_reserve: new_lens", new_lens, cache.batch)
+    st = _on_device(cache, stream, free_pages, num_free, ws, keep, new_lens)
+    _check(lib().crisp_kv_reserve(ctypes.byref(cache), cache.table, free, num, kept, new, ctypes.byref(step),
+                                  ws.data_ptr(), _nbytes(ws), st), "crisp_kv_reserve")
+
+
+def _packed_tokens(what, t, rows, heads):
+    """Packed [rows][heads][128] bf16."""
+    d = t.dtype
+    if t.shape != (rows, heads, D) or d.itemsize != 2 or str(d) != "torch.bfloat16":
+        raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {d} {tuple(t.shape)}")
+    i, h, e = t.stride()
+    if e != 1:
+        raise ValueError(f"{what}: the 128 features must be contiguous")
+    return Tokens(t.data_ptr(), 0, h, i)
+
+
+def kv_append_packed(cache, step, k_new, v_new, ws, stream=None):
+    """Writes a step's new tokens into the cache: bf16 [max_new][hkv][128], token i
+    at slots[i] (rows past the step's total are not read)."""
+    _step_of("kv_append_packed", step, cache)
+    kt = _packed_tokens("kv_append_packed: k_new", k_new, step.max_new, cache.hkv)
+    vt = _packed_tokens("kv_append_packed: v_new", v_new, step.max_new, cache.hkv)
+    st = _on_device(cache, stream, k_new, v_new, ws)
+    _check(lib().crisp_kv_append_packed(ctypes.byref(cache), ctypes.byref(step), ctypes.byref(kt), ctypes.byref(vt),
+                                        ws.data_ptr(), _nbytes(ws), st), "crisp_kv_append_packed")
+
+
+def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
+    """Reads cached tokens back: row i of k_out and v_out (bf16 [n][hkv][128]) from
+    slot slots[i] (int32 [n], e.g. a step's all_slots), exactly; count: int32 [1],
+    how many of the n rows there are (e.g. step.cu_all[-1:]; None: all). Rows of
+    negative slots are left alone."""
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    at = _ints("kv_gather: slots", slots, n)
+    num = _ints("kv_gather: count", count, 1)
+    kt = _packed_tokens("kv_gather: k_out", k_out, n, cache.hkv)
+    vt = _packed_tokens("kv_gather: v_out", v_out, n, cache.hkv)
+    st = _on_device(cache, stream, slots, k_out, v_out, ws, count)
+    _check(lib().crisp_kv_gather(ctypes.byref(cache), at, n, num, ctypes.byref(kt), ctypes.byref(vt), ws.data_ptr(),
+                                 _nbytes(ws), st), "crisp_kv_gather")
+
+
+def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) -> Packed:
+    """A batch of packed sequences: sequence b has the query rows [cu_q[b], cu_q[b +
+    1]) of total_q and the key rows [cu_k[b], cu_k[b + 1]) of total_k (int32 CUDA
+    tensors of batch + 1 running sums; the same tensor for whole prompts). max_k:
+    about the longest sequence's keys (None: total_k), for how work is split; no
+    limit. The structure keeps the tensors alive; their contents may change
+    between calls."""
+    n = cu_q.shape[0] if cu_q.dim() == 1 else 0
+    _need(n >= 1, "make_packed: cu_q must be int32 [batch + 1]")
+    q, k = _ints("make_packed: cu_q", cu_q, n), _ints("make_packed: cu_k", cu_k, n)
+    _need(cu_q.device == cu_k.device, "make_packed: the tensors must be on one device")
+    _need(max_k is None or max_k >= 0, "make_packed: max_k must not be negative")
+    p = Packed(n - 1, hq, hkv, D, total_q, total_k, max_k or 0, scale, q, k)
+    p.tensors, p.device_index = (cu_q, cu_k), cu_q.get_device()
+    return p
+
+
+def packed_workspace_size(packed: Packed) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().crisp_packed_workspace_size(ctypes.byref(packed), ctypes.byref(n)), "crisp_packed_workspace_size")
+    return n.value
+
+
+def packed_prefill(packed, q, k, v, out, ws, stream=None):
+    """Causal softmax attention of every sequence of a packed batch: q, out bf16
+    [total_q][hq][128], k, v bf16 [total_k][hkv][128], features contiguous (any
+    token and head strides that are multiples of 8 elements). Query i of a
+    sequence of nq queries and nk keys sees its keys j <= nk - nq + i; rows that
+    see none become zeros, rows behind the last sequence are left alone."""
+    qt = _packed_tokens("packed_prefill: q", q, packed.total_q, packed.hq)
+    kt = _packed_tokens("packed_prefill: k", k, packed.total_k, packed.hkv)
+    vt = _packed_tokens("packed_prefill: v", v, packed.total_k, packed.hkv)
+    ot = _packed_tokens("packed_prefill: out", out, packed.total_q, packed.hq)
+    st = _on_device(packed, stream, q, k, v, out, ws)
+    _check(lib().crisp_packed_prefill(ctypes.byref(packed), ctypes.byref(qt), ctypes.byref(kt), ctypes.byref(vt),
+                                      ctypes.byref(ot), ws.data_ptr(), _nbytes(ws), st), "crisp_packed_prefill")
 
 
 def wait_selftest(ws, limit_ns, stream=None):

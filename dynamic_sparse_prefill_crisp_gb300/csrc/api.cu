@@ -1067,6 +1067,152 @@ crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst
 
 }  // extern "C"
 
+// ---------------------------------------------------------------------------
+// Batches of packed sequences.
+namespace crisp {
+namespace {
+
+crisp_status check_step(const crisp_kv_step* s) {
+  if (!s) return CRISP_ERR_INVALID_ARG;
+  if (s->max_new < 0 || s->max_new > kMaxPacked || s->max_all < 0 || s->max_all > kMaxPacked) return CRISP_ERR_SHAPE;
+  return CRISP_OK;
+}
+
+crisp_status check_packed(const crisp_packed* p) {
+  if (!p) return CRISP_ERR_INVALID_ARG;
+  if (p->head_dim != kD || p->hq <= 0 || p->hq > 4096 || p->hkv <= 0 || p->hq % p->hkv != 0) return CRISP_ERR_SHAPE;
+  if (p->batch < 0 || p->batch > kMaxBatch || p->total_q < 0 || p->total_q > kMaxPacked || p->total_k < 0 ||
+      p->total_k > kMaxPacked || p->max_k < 0)
+    return CRISP_ERR_SHAPE;
+  if (!(p->scale >= 0.f) || std::isinf(p->scale)) return CRISP_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->total_q == 0) return CRISP_OK;  // nothing is addressed
+  if (!p->cu_q || !p->cu_k) return CRISP_ERR_INVALID_ARG;
+  return aligned(p->cu_q, 4) && aligned(p->cu_k, 4) ? CRISP_OK : CRISP_ERR_ALIGN;
+}
+
+// The stride of an axis of one entry is not used, but has to be one that a tensor map accepts.
+int64_t used_stride(int64_t stride, int size) { return size > 1 ? stride : kD; }
+
+// q of a packed batch: boxes of 64 features x a tile's heads x its tokens.
+crisp_status make_packed_q_map(CUtensorMap* m, const crisp_packed& p, const crisp_tokens& q) {
+  int heads = 0, tokens = 0;
+  packed_q_box(p, &heads, &tokens);
+  const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(p.total_q)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(used_stride(q.head_stride, p.hq)) * 2,
+                                 static_cast<cuuint64_t>(used_stride(q.tok_stride, p.total_q)) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.data, dims, strides, box);
+}
+
+}  // namespace
+}  // namespace crisp
+
+extern "C" {
+
+crisp_status crisp_kv_reserve(const crisp_kv_cache* cache, int32_t* table, int32_t* free_pages, int32_t* num_free,
+                              const int32_t* keep, const int32_t* new_lens, const crisp_kv_step* step, void* ws,
+                              size_t ws_bytes, crisp_stream_t stream) {
+  return traced("crisp_kv_reserve", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if ((st = check_step(step)) != CRISP_OK) return st;
+    if (cache->batch == 0) return CRISP_OK;  // no sequences: nothing is addressed
+    if (!table || table != cache->table || !free_pages || !num_free) return CRISP_ERR_INVALID_ARG;
+    if (keep == cache->lens || new_lens == cache->lens) return CRISP_ERR_INVALID_ARG;  // read while written
+    if (!step->cu_new || !step->cu_all || !step->runs || (step->max_new > 0 && (!step->slots || !step->positions)) ||
+        (step->max_all > 0 && !step->all_slots))
+      return CRISP_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(free_pages), static_cast<const void*>(num_free),
+                          static_cast<const void*>(keep), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(step->cu_new), static_cast<const void*>(step->cu_all),
+                          static_cast<const void*>(step->slots), static_cast<const void*>(step->positions),
+                          static_cast<const void*>(step->runs), static_cast<const void*>(step->all_slots)})
+      if (!aligned(p, 4)) return CRISP_ERR_ALIGN;
+    if ((st = check_cache_ws(ws, ws_bytes, align_up(sizeof(DevStatus)))) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    return from_cuda(launch_kv_reserve(*cache, table, free_pages, num_free, keep, new_lens, *step, status_of(ws), stream));
+  });
+}
+
+crisp_status crisp_kv_append_packed(const crisp_kv_cache* cache, const crisp_kv_step* step, const crisp_tokens* k_new,
+                                    const crisp_tokens* v_new, void* ws, size_t ws_bytes, crisp_stream_t stream) {
+  return traced("crisp_kv_append_packed", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if ((st = check_step(step)) != CRISP_OK) return st;
+    if (step->max_new == 0 || cache->batch == 0) return CRISP_OK;  // no tokens
+    if (!step->runs || !step->slots) return CRISP_ERR_INVALID_ARG;
+    if (!aligned(step->runs, 4) || !aligned(step->slots, 4)) return CRISP_ERR_ALIGN;
+    if ((st = check_tokens(k_new, 1, cache->hkv, step->max_new)) != CRISP_OK) return st;
+    if ((st = check_tokens(v_new, 1, cache->hkv, step->max_new)) != CRISP_OK) return st;
+    if ((st = check_cache_ws(ws, ws_bytes, align_up(sizeof(DevStatus)))) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    return from_cuda(launch_kv_append_packed(*cache, *step, *k_new, *v_new, status_of(ws), stream));
+  });
+}
+
+crisp_status crisp_kv_gather(const crisp_kv_cache* cache, const int32_t* slots, int32_t n, const int32_t* count,
+                             const crisp_tokens* k_out, const crisp_tokens* v_out, void* ws, size_t ws_bytes,
+                             crisp_stream_t stream) {
+  return traced("crisp_kv_gather", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_cache(cache);
+    if (st != CRISP_OK) return st;
+    if (n < 0 || n > kMaxPacked) return CRISP_ERR_SHAPE;
+    if (n == 0 || cache->batch == 0) return CRISP_OK;  // no rows
+    if (!slots) return CRISP_ERR_INVALID_ARG;
+    if (!aligned(slots, 4) || !aligned(count, 4)) return CRISP_ERR_ALIGN;
+    if ((st = check_tokens(k_out, 1, cache->hkv, n)) != CRISP_OK) return st;
+    if ((st = check_tokens(v_out, 1, cache->hkv, n)) != CRISP_OK) return st;
+    if ((st = check_cache_ws(ws, ws_bytes, align_up(sizeof(DevStatus)))) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    return from_cuda(launch_kv_gather(*cache, slots, n, count, *k_out, *v_out, status_of(ws), stream));
+  });
+}
+
+crisp_status crisp_packed_workspace_size(const crisp_packed* packed, size_t* bytes) {
+  return traced("crisp_packed_workspace_size", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_packed(packed);
+    if (st != CRISP_OK) return st;
+    if (!bytes) return CRISP_ERR_INVALID_ARG;
+    *bytes = packed_layout(*packed).total;
+    return CRISP_OK;
+  });
+}
+
+crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,
+                                  const crisp_tokens* v, const crisp_tokens* out, void* ws, size_t ws_bytes,
+                                  crisp_stream_t stream) {
+  return traced("crisp_packed_prefill", nullptr, [&]() -> crisp_status {
+    crisp_status st = check_packed(packed);
+    if (st != CRISP_OK) return st;
+    const crisp_packed& p = *packed;
+    if (p.batch == 0 || p.total_q == 0) return CRISP_OK;  // no queries
+    if ((st = check_tokens(q, 1, p.hq, p.total_q)) != CRISP_OK) return st;
+    if ((st = check_tokens(out, 1, p.hq, p.total_q)) != CRISP_OK) return st;
+    const bool keys = p.total_k > 0;  // without, every row is empty and k and v are not looked at
+    if (keys && (st = check_tokens(k, 1, p.hkv, p.total_k)) != CRISP_OK) return st;
+    if (keys && (st = check_tokens(v, 1, p.hkv, p.total_k)) != CRISP_OK) return st;
+    if ((st = check_cache_ws(ws, ws_bytes, packed_layout(p).total)) != CRISP_OK) return st;
+    if ((st = check_device()) != CRISP_OK) return st;
+    TmaMaps maps;
+    if ((st = make_packed_q_map(&maps.q, p, *q)) != CRISP_OK) return st;
+    if (keys) {
+      st = make_map(&maps.k64, k->data, p.hkv, p.total_k, used_stride(k->head_stride, p.hkv),
+                    used_stride(k->tok_stride, p.total_k), kB / 2);
+      if (st != CRISP_OK) return st;
+      st = make_map(&maps.v, v->data, p.hkv, p.total_k, used_stride(v->head_stride, p.hkv),
+                    used_stride(v->tok_stride, p.total_k), kB / 2);
+      if (st != CRISP_OK) return st;
+    } else {
+      maps.k64 = maps.v = maps.q;
+    }
+    const float c = p.scale == 0.f ? 1.0f / std::sqrt(static_cast<float>(kD)) : p.scale;
+    return from_cuda(launch_packed(p, maps, c, keys ? *v : *q, *out, static_cast<char*>(ws), stream));
+  });
+}
+
+}  // extern "C"
+
 namespace crisp {
 namespace {
 
@@ -1127,6 +1273,7 @@ const char* crisp_status_string(crisp_status status) {
 #else
     case CRISP_ERR_BOUNDS: return "device index outside its buffer";
 #endif
+    case CRISP_ERR_PAGES: return "too few free pages";
   }
   return "unknown status";
 }

@@ -126,6 +126,10 @@ struct KvMaps {
   CUtensorMap k, v;  // whole pages of one head: 128 tokens x 128 codes
 };
 
+// Attention over packed sequences.
+constexpr int kPackedCtas = 304;      // 152 SMs x 2: from that many tiles on none is split
+constexpr int kMaxPacked = 1 << 24;   // rows of a packed tensor
+
 inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace of crisp_decode_attention (the status word comes first).
@@ -148,6 +152,21 @@ EvictLayout evict_layout(const crisp_kv_cache& src, int keep);
 
 DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights);
 int decode_row_chunks(int rows);  // row chunks of a (sequence, kv head)
+
+// Workspace of crisp_packed_prefill (the status word comes first).
+struct PackedLayout {
+  size_t part;     // fp32 [splits][total_q][hq][128]    unfinished rows
+  size_t part_ml;  // float2 [splits][total_q][hq]       their references and sums
+  size_t total;
+};
+PackedLayout packed_layout(const crisp_packed& p);
+void packed_q_box(const crisp_packed& p, int* heads, int* tokens);  // rows of q that a tile takes
+
+// Pages that max_new new tokens of a batch can touch (runs of crisp_kv_step).
+inline int64_t max_runs(int batch, int max_new) {
+  const int64_t pages = max_new / kB + int64_t(2) * batch;
+  return pages < max_new ? pages : max_new;
+}
 
 // A launch that may be scheduled while the kernel before it in the stream still
 // ends: the kernel calls ptx::grid_dep_wait before it reads or writes what
@@ -199,6 +218,15 @@ cudaError_t launch_decode(const crisp_kv_cache& c, const KvMaps& maps, int hq, i
                           char* ws, int sms, cudaStream_t st);
 cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
                              const int32_t* new_lens, DevStatus* status, cudaStream_t st);
+cudaError_t launch_kv_append_packed(const crisp_kv_cache& c, const crisp_kv_step& step, const crisp_tokens& k_new,
+                                    const crisp_tokens& v_new, DevStatus* status, cudaStream_t st);
+cudaError_t launch_kv_reserve(const crisp_kv_cache& c, int32_t* table, int32_t* free_pages, int32_t* num_free,
+                              const int32_t* keep, const int32_t* new_lens, const crisp_kv_step& step,
+                              DevStatus* status, cudaStream_t st);
+cudaError_t launch_kv_gather(const crisp_kv_cache& c, const int32_t* slots, int n, const int32_t* count,
+                             const crisp_tokens& k_out, const crisp_tokens& v_out, DevStatus* status, cudaStream_t st);
+cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scale, const crisp_tokens& v,
+                          const crisp_tokens& out, char* ws, cudaStream_t st);
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
                             int sink, int recent, float* new_weights, int32_t* kept, char* ws, int sms,
                             cudaStream_t st);

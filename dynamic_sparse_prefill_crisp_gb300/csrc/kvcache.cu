@@ -130,36 +130,23 @@ struct Pool {
   float* scale;
 };
 
-// New tokens of one page of one head, K or V: the page's new scale from the
-// new values (and its old scale, where it held tokens before them), the new
-// tokens' codes, and the old tokens' codes again if the scale grew. Bound by
-// HBM from a few thousand tokens on (32k tokens of 8 heads: 33 us, 6.2 TB/s);
-// before bf16 values were handled in pairs it was bound by instructions (39
-// us). A token for each of 64 sequences takes 4.7 us, a chain of four reads.
-__global__ void __launch_bounds__(kThreads, 4)
-    append_kernel(Pool pk, Pool pv, int64_t page_stride, int64_t head_stride, int hkv, int num_pages, int max_pages,
-                  const int32_t* table, const int32_t* lens, const int32_t* new_lens, int n_new, crisp_tokens kt,
-                  crisp_tokens vt, DevStatus* status) {
-  __shared__ float red[kThreads / 32];
-  const int g = blockIdx.y >> 1, b = blockIdx.z;
-  const bool is_v = blockIdx.y & 1;
-  const int cap = max_pages * kB;
-  grid_dep_launch();
-  grid_dep_wait();
-  int len = lens[b], cnt = new_lens != nullptr ? new_lens[b] : n_new;
-  const bool bad = len < 0 || len > cap || cnt < 0 || cnt > min(n_new, len);
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x701);
-  len = min(max(len, 0), cap);
-  cnt = min(max(cnt, 0), min(n_new, len));
-  const int start = len - cnt;
-  const int page = start / kB + static_cast<int>(blockIdx.x);
-  const int lo = page * kB;  // position of the page's row 0
-  if (cnt == 0 || lo >= len) return;
-  const int32_t* entry = table + static_cast<int64_t>(b) * max_pages + page;
-  const crisp_tokens t = is_v ? vt : kt;
-  const auto* src = static_cast<const __nv_bfloat16*>(t.data) + b * t.batch_stride + g * t.head_stride;
+// Where new tokens go.
+struct PageSet {
+  Pool pk, pv;
+  int64_t page_stride, head_stride;
+  int hkv, num_pages;
+  DevStatus* status;
+};
+
+// New tokens of one page of one head, K or V, by a CTA: the page's new scale
+// from the new values (and its old scale, where it held tokens before them), the
+// new tokens' codes, and the old tokens' codes again if the scale grew. Rows
+// [first, end) are new, [0, first) old; src: the token of row `first`; page_id():
+// asked once the new values are on their way.
+template <class Id>
+__device__ __forceinline__ void append_page(const PageSet& to, bool is_v, int g, const __nv_bfloat16* src,
+                                            int64_t tok_stride, int first, int end, float* red, Id&& page_id) {
   const int col = (threadIdx.x & (kRowThreads - 1)) * 16, row0 = threadIdx.x / kRowThreads;
-  const int first = max(start - lo, 0), end = min(len - lo, kB);  // rows [first, end) are new, [0, first) old
   // the new values are asked for before the page is looked up
   uint4 x[kPasses][2];
 #pragma unroll
@@ -167,19 +154,19 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int row = row0 + p * kRowsAtOnce;
     x[p][0] = x[p][1] = make_uint4(0u, 0u, 0u, 0u);
     if (row >= first && row < end) {
-      const auto* s = reinterpret_cast<const uint4*>(src + (lo + row - start) * t.tok_stride + col);
+      const auto* s = reinterpret_cast<const uint4*>(src + (row - first) * tok_stride + col);
       x[p][0] = __ldcs(s);
       x[p][1] = __ldcs(s + 1);
     }
   }
-  const int id = *entry;
-  if (id < 0 || id >= num_pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(status, CRISP_ERR_BOUNDS, 0x702);
+  const int id = page_id();
+  if (id < 0 || id >= to.num_pages) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(to.status, CRISP_ERR_BOUNDS, 0x702);
     return;
   }
-  const Pool pool = is_v ? pv : pk;
-  uint8_t* codes = pool.codes + id * page_stride + g * head_stride;
-  float* scale = pool.scale + static_cast<int64_t>(id) * hkv + g;
+  const Pool pool = is_v ? to.pv : to.pk;
+  uint8_t* codes = pool.codes + id * to.page_stride + g * to.head_stride;
+  float* scale = pool.scale + static_cast<int64_t>(id) * to.hkv + g;
   const bool held = first > 0;
   const float s_old = held ? *scale : 0.f;
   uint32_t top = 0u;
@@ -218,6 +205,60 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
   }
   if (threadIdx.x == 0 && (!held || s != s_old)) *scale = s;
+}
+
+// Tokens of a batch padded to n_new. Bound by HBM from a few thousand tokens on
+// (32k tokens of 8 heads: 33 us, 6.2 TB/s); before bf16 values were handled in
+// pairs it was bound by instructions (39 us). A token for each of 64 sequences
+// takes 4.7 us, a chain of four reads.
+__global__ void __launch_bounds__(kThreads, 4)
+    append_kernel(PageSet to, int max_pages, const int32_t* table, const int32_t* lens, const int32_t* new_lens,
+                  int n_new, crisp_tokens kt, crisp_tokens vt) {
+  __shared__ float red[kThreads / 32];
+  const int g = blockIdx.y >> 1, b = blockIdx.z;
+  const bool is_v = blockIdx.y & 1;
+  const int cap = max_pages * kB;
+  grid_dep_launch();
+  grid_dep_wait();
+  int len = lens[b], cnt = new_lens != nullptr ? new_lens[b] : n_new;
+  const bool bad = len < 0 || len > cap || cnt < 0 || cnt > min(n_new, len);
+  if (bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_error(to.status, CRISP_ERR_BOUNDS, 0x701);
+  len = min(max(len, 0), cap);
+  cnt = min(max(cnt, 0), min(n_new, len));
+  const int start = len - cnt;
+  const int page = start / kB + static_cast<int>(blockIdx.x);
+  const int lo = page * kB;  // position of the page's row 0
+  if (cnt == 0 || lo >= len) return;
+  const int32_t* entry = table + static_cast<int64_t>(b) * max_pages + page;
+  const crisp_tokens t = is_v ? vt : kt;
+  const int first = max(start - lo, 0), end = min(len - lo, kB);
+  const auto* src = static_cast<const __nv_bfloat16*>(t.data) + b * t.batch_stride + g * t.head_stride +
+                    (lo + first - start) * t.tok_stride;
+  append_page(to, is_v, g, src, t.tok_stride, first, end, red, [&] { return *entry; });
+}
+
+// Tokens of packed sequences: a run of tokens is what one page takes of them,
+// from its first token's slot on (crisp_kv_reserve writes both).
+__global__ void __launch_bounds__(kThreads, 4)
+    append_packed_kernel(PageSet to, const int32_t* runs, const int32_t* slots, int max_new, crisp_tokens kt,
+                         crisp_tokens vt) {
+  __shared__ float red[kThreads / 32];
+  const int g = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int i0 = runs[blockIdx.x], i1 = runs[blockIdx.x + 1];
+  if (i0 == i1) return;  // past the last run
+  const bool in_room = i0 >= 0 && i0 < i1 && i1 <= max_new;
+  const int slot = in_room ? slots[i0] : -1;
+  const int first = slot & (kB - 1);
+  if (slot < 0 || i1 - i0 > kB - first) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) report_error(to.status, CRISP_ERR_BOUNDS, 0x703);
+    return;
+  }
+  const crisp_tokens t = is_v ? vt : kt;
+  const auto* src = static_cast<const __nv_bfloat16*>(t.data) + g * t.head_stride + i0 * t.tok_stride;
+  append_page(to, is_v, g, src, t.tok_stride, first, first + i1 - i0, red, [&] { return slot / kB; });
 }
 
 // ------------------------------------------------------------------ eviction
@@ -808,13 +849,24 @@ Pool v_pool(const crisp_kv_cache& c) { return {static_cast<uint8_t*>(c.v), c.v_s
 
 }  // namespace
 
+static PageSet pages_of(const crisp_kv_cache& c, DevStatus* status) {
+  return PageSet{k_pool(c), v_pool(c), c.page_stride, c.head_stride, c.hkv, c.num_pages, status};
+}
+
 cudaError_t launch_kv_append(const crisp_kv_cache& c, const crisp_tokens& k_new, const crisp_tokens& v_new, int n_new,
                              const int32_t* new_lens, DevStatus* status, cudaStream_t st) {
   const unsigned reach = static_cast<unsigned>((n_new + kB - 2) / kB + 1);  // pages n_new tokens can touch
   return launch_dependent(append_kernel, dim3(reach, static_cast<unsigned>(2 * c.hkv), static_cast<unsigned>(c.batch)),
-                          kThreads, 0, st, k_pool(c), v_pool(c), c.page_stride, c.head_stride, c.hkv, c.num_pages,
-                          c.max_pages, c.table, static_cast<const int32_t*>(c.lens), new_lens, n_new, k_new, v_new,
-                          status);
+                          kThreads, 0, st, pages_of(c, status), c.max_pages, c.table,
+                          static_cast<const int32_t*>(c.lens), new_lens, n_new, k_new, v_new);
+}
+
+cudaError_t launch_kv_append_packed(const crisp_kv_cache& c, const crisp_kv_step& step, const crisp_tokens& k_new,
+                                    const crisp_tokens& v_new, DevStatus* status, cudaStream_t st) {
+  return launch_dependent(append_packed_kernel,
+                          dim3(static_cast<unsigned>(max_runs(c.batch, step.max_new)), static_cast<unsigned>(2 * c.hkv)),
+                          kThreads, 0, st, pages_of(c, status), static_cast<const int32_t*>(step.runs),
+                          static_cast<const int32_t*>(step.slots), step.max_new, k_new, v_new);
 }
 
 EvictLayout evict_layout(const crisp_kv_cache& src, int keep) {

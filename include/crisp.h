@@ -84,9 +84,11 @@ typedef enum crisp_status {
   CRISP_ERR_CUDA = 5,        /* a CUDA runtime call failed (launch, copy) */
   CRISP_ERR_TIMEOUT = 6,     /* device: a bounded wait inside a kernel ran out */
   CRISP_ERR_DEVICE = 7,      /* the current device is not sm_103 */
-  CRISP_ERR_BOUNDS = 8       /* device: an index fell outside its buffer; the access was skipped. From
-                                the cache calls, which read page ids and lengths on the device, in
-                                every build; from the others in the bounds-checking build only */
+  CRISP_ERR_BOUNDS = 8,      /* device: an index fell outside its buffer; the access was skipped. From
+                                the cache calls and the packed attention, which read page ids and
+                                lengths on the device, in every build; from the others in the
+                                bounds-checking build only */
+  CRISP_ERR_PAGES = 9        /* device: crisp_kv_reserve needs more pages than are free; it took none */
 } crisp_status;
 
 typedef enum crisp_pe_mode {
@@ -557,6 +559,109 @@ CRISP_API crisp_status crisp_decode_attention(const crisp_kv_cache* cache, int32
 CRISP_API crisp_status crisp_kv_evict(const crisp_kv_cache* src, const crisp_kv_cache* dst, const float* weights,
                                       int32_t keep, int32_t sink, int32_t recent, float* new_weights, int32_t* kept,
                                       void* ws, size_t ws_bytes, crisp_stream_t stream);
+
+/* ---- Batches of packed sequences -------------------------------------------
+ * Requests of different lengths in one call, token by token with no padding:
+ * sequence b of a packed tensor is its rows [cu[b], cu[b + 1]), cu an int32
+ * array of batch + 1 running sums on the device. A packed tensor is a
+ * crisp_tokens of one batch entry, [heads][rows][128] (its batch_stride is not
+ * used), and its rows may be more than cu[batch]: those behind the last sequence
+ * are neither read nor written, so that a captured graph serves any batch that
+ * fits. A step of a server is: crisp_kv_reserve, once; then for every layer
+ * crisp_kv_append_packed and crisp_packed_prefill (over the new keys, or over all
+ * of them read back by crisp_kv_gather where the prompts go on from cached
+ * tokens) or crisp_decode_attention. */
+
+/* What crisp_kv_reserve finds out for a step; device arrays, contiguous, 4-byte
+ * aligned. runs: one entry more than the pages that max_new tokens of the
+ * batch can touch, R = min(max_new, max_new / 128 + 2 * batch). */
+typedef struct crisp_kv_step {
+  int32_t max_new;    /* new tokens there is room for, 0 .. 2^24 */
+  int32_t max_all;    /* room for the slots of all tokens, 0 .. 2^24; 0: not wanted */
+  int32_t* cu_new;    /* int32 [batch + 1]  where each sequence's new tokens begin */
+  int32_t* cu_all;    /* int32 [batch + 1]  the same of all its tokens, old and new */
+  int32_t* slots;     /* int32 [max_new]    new token i is row slots[i] % 128 of page slots[i] / 128 */
+  int32_t* positions; /* int32 [max_new]    its position in its sequence */
+  int32_t* runs;      /* int32 [R + 1]      the first new token of each page touched; from there on the total */
+  int32_t* all_slots; /* int32 [max_all]    the slot of every token, in order */
+} crisp_kv_step;
+
+/* Hands out the cache's pages for a step. Sequence b keeps its first k =
+ * min(keep[b], lens[b]) tokens (keep NULL: all; 0: the request is done or replaced;
+ * fewer than lens[b]: drafted tokens are taken back) and gets new_lens[b] more
+ * (NULL: none). Pages past ceil(k / 128) go back to the free pages, missing ones
+ * are taken from them; table (the cache's own, entries given back become -1) and
+ * cache->lens = k + new_lens[b] are updated, and *step is filled: entries of
+ * slots, positions and all_slots at or past their totals are left as they were.
+ *
+ * free_pages int32 [num_pages] holds the *num_free (int32, device) free page ids
+ * as a stack. In the order of sequences and their pages, the pages given back are
+ * pushed last first, then those needed are popped first to last: a call that
+ * takes back what the one before took leaves the stack as it was. A page that
+ * stands in several tables must not be given back.
+ *
+ * Where the step cannot be, the status word says so, cu_new, cu_all and runs become
+ * zeros (the calls that follow do nothing), and nothing else changes:
+ * CRISP_ERR_PAGES if too few pages are free; CRISP_ERR_BOUNDS for a length, keep
+ * or new_lens outside [0, 128 * max_pages], more than 128 * max_pages tokens in a
+ * sequence, max_new or (where it is not 0) max_all exceeded, num_free outside [0,
+ * num_pages], or a page to be given back that is none. A page id on the stack or
+ * in the table that is none gives slots of -1. Workspace: as for crisp_kv_append.
+ * keep, new_lens: int32 [batch], neither of them cache->lens. */
+CRISP_API crisp_status crisp_kv_reserve(const crisp_kv_cache* cache, int32_t* table, int32_t* free_pages,
+                                        int32_t* num_free, const int32_t* keep, const int32_t* new_lens,
+                                        const crisp_kv_step* step, void* ws, size_t ws_bytes, crisp_stream_t stream);
+
+/* crisp_kv_append for packed tokens: token i < cu_new[batch] of k_new and v_new
+ * ([hkv][max_new][128] bf16) goes to slots[i]. Reads runs and slots of the step
+ * only: a run's tokens stand in its page from its first one's slot on, and the
+ * page's scale only grows where that is not the page's row 0. A run that is
+ * outside [0, max_new], or does not fit its page, is CRISP_ERR_BOUNDS and not
+ * written. */
+CRISP_API crisp_status crisp_kv_append_packed(const crisp_kv_cache* cache, const crisp_kv_step* step,
+                                              const crisp_tokens* k_new, const crisp_tokens* v_new, void* ws,
+                                              size_t ws_bytes, crisp_stream_t stream);
+
+/* Reads cached tokens back: row i of k_out and v_out ([hkv][n][128] bf16) becomes
+ * code * scale of slot slots[i], exactly, for i < min(n, *count) (count: int32 on
+ * the device, NULL: n; after crisp_kv_reserve, all_slots and cu_all + batch). A
+ * negative slot leaves its row as it was; one outside the pool is
+ * CRISP_ERR_BOUNDS and does too. 0 <= n <= 2^24. The cache's table and lens are
+ * not read. Workspace: as for crisp_kv_append. */
+CRISP_API crisp_status crisp_kv_gather(const crisp_kv_cache* cache, const int32_t* slots, int32_t n,
+                                       const int32_t* count, const crisp_tokens* k_out, const crisp_tokens* v_out,
+                                       void* ws, size_t ws_bytes, crisp_stream_t stream);
+
+typedef struct crisp_packed {
+  int32_t batch;        /* sequences, at most 1024 */
+  int32_t hq;           /* query heads, at most 4096 */
+  int32_t hkv;          /* key/value heads; hq % hkv == 0 */
+  int32_t head_dim;     /* must be 128 */
+  int32_t total_q;      /* rows of q and out, at most 2^24 */
+  int32_t total_k;      /* rows of k and v, at most 2^24 */
+  int32_t max_k;        /* about the most keys of a sequence (0: total_k): decides how work is split, is no limit */
+  float scale;          /* 0: 1/sqrt(128) */
+  const int32_t* cu_q;  /* int32 [batch + 1] */
+  const int32_t* cu_k;  /* int32 [batch + 1]; may be cu_q */
+} crisp_packed;
+
+CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, size_t* bytes /* host */);
+
+/* Exact causal softmax attention of every sequence of a batch: with nq and nk its
+ * rows in cu_q and cu_k, its query i sees its keys j <= nk - nq + i (the whole
+ * prompt where nq = nk; a chunk that goes on from nk - nq earlier tokens where
+ * not), and
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j,    zeros where no key is seen,
+ * kv head h / (hq / hkv). q bf16 [hq][total_q][128], k, v [hkv][total_k][128], out
+ * as q. What a row does not see does not reach it, infinities and NaN in v
+ * included. A sequence whose running sums descend, leave [0, total_q] or [0,
+ * total_k], or are more than 2^20 rows apart is CRISP_ERR_BOUNDS and counts as
+ * empty: its rows are left as they were. Precision: products of bf16 in fp32, p
+ * rounded to bf16 (2^-8 of itself) for the product with v, sums in fp32. The
+ * result does not depend on timing. */
+CRISP_API crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,
+                                            const crisp_tokens* v, const crisp_tokens* out, void* ws, size_t ws_bytes,
+                                            crisp_stream_t stream);
 
 /* Synchronises `stream` and copies the workspace status word to *status
  * (host). Returns CRISP_ERR_CUDA if the stream or the copy failed. */
