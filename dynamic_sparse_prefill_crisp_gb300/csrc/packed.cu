@@ -24,6 +24,7 @@
 // Warp roles: 0-7 softmax + epilogue, 8 TMA producer, 9 MMA issuer (TMEM owner).
 #include <algorithm>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -312,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = bars.tmem_base;
 
   // Phase counters that persist across passes (each role counts its own).
-  uint32_t kn[2] = {0u, 0u}, vn[2] = {0u, 0u};  // TMA: loads issued per slot; MMA: loads consumed per slot
-  SlotCounts pn;                                // MMA: p_full phases consumed per slot
-  SlotCounts sn;                                // softmax: s_full phases consumed per slot
+  SlotCounts kn, vn;  // TMA: loads issued per slot; MMA: loads consumed per slot
+  SlotCounts pn;      // MMA: p_full phases consumed per slot
+  SlotCounts sn;      // softmax: s_full phases consumed per slot
   uint32_t drains = 0u, o_phase = 0u, x_phase = 0u;
   // Softmax state (per thread: one row, one 32-column chunk).
   const int quarter = warp & 3, chunk = warp >> 2;
@@ -355,12 +356,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int s = t & 1;
           uint64_t* empty = is_k ? &bars.s_full[s] : &bars.v_empty[s];
           uint64_t* full = is_k ? &bars.k_full[s] : &bars.v_full[s];
-          uint32_t& cnt = is_k ? kn[s] : vn[s];
-          if (!mbar_wait(empty, (cnt & 1u) ^ 1u, &bars.abort)) {
+          SlotCounts& cnt = is_k ? kn : vn;
+          if (!mbar_wait(empty, cnt.parity(s) ^ 1u, &bars.abort)) {
             fail(&bars.abort, a.status, is_k ? 0x821 : 0x822);
             return false;
           }
-          ++cnt;
+          cnt.inc(s);
           uint8_t* dst = (is_k ? sK : sV) + s * kSub;
           const CUtensorMap* map = is_k ? &tk : &tv;
           const int row = tile.k0 + (sub0 + t) * kSubKeys;
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int never = 0;
         mbar_wait(&bars.q_full, 0, &never);
         for (int s = 0; s < 2; ++s) {
-          if (kn[s] > 0) mbar_wait(&bars.k_full[s], (kn[s] - 1u) & 1u, &never);
-          if (vn[s] > 0) mbar_wait(&bars.v_full[s], (vn[s] - 1u) & 1u, &never);
+          if (kn.any(s)) mbar_wait(&bars.k_full[s], kn.parity(s) ^ 1u, &never);
+          if (vn.any(s)) mbar_wait(&bars.v_full[s], vn.parity(s) ^ 1u, &never);
         }
       }
     } else if (warp == kMmaWarp) {
@@ -392,17 +393,20 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024), dk1 = dk0 + (kSub >> 4);
       const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kSubHalf, 1024), dv1 = dv0 + (kSub >> 4);
-      // S_s = Q K_s^T into buffer s.
-      auto issue_qk = [&](int s) -> bool {
-        if (!mbar_wait(&bars.k_full[s], kn[s] & 1u, &bars.abort)) return false;
-        ++kn[s];
+      // S_s = Q K_s^T into buffer s (the slot as a constant: its descriptors and
+      // barriers then take no instruction between the products).
+      auto issue_qk = [&](auto slot) -> bool {
+        constexpr int s = decltype(slot)::value;
+        if (!mbar_wait(&bars.k_full[s], kn.parity(s), &bars.abort)) return false;
+        kn.inc(s);
         tc_fence_after();
         umma_qk_x8<(kHalf >> 4), (kSubHalf >> 4)>(tmem + s * kSubKeys, dq, s ? dk1 : dk0, idesc_qk);
         umma_commit(&bars.s_full[s]);
         return true;
       };
       // O += P_s V_s; V_s has landed.
-      auto issue_pv = [&](int s, bool first) -> bool {
+      auto issue_pv = [&](auto slot, bool first) -> bool {
+        constexpr int s = decltype(slot)::value;
         if (!mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort)) return false;
         pn.inc(s);
         tc_fence_after();
@@ -411,10 +415,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         return true;
       };
       auto wait_v = [&](int s) -> bool {
-        if (!mbar_wait(&bars.v_full[s], vn[s] & 1u, &bars.abort)) return false;
-        ++vn[s];
+        if (!mbar_wait(&bars.v_full[s], vn.parity(s), &bars.abort)) return false;
+        vn.inc(s);
         return true;
       };
+      // Sub-block i's second product, then the scores of sub-block i + 2.
+      auto issue_step = [&](auto slot, int i) -> bool {
+        if (!issue_pv(slot, i == 0)) return false;
+        return i + 2 >= nsub || issue_qk(slot);
+      };
+      constexpr std::integral_constant<int, 0> s0;
+      constexpr std::integral_constant<int, 1> s1;
       bool go = true;
       if (lane == 0) {
         go = mbar_wait(&bars.q_full, 0, &bars.abort);
@@ -427,11 +438,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         // take lane 0 alone; before each of the others the warp looks through
         // its V, while the softmax warps work on its scores.
         if (lane == 0) {
-          for (int s = 0; go && s < 2 && s < nsub; ++s) go = issue_qk(s);
-          for (int i = 0; go && i < guarded; ++i) {
-            const int s = i & 1;
-            go = wait_v(s) && issue_pv(s, i == 0);
-            if (go && i + 2 < nsub) go = issue_qk(s);
+          go = go && issue_qk(s0) && (nsub < 2 || issue_qk(s1));
+          for (int i = 0; go && i < guarded; i += 2) {
+            go = wait_v(0) && issue_step(s0, i);
+            if (go && i + 1 < guarded) go = wait_v(1) && issue_step(s1, i + 1);
           }
         }
         for (int i = guarded; i < nsub; ++i) {
@@ -443,10 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (guard_v(sV + s * kSub, kv_all - key0, kv_end - key0, lane)) *reinterpret_cast<volatile int*>(&bars.odd_v) = 1;
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) {
-            go = issue_pv(s, i == 0);
-            if (go && i + 2 < nsub) go = issue_qk(s);
-          }
+          if (lane == 0) go = s ? issue_step(s1, i) : issue_step(s0, i);
         }
         if (lane == 0 && go) umma_commit(&bars.o_full);
       } else if (lane == 0) {
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             go = mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort);
             if (go) pn.inc(s);
           }
-          if (go) go = issue_qk(s);
+          if (go) go = s ? issue_qk(s1) : issue_qk(s0);
         }
         for (int s = 0; go && s < 2 && s < nsub; ++s) {
           go = mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort);
