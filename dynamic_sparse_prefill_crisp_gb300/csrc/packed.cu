@@ -6,22 +6,34 @@
 // A tile is `tokens` consecutive queries of one sequence times `hp` query heads
 // of one kv head (128 rows at most, token by token): a kv head's keys are read
 // once for its whole group, and a short prompt fills a tile with its heads
-// where rows of one head alone would leave it empty. Tiles run in the order of
-// the keys they see, most first, kv head by kv head; a CTA finds its tile from
-// the lengths (find_tile), so that no schedule has to be made or kept.
+// where rows of one head alone would leave it empty. A block of the grid stands
+// for a tile (or a part of one, see below): kv head by kv head, the sequences of
+// most keys first, each from its last tile to its first. A block's tile follows
+// from the lengths, so that no schedule has to be made or kept. (In the order of
+// all tiles' keys, the search for a tile took 5000 cycles, three sub-blocks.)
 //
-// The work on a tile is csrc/attention.cu's: 64-key sub-blocks, two score
-// buffers in TMEM, the first sub-block's row maximum as the reference, two more
-// passes where a row's sum passes 2^64. What differs:
+// Two CTAs stay on each SM and take over blocks that have not started, one
+// ahead: the next tile's Q and first K and V are on their way while this one's
+// softmax and epilogue run. Short prompts need that (256 of up to 300 tokens,
+// 28/4 heads: XX us; a CTA per tile, whose start, loads and end came one after
+// the other, 340 us).
+//
+// The products are csrc/attention.cu's: 64-key sub-blocks, two score buffers in
+// TMEM, the first sub-block's row maximum as the reference. What differs:
 //  - sub-blocks start at any key row, so the rows behind a sequence's last key
-//    are another sequence's. Their scores are masked and their V rows are zeroed
-//    in shared memory; elements of V that only some of the tile's rows see and
-//    that are no finite number are taken out of the product and added to the
-//    rows that see them at the end (0 times NaN would reach the others).
+//    are another sequence's, and of the last ones some rows of the tile see a
+//    part. Masked scores give p = 0, which leaves V out as long as V is finite: a
+//    result that is not says that it may not have been, and the tile is done
+//    again with such elements taken out of the product and added to the rows that
+//    see them (to look through V first took 5000 cycles of a tile's 60000 in a 4k
+//    prompt).
+//  - a tile is done again, as two more items of the CTA, too where a row's sum
+//    passes 2^64: the exact row maxima first, then the sums at those.
 //  - when there are too few tiles for the GPU, a tile's keys are split over
-//    several CTAs, whose unfinished rows a second kernel joins in a fixed order.
+//    several blocks, whose unfinished rows a second kernel joins in a fixed order.
 //
-// Warp roles: 0-7 softmax + epilogue, 8 TMA producer, 9 MMA issuer (TMEM owner).
+// Warp roles: 0-7 softmax + epilogue, 8 finds tiles and issues TMA, 9 issues the
+// products (TMEM owner).
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <type_traits>
@@ -43,9 +55,19 @@ constexpr uint32_t kHalf = kTile / 2;                     // Q: one 64-feature h
 constexpr uint32_t kSub = kTile / 2;                      // K or V: one sub-block (both feature halves)
 constexpr uint32_t kSubHalf = kSub / 2;                   // 64 keys x 64 features
 constexpr uint32_t kSmemBytes = 1024 + kTile + 4 * kSub;  // Q, K[2], V[2] (+ alignment slack)
+#ifndef ASKN
+#define ASKN 4
+#endif
+constexpr int kAskAhead = ASKN;
 constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,128), O [128,256)
 
-enum Mode : int { kFast = 0, kMaxOnly = 1, kFixed = 2 };
+// What the CTA does with a tile: kFast; then, where its result is not finite,
+// kGuarded, the same but for a look through V; or, where it met an overflow,
+// kMaxOnly and kFixed (with that look too).
+enum Mode : int { kFast, kGuarded, kMaxOnly, kFixed, kEnd };
+constexpr uint32_t batch_bytes(int batch) { return batch * 6u + 8u; }  // ranks and order
+
+enum Redo : int { kNotFinite = 1, kOverflow = 2 };
 
 struct PackedArgs {
   const int32_t *cu_q, *cu_k;
@@ -58,6 +80,7 @@ struct PackedArgs {
   float c_log2;
   __nv_bfloat16* out;
   int64_t o_hs, o_ts;
+  int wide_out;           // out's rows allow 32-byte stores
   const __nv_bfloat16* v;
   int64_t v_hs, v_ts;
   float* part;            // [splits][total_q][hq][128]  unfinished rows (splits > 1)
@@ -65,28 +88,33 @@ struct PackedArgs {
   DevStatus* status;
 };
 
-struct Tile {
+// A tile, or one split of it, on its way through the CTA.
+struct Item {
+  int mode;
   int q0, k0;        // the sequence's first rows
   int nq, nk;
   int t0;            // the tile's first query
-  int cost;          // sub-blocks it sees
+  int g, hc;         // kv head; first head of the tile inside its group
+  int split;
+  int sub0, nsub;    // sub-blocks [sub0, sub0 + nsub) of those the tile sees
+  int partial;       // other splits hold the rest
 };
 
-struct Bars {
-  uint64_t q_full;
+struct Shared {
+  uint64_t q_full, q_empty;
   uint64_t k_full[2], v_full[2], v_empty[2];  // a K slot is free again once s_full of its sub-block completes
   uint64_t s_full[2], p_full[2];
-  uint64_t o_full, drain;
-  uint64_t xbar[4];      // per lane quarter: both warps have written their partial row maxima
+  uint64_t o_full, o_empty;
+  uint64_t item_full[2], item_empty[2];
+  uint64_t next, drain;
+  uint64_t xbar[4];      // per lane quarter: both warps have posted a value
+  uint4 answer;          // about a block to take over
   uint32_t tmem_base;
   int abort;
-  int redo;              // a chunk row sum passed kOverflowSum (fast pass)
-  int odd_v;             // a partly seen V element is not finite
-  int found;             // the CTA has a tile
-  int sum[kWarps], top[kWarps], count[2][kWarps];
-  Tile tile;
-  float xmax[2][kB];     // [chunk][row]: partial row maxima
-  float xsum[2][kB];     // [chunk][row]: partial row sums (epilogue)
+  int redo[2];           // Redo bits: a result of the slot's item is not finite, a chunk row sum passed kOverflowSum
+  int odd_v[2];          // a partly seen V element of the slot's item is not finite
+  Item item[2], again[2];
+  float xch[2][2][kB];   // [exchange & 1][chunk][row]: partial row maxima, partial row sums
 };
 
 __host__ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -99,16 +127,6 @@ __device__ __forceinline__ int tile_cost(int nq, int nk, int t0, int tokens) {
   const int end = nk - nq + min(t0 + tokens, nq);
   return end > 0 ? (end + kSubKeys - 1) / kSubKeys : 0;
 }
-__device__ __forceinline__ int tiles_of(const PackedArgs& a, int nq) { return over_tokens(a, nq + a.tokens - 1); }
-// Tiles of a sequence that see c sub-blocks or more: its last ones.
-__device__ __forceinline__ int tiles_from(const PackedArgs& a, int2 n, int c) {
-  const int tiles = tiles_of(a, n.x);
-  if (c <= 0 || tiles == 0) return tiles;
-  const int keys = kSubKeys * (c - 1);  // more than these
-  if (n.y <= keys) return 0;
-  const int x = keys - (n.y - n.x);  // queries that see no more, if whole tiles of them
-  return x <= 0 ? tiles : tiles - min(over_tokens(a, x), tiles - 1);
-}
 
 // The lengths of sequence b, or {0, 0} where cu_q or cu_k do not describe one.
 __device__ __forceinline__ int2 seq_lens(const PackedArgs& a, int b, bool& ok) {
@@ -118,95 +136,90 @@ __device__ __forceinline__ int2 seq_lens(const PackedArgs& a, int b, bool& ok) {
   return ok ? make_int2(q1 - q0, k1 - k0) : make_int2(0, 0);
 }
 
-// The tile of a rank in the order of descending cost (equal costs: by sequence,
-// then by query). With N(c) the tiles of cost c or more, the rank's cost is the
-// largest c with N(c) > rank; each warp counts one N(c) a round, so that a
-// round cuts the range to an eleventh (16k tokens, 256 costs: three rounds).
-// seqs: room for the batch's lengths. All threads; the result in bars.tile
-// (bars.found stays 0 where there is none).
-__device__ void find_tile(const PackedArgs& a, int rank, int2* seqs, Bars& bars) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int tiles = 0, top = 0;
-  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    bool ok;
-    const int2 n = seq_lens(a, b, ok);
-    if (!ok && blockIdx.x == 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x801);
-    seqs[b] = n;
-    tiles += tiles_of(a, n.x);
-    if (n.x > 0) top = max(top, (n.y + kSubKeys - 1) / kSubKeys);
-  }
-  tiles = __reduce_add_sync(0xffffffffu, tiles);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) {
-    bars.sum[warp] = tiles;
-    bars.top[warp] = top;
+// The order in which the CTAs take the sequences, most keys first (equal ones: in
+// the batch's order): order[i] the i-th one's place in the batch, ranks[i] the
+// tiles of those before it, ranks[batch] all tiles. All threads; keys: room for
+// the batch's key counts, tiles of each beside them (2 ints a sequence).
+__device__ __forceinline__ void order_sequences(const PackedArgs& a, int* keys, uint16_t* order, int* ranks) {
+  const int padded = div_up(a.batch, 4) * 4;
+  int* tiles = keys + padded;
+#pragma unroll 1
+  for (int b = threadIdx.x; b < padded; b += kThreads) {
+    int2 n = make_int2(0, -1);
+    if (b < a.batch) {
+      bool ok;
+      n = seq_lens(a, b, ok);
+      if (!ok && blockIdx.x == 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x801);
+    }
+    keys[b] = n.y;
+    tiles[b] = over_tokens(a, n.x + a.tokens - 1);
   }
   __syncthreads();
-  tiles = top = 0;
+#pragma unroll 1
+  for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+    const int mine = keys[b];
+    int before = 0, ranked = 0;
+#pragma unroll 1
+    for (int c = 0; c < padded; c += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(keys + c), t = *reinterpret_cast<const int4*>(tiles + c);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    tiles += bars.sum[w];
-    top = max(top, bars.top[w]);
-  }
-  if (rank >= tiles) return;
-  int lo = 0, hi = top + 1, above = 0;  // N(lo) > rank >= N(hi) = above
-  for (int round = 0; hi - lo > 1; ++round) {
-    const int step = (hi - lo + kWarps) / (kWarps + 1), c = lo + (warp + 1) * step;
-    int n = 0;
-    if (c < hi)
-      for (int b = lane; b < a.batch; b += 32) n += tiles_from(a, seqs[b], c);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) bars.count[round & 1][warp] = n;
-    __syncthreads();
-    const int lo0 = lo, hi0 = hi;
-    for (int w = 0; w < kWarps; ++w) {
-      const int cw = lo0 + (w + 1) * step;
-      if (cw >= hi0) break;
-      const int nw = bars.count[round & 1][w];
-      if (nw <= rank) {
-        hi = cw;
-        above = nw;
-        break;
+      for (int e = 0; e < 4; ++e) {
+        const int other = (&k.x)[e];
+        if (other > mine || (other == mine && c + e < b)) {
+          ++before;
+          ranked += (&t.x)[e];
+        }
       }
-      lo = cw;
     }
-  }
-  if (warp == kTmaWarp) {
-    // The rank-th of the tiles of cost lo, each lane counting neighbouring sequences.
-    const int per = div_up(a.batch, 32), b0 = min(lane * per, a.batch), b1 = min(b0 + per, a.batch);
-    auto of_cost = [&](int b) {
-      return tiles_from(a, seqs[b], lo) - tiles_from(a, seqs[b], lo + 1);
-    };
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += of_cost(b);
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    int left = rank - above - (upto - mine);
-    if (left >= 0 && left < mine) {
-      int b = b0;
-      for (; b + 1 < b1; ++b) {
-        const int m = of_cost(b);
-        if (left < m) break;
-        left -= m;
-      }
-      const int2 n = seqs[b];
-      Tile t;
-      t.nq = n.x;
-      t.nk = n.y;
-      t.q0 = a.cu_q[b];
-      t.k0 = a.cu_k[b];
-      t.t0 = (tiles_of(a, n.x) - tiles_from(a, n, lo) + left) * a.tokens;
-      t.cost = lo;
-      bars.tile = t;
-      bars.found = 1;
-    }
+    order[before] = static_cast<uint16_t>(b);
+    ranks[before] = ranked;
+    if (before == a.batch - 1) ranks[a.batch] = ranked + tiles[b];
   }
   __syncthreads();
 }
+
+// The item of a block: the tiles of a sequence in descending order of the keys
+// they see. Returns false where the block has none.
+__device__ __forceinline__ bool find_item(const PackedArgs& a, uint3 block, const uint16_t* order, const int* ranks,
+                                          Item& it) {
+  const int rank = static_cast<int>(block.x), split = static_cast<int>(block.y), gc = static_cast<int>(block.z);
+  if (rank >= ranks[a.batch]) return false;
+  int lo = 0, hi = a.batch;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ranks[mid] <= rank) lo = mid;
+    else hi = mid;
+  }
+  const int b = order[lo];
+  it.q0 = a.cu_q[b];
+  it.k0 = a.cu_k[b];
+  it.nq = a.cu_q[b + 1] - it.q0;
+  it.nk = a.cu_k[b + 1] - it.k0;
+  it.t0 = (ranks[lo + 1] - 1 - rank) * a.tokens;
+  const int cost = tile_cost(it.nq, it.nk, it.t0, a.tokens);
+  it.split = split;
+  it.sub0 = split * a.split_subs;
+  it.nsub = (split == a.splits - 1 ? cost : min(cost, it.sub0 + a.split_subs)) - it.sub0;
+  it.partial = a.splits > 1 && cost > a.split_subs;
+  it.g = a.chunks == 1 ? gc : gc / a.chunks;
+  it.hc = (gc - it.g * a.chunks) * a.hp;
+  return split == 0 || it.nsub > 0;
+}
+
+// The waits and what follows a failed one are calls: in line, at some thirty
+// places, they made the kernel half as large again, and what a tile runs once
+// (its search, its epilogue) then came from beyond the instruction cache every time.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort);
+}
+__device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, await(bar, parity, abort));
+}
+__device__ __noinline__ void give_up(int* abort, DevStatus* st, uint32_t where) { fail(abort, st, where); }
 
 // Keys past the row's last one (columns above lim) -> -inf.
 __device__ __forceinline__ void mask_from32(int lim, uint32_t (&sv)[32]) {
@@ -216,40 +229,86 @@ __device__ __forceinline__ void mask_from32(int lim, uint32_t (&sv)[32]) {
 }
 
 __device__ __forceinline__ bool odd_bf16(uint32_t h) { return (h & 0x7f80u) == 0x7f80u; }
+// acc + 0 * w of bf16 pairs: no longer zero once a w was no finite number.
+__device__ __forceinline__ void note_odd(uint32_t& acc, uint32_t w) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+}
 
 // Makes a sub-block of V (two halves of 64 keys x 64 features, each key's 128
 // bytes in a row) safe to multiply with p = 0: rows from `seen_end` on are no
 // keys of this tile and become zeros, and in rows from `all_end` on, which some
 // of the tile's rows do not see, elements that are not finite become zero.
-// Returns whether there were such elements. One warp; swizzling moves 16-byte
-// pieces inside a row only.
+// Returns whether there were such elements. One warp, eight lanes a row, eight
+// reads in flight; swizzling moves 16-byte pieces inside a row only.
 __device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end, int lane) {
   bool odd = false;
-  for (int row = max(all_end, 0) + (lane >> 3); row < kSubKeys; row += 4) {
+  uint8_t* mine = sub + (lane >> 3) * 128 + (lane & 7) * 16;
+  for (int row0 = max(all_end, 0) & ~15; row0 < kSubKeys; row0 += 16) {
+    uint4 x[4][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint4* at = reinterpret_cast<uint4*>(sub + half * kSubHalf + row * 128 + (lane & 7) * 16);
-      if (row >= seen_end) {
-        *at = make_uint4(0u, 0u, 0u, 0u);
-        continue;
+    for (int u = 0; u < 4; ++u) {
+      const int row = row0 + 4 * u + (lane >> 3);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint4* at = reinterpret_cast<uint4*>(mine + half * kSubHalf + (row0 + 4 * u) * 128);
+        x[u][half] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= seen_end) *at = x[u][half];
+        else if (row >= all_end) x[u][half] = *at;
       }
-      uint4 x = *at;
-      uint32_t m = 0u;
+    }
+    uint32_t acc = 0u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m = __vmaxu2(m, (&x.x)[e] & 0x7fff7fffu);
-      if ((m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u) {
-        odd = true;
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t& w = (&x.x)[e];
-          if (odd_bf16(w)) w &= 0xffff0000u;
-          if (odd_bf16(w >> 16)) w &= 0x0000ffffu;
-        }
-        *at = x;
-      }
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) note_odd(acc, (&x[u][half].x)[e]);
+    if ((acc & 0x7fff7fffu) == 0u) continue;
+    odd = true;
+#pragma unroll 1
+    for (int e = 0; e < 4 * 2 * 4; ++e) {  // word by word
+      const int u = e >> 3, half = e >> 2 & 1;
+      if (row0 + 4 * u + (lane >> 3) < all_end) continue;
+      uint32_t* at = reinterpret_cast<uint32_t*>(mine + half * kSubHalf + (row0 + 4 * u) * 128) + (e & 3);
+      uint32_t w = *at;
+      if (odd_bf16(w)) w &= 0xffff0000u;
+      if (odd_bf16(w >> 16)) w &= 0x0000ffffu;
+      *at = w;
     }
   }
   return odd;
+}
+
+// 32 bytes of a row, eight words.
+__device__ __forceinline__ void store_row32(void* to, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    auto* v = static_cast<uint4*>(to);
+    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// out += v_j over the keys j in [from, last] and 64 columns, where v_j is not
+// finite; `to`: those of a row of out, or of an unfinished row.
+__device__ __noinline__ void add_odd(const PackedArgs& a, const Item& it, int64_t to, bool partial, int col0, int from,
+                                     int last) {
+#pragma unroll 1
+  for (int j = from; j <= last; ++j) {
+    const __nv_bfloat16* vj = a.v + it.g * a.v_hs + (it.k0 + j) * a.v_ts + col0;
+#pragma unroll 1
+    for (int e = 0; e < 64; ++e) {
+      const float x = __bfloat162float(vj[e]);
+      if (fabsf(x) < INFINITY) continue;
+      if (partial)
+        a.part[to + e] += x;
+      else
+        a.out[to + e] = __float2bfloat16(__bfloat162float(a.out[to + e]) + x);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 2)
@@ -260,371 +319,475 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* sQ = base;
   uint8_t* sK = base + kTile;             // K sub-block slots 0, 1
   uint8_t* sV = base + kTile + 2 * kSub;  // V sub-block slots 0, 1
-  __shared__ Bars bars;
+  int* ranks = reinterpret_cast<int*>(base + kTile + 4 * kSub);
+  uint16_t* order = reinterpret_cast<uint16_t*>(ranks + a.batch + 1);
+  __shared__ Shared sh;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    bars.abort = 0;
-    bars.redo = 0;
-    bars.odd_v = 0;
-    bars.found = 0;
-    mbar_init(&bars.q_full, 1);
+    sh.abort = 0;
+    for (int s = 0; s < 2; ++s) sh.redo[s] = sh.odd_v[s] = 0;
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.k_full[s], 1);
-      mbar_init(&bars.v_full[s], 1);
-      mbar_init(&bars.v_empty[s], 1);
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s], kSoftmaxWarps);
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 1);
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.p_full[s], kSoftmaxWarps);
+      mbar_init(&sh.item_full[s], 1);
+      mbar_init(&sh.item_empty[s], kSoftmaxWarps + 1);
     }
-    mbar_init(&bars.o_full, 1);
-    mbar_init(&bars.drain, 1);
-    for (int qq = 0; qq < 4; ++qq) mbar_init(&bars.xbar[qq], 64);
+    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.o_empty, kSoftmaxWarps);
+    mbar_init(&sh.next, 1);
+    mbar_init(&sh.drain, 1);
+    for (int qq = 0; qq < 4; ++qq) mbar_init(&sh.xbar[qq], 64);
     fence_mbar_init();
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
   grid_dep_wait();
-  // blockIdx.x = ((kv head, head chunk) * bound + rank) * splits + split
-  const int split = static_cast<int>(blockIdx.x) % a.splits, item = static_cast<int>(blockIdx.x) / a.splits;
-  const int rank = item % a.bound, gc = item / a.bound;
-  find_tile(a, rank, reinterpret_cast<int2*>(sK), bars);  // ends with a barrier
-  if (bars.found == 0) return;
-  const Tile tile = bars.tile;
-  const int sub0 = split * a.split_subs;
-  const int nsub = (split == a.splits - 1 ? tile.cost : min(tile.cost, sub0 + a.split_subs)) - sub0;
-  if (split > 0 && nsub <= 0) return;
-  const bool partial = min(a.splits, div_up(tile.cost, a.split_subs)) > 1;
-  const int g = gc / a.chunks, hc = (gc % a.chunks) * a.hp;  // kv head; first head of the tile inside the group
-  const int off = tile.nk - tile.nq;
-  // the tile's first row sees the keys [0, off + t0], its last one those below kv_end
-  const int kv_all = max(off + tile.t0 + 1, 0), kv_end = off + min(tile.t0 + a.tokens, tile.nq);
-  // sub-blocks from here on (of this CTA's) are seen in part by some rows
-  const int guarded = min(max(kv_all / kSubKeys - sub0, 0), max(nsub, 0));
+  order_sequences(a, reinterpret_cast<int*>(sK), order, ranks);
   if (warp == kMmaWarp) {
-    tmem_alloc(&bars.tmem_base, kTmemCols);
+    tmem_alloc(&sh.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  fence_async_shared();  // find_tile's use of the K slots comes before the copies into them
+  fence_async_shared();  // the K slots' use above comes before the copies into them
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_dep_launch();  // not before every CTA of this grid has its TMEM: the next kernel may ask for some
-  const uint32_t tmem = bars.tmem_base;
+  const uint32_t tmem = sh.tmem_base;
+  // The tile's first row sees the keys [0, all_of), its last one those below end_of.
+  auto all_of = [&](const Item& it) { return max(it.nk - it.nq + it.t0 + 1, 0); };
+  auto end_of = [&](const Item& it) { return it.nk - it.nq + min(it.t0 + a.tokens, it.nq); };
+  // Sub-blocks of the item from here on are seen in part by some rows.
+  auto guard_of = [&](const Item& it) { return min(max(all_of(it) / kSubKeys - it.sub0, 0), max(it.nsub, 0)); };
 
-  // Phase counters that persist across passes (each role counts its own).
-  SlotCounts kn, vn;  // TMA: loads issued per slot; MMA: loads consumed per slot
-  SlotCounts pn;      // MMA: p_full phases consumed per slot
-  SlotCounts sn;      // softmax: s_full phases consumed per slot
-  uint32_t drains = 0u, o_phase = 0u, x_phase = 0u;
-  // Softmax state (per thread: one row, one 32-column chunk).
-  const int quarter = warp & 3, chunk = warp >> 2;
-  const int r = quarter * 32 + lane;
-  const int t_row = tile.t0 + r / a.hp, h_row = hc + r % a.hp;  // query of the sequence, head of the group
-  const bool live = r < a.hp * a.tokens && t_row < tile.nq && h_row < a.group;
-  const int pos = live ? off + t_row : -1;  // the row's last key
-  const bool warp_live = __any_sync(0xffffffffu, live);
-  const int pair_bar = 1 + quarter;
-  auto row_max = [&](float partial_max, float& m) -> bool {
-    bars.xmax[chunk][r] = partial_max;
-    mbar_arrive(&bars.xbar[quarter]);
-    const bool got = warp_wait(&bars.xbar[quarter], x_phase & 1u, &bars.abort);
-    ++x_phase;
-    m = fmaxf(bars.xmax[0][r], bars.xmax[1][r]);
-    return got;
-  };
-  const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-  float m_ref = 0.f, l = 0.f;
-  bool ok = true;
-
-  int mode = kFast;
-  for (int pass = 0; pass < 3 && nsub > 0; ++pass) {
-    mode = pass;
-    if (warp == kTmaWarp) {
+  if (warp == kTmaWarp) {
+    SlotCounts kn, vn;  // loads issued per slot
+    uint32_t loads = 0u, asks = 0u;
+    bool asked = false, have = true, go = true;
+    uint3 block = blockIdx;
+    bool more = true;  // no answer was no yet
+    auto send = [&]() {
+      mbar_arrive_expect_tx(&sh.next, 16);
+      take_block(&sh.answer, &sh.next);
+    };
+    auto ask = [&]() {
+      if (lane == 0) send();
+      ++asks;
+      asked = true;
+    };
+    // The next item, passing over blocks that have none.
+    Item ahead;
+    bool found = false;  // ahead is one
+    auto look_ahead = [&]() {
+      while (go && !found && (have || asked)) {
+        if (!have) {
+          go = await_warp(&sh.next, (asks - 1u) & 1u, &sh.abort);
+          asked = false;
+          if (!go) return;
+          have = more = taken_block(&sh.answer, block);
+          fence_async_shared();  // read before the next answer is written
+          __syncwarp();
+          if (!have) return;
+        }
+        have = false;
+        found = find_item(a, block, order, ranks, ahead);
+        if (!found) ask();
+      }
+    };
+    int again = 0;           // items that come back
+    bool fixed_next = false;
+    Item it;
+    // An item is through, and comes back if there is a reason.
+    auto retire = [&](int n) -> bool {
+      if (!await_warp(&sh.item_empty[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort)) return false;
+      const int why = *reinterpret_cast<volatile int*>(&sh.redo[n & 1]);
+      if (why != 0) {
+        __syncwarp();
+        if (lane == 0) {
+          sh.again[again] = sh.item[n & 1];
+          sh.again[again].mode = why & kOverflow ? kMaxOnly : kGuarded;
+          sh.redo[n & 1] = 0;
+        }
+        ++again;
+        __syncwarp();
+      }
+      return true;
+    };
+    for (int n = 0; go; ++n) {
+      if (n >= 2) go = retire(n - 2);
+      if (!go) break;
+      if (fixed_next) {
+        it.mode = kFixed;
+        fixed_next = false;
+      } else {
+        if (again == 0) look_ahead();
+        if (go && again == 0 && !found && n >= 1) go = retire(n - 1);  // the last one may come back
+        if (!go) break;
+        if (again > 0) {
+          it = sh.again[--again];
+          fixed_next = it.mode == kMaxOnly;
+        } else {
+          it = ahead;
+          it.mode = found ? kFast : kEnd;
+          found = false;
+        }
+      }
       if (lane == 0) {
-        if (pass == 0) {
-          if (CRISP_CHECK(tile.q0 + tile.t0 < a.total_q && g * a.group + hc < a.hq, a.status, 0x812)) {
-            mbar_arrive_expect_tx(&bars.q_full, static_cast<uint32_t>(a.hp * a.tokens) * 256u);
-            tma_load_3d(sQ, &tq, &bars.q_full, 0, g * a.group + hc, tile.q0 + tile.t0);
-            tma_load_3d(sQ + kHalf, &tq, &bars.q_full, 64, g * a.group + hc, tile.q0 + tile.t0);
+        sh.item[n & 1] = it;
+        sh.odd_v[n & 1] = 0;
+        mbar_arrive(&sh.item_full[n & 1]);
+      }
+      if (it.mode == kEnd) break;
+      // The next block is asked for when this item is about to end: taken earlier, it
+      // would wait here while other CTAs run out of work.
+      const bool ask_next = it.mode == kFast && more;
+      const int ask_at = max(it.nsub - kAskAhead, 0);
+      const int head = it.g * a.group + it.hc;
+      // K runs one sub-block ahead of V: the order in which the products free their slots.
+      auto load = [&](bool is_k, int t) -> bool {
+        const int s = t & 1;
+        uint64_t* empty = is_k ? &sh.s_full[s] : &sh.v_empty[s];
+        uint64_t* full = is_k ? &sh.k_full[s] : &sh.v_full[s];
+        SlotCounts& cnt = is_k ? kn : vn;
+        if (!await(empty, cnt.parity(s) ^ 1u, &sh.abort)) {
+          give_up(&sh.abort, a.status, is_k ? 0x821 : 0x822);
+          return false;
+        }
+        cnt.inc(s);
+        uint8_t* dst = (is_k ? sK : sV) + s * kSub;
+        const CUtensorMap* map = is_k ? &tk : &tv;
+        const int row = it.k0 + (it.sub0 + t) * kSubKeys;
+        if (CRISP_CHECK(row < a.total_k && head < a.hq, a.status, 0x814)) {
+          mbar_arrive_expect_tx(full, kSub);
+          tma_load_3d(dst, map, full, 0, row, it.g);
+          tma_load_3d(dst + kSubHalf, map, full, 64, row, it.g);
+        } else {
+          mbar_arrive(full);
+        }
+        return true;
+      };
+      if (lane == 0 && it.nsub > 0) {
+        if (loads > 0u) go = await(&sh.q_empty, (loads - 1u) & 1u, &sh.abort);
+        if (!go) {
+          give_up(&sh.abort, a.status, 0x820);
+        } else {
+          ++loads;
+          if (CRISP_CHECK(it.q0 + it.t0 < a.total_q && head < a.hq, a.status, 0x812)) {
+            mbar_arrive_expect_tx(&sh.q_full, static_cast<uint32_t>(a.hp * a.tokens) * 256u);
+            tma_load_3d(sQ, &tq, &sh.q_full, 0, head, it.q0 + it.t0);
+            tma_load_3d(sQ + kHalf, &tq, &sh.q_full, 64, head, it.q0 + it.t0);
           } else {
-            mbar_arrive(&bars.q_full);
+            mbar_arrive(&sh.q_full);
           }
         }
-        // K runs one sub-block ahead of V: the order in which the products free their slots.
-        auto load = [&](bool is_k, int t) -> bool {
-          const int s = t & 1;
-          uint64_t* empty = is_k ? &bars.s_full[s] : &bars.v_empty[s];
-          uint64_t* full = is_k ? &bars.k_full[s] : &bars.v_full[s];
-          SlotCounts& cnt = is_k ? kn : vn;
-          if (!mbar_wait(empty, cnt.parity(s) ^ 1u, &bars.abort)) {
-            fail(&bars.abort, a.status, is_k ? 0x821 : 0x822);
-            return false;
-          }
-          cnt.inc(s);
-          uint8_t* dst = (is_k ? sK : sV) + s * kSub;
-          const CUtensorMap* map = is_k ? &tk : &tv;
-          const int row = tile.k0 + (sub0 + t) * kSubKeys;
-          if (CRISP_CHECK(row < a.total_k && g * a.group < a.hq, a.status, 0x814)) {
-            mbar_arrive_expect_tx(full, kSub);
-            tma_load_3d(dst, map, full, 0, row, g);
-            tma_load_3d(dst + kSubHalf, map, full, 64, row, g);
-          } else {
-            mbar_arrive(full);
-          }
+      }
+      // All loads but the last V; then the next item is looked for, while the
+      // products of this one's last sub-blocks run, and the last V follows.
+#pragma unroll 1
+      for (int t = 0; t <= it.nsub; ++t) {
+        if (t == ask_at && ask_next) ask();
+        if (t == it.nsub) {
+          go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+          if (it.mode == kFast) look_ahead();
+          if (!go) break;
+        }
+        if (lane == 0) {
+          if (go && t < it.nsub) go = load(true, t);
+          if (go && t >= 1 && it.mode != kMaxOnly) go = load(false, t - 1);
+        }
+      }
+      go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+    }
+    if (lane == 0) {
+      if (!go) give_up(&sh.abort, a.status, 0x82b);
+      // Everything asked for has landed before the CTA ends (after a timeout the
+      // consumers may not have waited). Bounded waits that ignore the abort flag.
+      const int never = 0;
+      if (asked) await(&sh.next, (asks - 1u) & 1u, &never);
+      if (loads > 0u) await(&sh.q_full, (loads - 1u) & 1u, &never);
+      for (int s = 0; s < 2; ++s) {
+        if (kn.any(s)) await(&sh.k_full[s], kn.parity(s) ^ 1u, &never);
+        if (vn.any(s)) await(&sh.v_full[s], vn.parity(s) ^ 1u, &never);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kSubKeys, false, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 128, false, true);
+    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);       // slot 0; slot 1 behind it
+    const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kSubHalf, 1024);
+    SlotCounts kn, vn, pn;               // loads and p_full phases consumed per slot
+    uint32_t q_items = 0u, o_items = 0u; // items with products; with second products
+    bool go = true;
+    for (int n = 0;; ++n) {
+      if (lane == 0) go = go && await(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort);
+      go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+      if (!go) break;
+      __syncwarp();
+      const Item& it = sh.item[n & 1];
+      const int mode = it.mode, nsub = it.nsub;
+      if (mode == kEnd) break;
+      if (nsub > 0) {
+        // in the fast pass V is taken as it is
+        const int guarded = mode == kFast ? nsub : guard_of(it), kv_all = all_of(it) - it.sub0 * kSubKeys, kv_end = end_of(it) - it.sub0 * kSubKeys;
+        // S_s = Q K_s^T into buffer s.
+        auto issue_qk = [&](auto s, int i) -> bool {
+          if (!await(&sh.k_full[s], kn.parity(s), &sh.abort)) return false;
+          kn.inc(s);
+          tc_fence_after();
+          umma_qk_x8<(kHalf >> 4), (kSubHalf >> 4)>(tmem + s * kSubKeys, dq, dk0 + s * (kSub >> 4), idesc_qk);
+          umma_commit(&sh.s_full[s]);
+          if (i == nsub - 1) umma_commit(&sh.q_empty);
           return true;
         };
-        bool go = true;
-        for (int t = 0; go && t <= nsub; ++t) {
-          if (t < nsub) go = load(true, t);
-          if (go && t >= 1 && mode != kMaxOnly) go = load(false, t - 1);
-        }
-        // Every copy issued has landed before the pass ends. Bounded waits that ignore the abort flag.
-        const int never = 0;
-        mbar_wait(&bars.q_full, 0, &never);
-        for (int s = 0; s < 2; ++s) {
-          if (kn.any(s)) mbar_wait(&bars.k_full[s], kn.parity(s) ^ 1u, &never);
-          if (vn.any(s)) mbar_wait(&bars.v_full[s], vn.parity(s) ^ 1u, &never);
-        }
-      }
-    } else if (warp == kMmaWarp) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kSubKeys, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 128, false, true);
-      const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024), dk1 = dk0 + (kSub >> 4);
-      const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kSubHalf, 1024), dv1 = dv0 + (kSub >> 4);
-      // S_s = Q K_s^T into buffer s (the slot as a constant: its descriptors and
-      // barriers then take no instruction between the products).
-      auto issue_qk = [&](auto slot) -> bool {
-        constexpr int s = decltype(slot)::value;
-        if (!mbar_wait(&bars.k_full[s], kn.parity(s), &bars.abort)) return false;
-        kn.inc(s);
-        tc_fence_after();
-        umma_qk_x8<(kHalf >> 4), (kSubHalf >> 4)>(tmem + s * kSubKeys, dq, s ? dk1 : dk0, idesc_qk);
-        umma_commit(&bars.s_full[s]);
-        return true;
-      };
-      // O += P_s V_s; V_s has landed.
-      auto issue_pv = [&](auto slot, bool first) -> bool {
-        constexpr int s = decltype(slot)::value;
-        if (!mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort)) return false;
-        pn.inc(s);
-        tc_fence_after();
-        umma_pv_x4(tmem + 128, tmem + s * kSubKeys + 16, s ? dv1 : dv0, idesc_pv, first ? 0u : 1u);
-        umma_commit(&bars.v_empty[s]);
-        return true;
-      };
-      auto wait_v = [&](int s) -> bool {
-        if (!mbar_wait(&bars.v_full[s], vn.parity(s), &bars.abort)) return false;
-        vn.inc(s);
-        return true;
-      };
-      // Sub-block i's second product, then the scores of sub-block i + 2.
-      auto issue_step = [&](auto slot, int i) -> bool {
-        if (!issue_pv(slot, i == 0)) return false;
-        return i + 2 >= nsub || issue_qk(slot);
-      };
-      constexpr std::integral_constant<int, 0> s0;
-      constexpr std::integral_constant<int, 1> s1;
-      bool go = true;
-      if (lane == 0) {
-        go = mbar_wait(&bars.q_full, 0, &bars.abort);
-        if (!go) fail(&bars.abort, a.status, 0x823);
-      }
-      if (mode != kMaxOnly) {
+        auto await_v = [&](auto s) -> bool {
+          if (!await(&sh.v_full[s], vn.parity(s), &sh.abort)) return false;
+          vn.inc(s);
+          return true;
+        };
+        auto await_p = [&](auto s) -> bool {
+          if (!await(&sh.p_full[s], pn.parity(s), &sh.abort)) return false;
+          pn.inc(s);
+          return true;
+        };
+        // O += P_s V_s.
+        auto issue_pv = [&](auto s, int i) {
+          tc_fence_after();
+          umma_pv_x4(tmem + 128, tmem + s * kSubKeys + 16, dv0 + s * (kSub >> 4), idesc_pv, i == 0 ? 0u : 1u);
+          umma_commit(&sh.v_empty[s]);
+        };
+        if (lane == 0) go = await(&sh.q_full, q_items & 1u, &sh.abort);
+        ++q_items;
         // QK(0) QK(1) | PV(0) QK(2) PV(1) QK(3) | ...: the QK that writes buffer s
         // is issued right behind the PV that reads P_s from it (the products of
-        // one thread execute in order). The sub-blocks that every row sees whole
-        // take lane 0 alone; before each of the others the warp looks through
-        // its V, while the softmax warps work on its scores.
-        if (lane == 0) {
-          go = go && issue_qk(s0) && (nsub < 2 || issue_qk(s1));
-          for (int i = 0; go && i < guarded; i += 2) {
-            go = wait_v(0) && issue_step(s0, i);
-            if (go && i + 1 < guarded) go = wait_v(1) && issue_step(s1, i + 1);
+        // one thread execute in order).
+        for (int j = 0; j < nsub + 2; ++j) {
+          const bool products = mode != kMaxOnly;
+          if (j == 2 && products) {
+            // O is the epilogue's until it has read the last item's
+            if (lane == 0 && o_items > 0u) go = go && await(&sh.o_empty, (o_items - 1u) & 1u, &sh.abort);
+            ++o_items;
+            // Lane 0 alone, with the slots as constants: their descriptors and
+            // barriers then take no instruction between the products.
+            if (lane == 0) {
+              constexpr std::integral_constant<int, 0> s0;
+              constexpr std::integral_constant<int, 1> s1;
+              auto step = [&](auto s, int i) -> bool {
+                if (!await_v(s) || !await_p(s)) return false;
+                issue_pv(s, i);
+                return i + 2 >= nsub || issue_qk(s, i + 2);
+              };
+              for (int i = 0; go && i < guarded; i += 2) {
+                go = step(s0, i);
+                if (go && i + 1 < guarded) go = step(s1, i + 1);
+              }
+            }
+            j += guarded;
+            if (j >= nsub + 2) break;
+          }
+          const int i = j - 2;
+          if (i >= 0 && products) {
+            // Some rows do not see all of this one: the warp looks through its V.
+            const int s = i & 1;
+            if (lane == 0) go = go && await_v(s);
+            go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+            if (!go) break;
+            if (guard_v(sV + s * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane))
+              *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) = 1;
+            fence_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0 && go) {
+            // (scores only: a buffer is free again once its scores have been read)
+            if (i >= 0) {
+              go = await_p(i & 1);
+              if (go && products) issue_pv(i & 1, i);
+            }
+            if (go && j < nsub) go = issue_qk(j & 1, j);
           }
         }
-        for (int i = guarded; i < nsub; ++i) {
-          const int s = i & 1;
-          if (lane == 0) go = go && wait_v(s);
-          go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
-          if (!go) break;
-          const int key0 = (sub0 + i) * kSubKeys;
-          if (guard_v(sV + s * kSub, kv_all - key0, kv_end - key0, lane)) *reinterpret_cast<volatile int*>(&bars.odd_v) = 1;
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) go = s ? issue_step(s1, i) : issue_step(s0, i);
-        }
-        if (lane == 0 && go) umma_commit(&bars.o_full);
-      } else if (lane == 0) {
-        // Scores only: a buffer is free again once its scores have been read.
-        for (int i = 0; go && i < nsub; ++i) {
-          const int s = i & 1;
-          if (i >= 2) {
-            go = mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort);
-            if (go) pn.inc(s);
-          }
-          if (go) go = s ? issue_qk(s1) : issue_qk(s0);
-        }
-        for (int s = 0; go && s < 2 && s < nsub; ++s) {
-          go = mbar_wait(&bars.p_full[s], pn.parity(s), &bars.abort);
-          if (go) pn.inc(s);
-        }
+        if (lane == 0 && go && mode != kMaxOnly) umma_commit(&sh.o_full);
       }
-      if (lane == 0) {
-        if (!go) fail(&bars.abort, a.status, 0x824);
-        // Every product issued in this pass has completed before it ends (a
-        // bounded wait that ignores the abort flag: TMEM is released later).
-        umma_commit(&bars.drain);
-        const int never = 0;
-        if (!mbar_wait(&bars.drain, drains & 1u, &never)) fail(&bars.abort, a.status, 0x826);
-        ++drains;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.item_empty[n & 1]);
+    }
+    if (lane == 0) {
+      if (!go) give_up(&sh.abort, a.status, 0x824);
+      // Every product has completed before TMEM is released (a bounded wait that ignores the abort flag).
+      umma_commit(&sh.drain);
+      const int never = 0;
+      if (!await(&sh.drain, 0u, &never)) give_up(&sh.abort, a.status, 0x826);
+    }
+  } else {
+    // Softmax and epilogue: per thread one row, one 32-column chunk of the scores.
+    const int quarter = warp & 3, chunk = warp >> 2;
+    const int r = quarter * 32 + lane;
+    const int t_row = r / a.hp, h_row = r % a.hp;  // query of the tile, head of the tile
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_col = static_cast<uint32_t>(chunk * 32);
+    SlotCounts sn;  // s_full phases consumed per slot
+    uint32_t o_items = 0u, x_phase = 0u;
+    float m_ref = 0.f;
+    bool ok = true;
+    // Posts this row's value of a chunk and takes the other's: {chunk 0's, chunk 1's}.
+    auto exchange = [&](float mine) -> float2 {
+      // (two buffers: the other warp may not have taken the last exchange's values yet)
+      float (*at)[kB] = sh.xch[x_phase & 1u];
+      at[chunk][r] = mine;
+      mbar_arrive(&sh.xbar[quarter]);
+      if (!await_warp(&sh.xbar[quarter], x_phase & 1u, &sh.abort)) {
+        if (lane == 0) give_up(&sh.abort, a.status, 0x829);
+        ok = false;
       }
-    } else {
-      const uint32_t s_col = static_cast<uint32_t>(chunk * 32);
-      float mx = -INFINITY;  // max-only pass: running raw max of this chunk
-      if (mode != kMaxOnly) l = 0.f;
+      ++x_phase;
+      return make_float2(at[0][r], at[1][r]);
+    };
+    for (int n = 0;; ++n) {
+      if (!await_warp(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort)) {
+        if (lane == 0) give_up(&sh.abort, a.status, 0x825);
+        break;
+      }
+      const Item& it = sh.item[n & 1];
+      const int mode = it.mode, nsub = it.nsub, sub0 = it.sub0;
+      if (mode == kEnd) break;
+      const bool live = r < a.hp * a.tokens && it.t0 + t_row < it.nq && it.hc + h_row < a.group;
+      const int pos = live ? it.nk - it.nq + it.t0 + t_row : -1;  // the row's last key
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int guarded = guard_of(it);
+      float mx = -INFINITY;  // running raw max of this chunk
+      float l = 0.f;
       for (int i = 0; ok && i < nsub; ++i) {
         const int s = i & 1;
-        if (!warp_wait(&bars.s_full[s], sn.parity(s), &bars.abort)) {
-          if (lane == 0) fail(&bars.abort, a.status, 0x827);
+        if (!await_warp(&sh.s_full[s], sn.parity(s), &sh.abort)) {
+          if (lane == 0) give_up(&sh.abort, a.status, 0x827);
           ok = false;
           break;
         }
         sn.inc(s);
         if (!warp_live) {  // rows of no token: what P holds there reaches no other row
-          if (lane == 0) mbar_arrive(&bars.p_full[s]);
+          if (lane == 0) mbar_arrive(&sh.p_full[s]);
           continue;
         }
         tc_fence_after();
         uint32_t sv[32];
         tmem_ld32(tmem + lane_addr + s * kSubKeys + s_col, sv);
         if (i >= guarded) mask_from32(pos - (sub0 + i) * kSubKeys - chunk * 32, sv);
-        if (mode == kMaxOnly) {
+        if (mode == kMaxOnly || (mode <= kGuarded && i == 0)) {
           mx = fmaxf(mx, max32(sv));
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.p_full[s]);
-          continue;
-        }
-        if (mode == kFast && i == 0) {
-          // First sub-block: its exact row max (both chunks) is the reference.
-          float m0;
-          if (!row_max(max32(sv), m0)) {
-            if (lane == 0) fail(&bars.abort, a.status, 0x829);
-            ok = false;
-            break;
+          if (mode == kMaxOnly) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[s]);
           }
-          m_ref = m0 > -INFINITY ? m0 * a.c_log2 : 0.f;  // a row that sees nothing here: every p is 0
+          // The reference: the row max (both chunks) of the first sub-block, or of all.
+          if (mode != kMaxOnly || i == nsub - 1) {
+            const float2 m = exchange(mx);
+            mx = fmaxf(m.x, m.y);
+            m_ref = mx > -INFINITY ? mx * a.c_log2 : 0.f;  // a row that sees nothing here: every p is 0
+          }
+          if (mode == kMaxOnly) continue;
         }
         uint32_t pk[16];
         float cs = 0.f;
         p_exp32(sv, a.c_log2, -m_ref, pk, cs);
         tmem_st16(tmem + lane_addr + s * kSubKeys + s_col + 16, pk);
         l += cs;
-        if (mode == kFast && live && cs > kOverflowSum) *reinterpret_cast<volatile int*>(&bars.redo) = 1;
+        if (mode == kFast && live && cs > kOverflowSum) atomicOr(&sh.redo[n & 1], kOverflow);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[s]);
+        if (lane == 0) mbar_arrive(&sh.p_full[s]);
       }
-      if (mode == kMaxOnly) {
-        if (warp_live) {
-          float m1;
-          if (!row_max(mx, m1)) {
-            if (lane == 0) fail(&bars.abort, a.status, 0x82a);
+      if (!ok) break;
+      if (mode != kMaxOnly) {
+        // This thread's row: its place in out (or among the unfinished rows).
+        const int tok = it.q0 + it.t0 + t_row, head = it.g * a.group + it.hc + h_row;
+        const int64_t row_index = static_cast<int64_t>(it.split) * a.total_q * a.hq + static_cast<int64_t>(tok) * a.hq + head;
+        const bool partial = it.partial != 0;
+        const int64_t to = (partial ? row_index * kD : head * a.o_hs + tok * a.o_ts) + chunk * 64;
+        float l_row = 0.f;
+        if (nsub > 0) {
+          if (warp_live) {
+            const float2 sums = exchange(l);
+            l_row = sums.x + sums.y;
+          }
+          // O is final once every second product of the item has completed.
+          if (!await_warp(&sh.o_full, o_items & 1u, &sh.abort)) {
+            if (lane == 0) give_up(&sh.abort, a.status, 0x828);
             ok = false;
           }
-          m_ref = m1 > -INFINITY ? m1 * a.c_log2 : 0.f;
+          ++o_items;
+          tc_fence_after();
         }
-      } else if (ok) {
-        // O is final once every PV of the pass has completed.
-        if (!warp_wait(&bars.o_full, o_phase & 1u, &bars.abort)) {
-          if (lane == 0) fail(&bars.abort, a.status, 0x828);
-          ok = false;
-        }
-        ++o_phase;
-        tc_fence_after();
-      }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    // After the fast pass, a marked CTA runs the max-only and fixed passes.
-    const bool stop = *reinterpret_cast<volatile int*>(&bars.abort) != 0;
-    if (stop || (pass == kFast && *reinterpret_cast<volatile int*>(&bars.redo) == 0) || pass == kFixed) break;
-  }
-
-  if (warp < kSoftmaxWarps && warp_live) {
-    const uint32_t o_addr = tmem + lane_addr + 128 + chunk * 64;
-    const bool have = ok && nsub > 0 && *reinterpret_cast<volatile int*>(&bars.abort) == 0;
-    const bool odd = *reinterpret_cast<volatile int*>(&bars.odd_v) != 0;
-    bars.xsum[chunk][r] = l;
-    named_bar_sync(pair_bar, 64);
-    const float l_row = have ? bars.xsum[0][r] + bars.xsum[1][r] : 0.f;
-    const int tok = tile.q0 + t_row, head = g * a.group + h_row;
-    const int64_t row_index = static_cast<int64_t>(tok) * a.hq + head;
-    uint4* stg = reinterpret_cast<uint4*>(sK + warp * (32 * 128));  // 32 rows x 128 B
-    const float inv_l = partial ? 1.f : (l_row != 0.f ? 1.0f / l_row : 0.f);
-    float* part = a.part + (static_cast<int64_t>(split) * a.total_q * a.hq + row_index) * kD + chunk * 64;
-#pragma unroll 1
-    for (int cc = 0; cc < 2; ++cc) {
-      uint32_t v[32];
-      if (have) {
-        tmem_ld32(o_addr + cc * 32, v);
-      } else {
+        if (!ok) break;
+        if (warp_live) {
+          uint32_t v[2][32];
+          if (nsub > 0) {
+            tmem_ld32_async(tmem + lane_addr + 128 + chunk * 64, v[0]);
+            tmem_ld32_async(tmem + lane_addr + 160 + chunk * 64, v[1]);
+            tmem_ld_wait32(v[0]);
+            tmem_ld_wait32(v[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_empty);
+          } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0u;
-      }
-      if (odd && live) {
-        // What guard_v took out, for the rows that see it: their p is above zero.
-        const int last = min(pos, (sub0 + nsub) * kSubKeys - 1);
-        for (int j = max(kv_all, sub0 * kSubKeys); j <= last; ++j) {
-          const __nv_bfloat16* at = a.v + g * a.v_hs + (tile.k0 + j) * a.v_ts + chunk * 64 + cc * 32;
-          for (int e = 0; e < 32; ++e) {
-            const float x = __bfloat162float(at[e]);
-            if (!(fabsf(x) < INFINITY)) v[e] = __float_as_uint(__uint_as_float(v[e]) + x);
+            for (int e = 0; e < 32; ++e) v[0][e] = v[1][e] = 0u;
           }
+          uint32_t odd = 0u;  // no longer zero: the result is no finite number
+          if (partial) {
+            if (live) {
+              float none = 0.f;
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                  store_row32(a.part + to + c * 32 + e, v[c] + e, true);
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) none = fmaf(__uint_as_float(v[c][e + x]), 0.f, none);
+                }
+              odd = none == 0.f ? 0u : 1u;
+              if (chunk == 0) a.part_ml[row_index] = make_float2(l_row != 0.f ? m_ref : -INFINITY, l_row);
+            }
+          } else {
+            const float inv_l = l_row != 0.f ? 1.0f / l_row : 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  float lo, hi;
+                  fmul2(lo, hi, __uint_as_float(v[c][e + 2 * x]), __uint_as_float(v[c][e + 2 * x + 1]), inv_l, inv_l);
+                  w[x] = pack_bf16x2(lo, hi);
+                  note_odd(odd, w[x]);
+                }
+                if (live) store_row32(a.out + to + c * 32 + e, w, a.wide_out != 0);
+              }
+          }
+          if (mode == kFast && live && (odd & 0x7fff7fffu) != 0u) atomicOr(&sh.redo[n & 1], kNotFinite);
+          if (live && mode != kFast && *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) != 0) {
+            // What guard_v took out, for the rows that see it (their p is above
+            // zero): infinities and NaN, whatever the finite rest is.
+            add_odd(a, it, to, partial, chunk * 64, max(all_of(it), sub0 * kSubKeys),
+                    min(pos, (sub0 + nsub) * kSubKeys - 1));
+          }
+          __syncwarp();
+        } else if (nsub > 0) {
+          if (lane == 0) mbar_arrive(&sh.o_empty);
         }
       }
-      if (partial) {
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + cc * 32 + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        }
-        continue;
-      }
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4) {
-        uint4 u;
-        u.x = pack_bf16x2(__uint_as_float(v[q4 * 8 + 0]) * inv_l, __uint_as_float(v[q4 * 8 + 1]) * inv_l);
-        u.y = pack_bf16x2(__uint_as_float(v[q4 * 8 + 2]) * inv_l, __uint_as_float(v[q4 * 8 + 3]) * inv_l);
-        u.z = pack_bf16x2(__uint_as_float(v[q4 * 8 + 4]) * inv_l, __uint_as_float(v[q4 * 8 + 5]) * inv_l);
-        u.w = pack_bf16x2(__uint_as_float(v[q4 * 8 + 6]) * inv_l, __uint_as_float(v[q4 * 8 + 7]) * inv_l);
-        const int c16 = cc * 4 + q4;  // 16-byte chunk of this warp's 128-byte row part
-        stg[lane * 8 + (c16 ^ (lane & 7))] = u;
-      }
-    }
-    if (partial) {
-      if (live && chunk == 0)
-        a.part_ml[static_cast<int64_t>(split) * a.total_q * a.hq + row_index] =
-            make_float2(l_row != 0.f ? m_ref : -INFINITY, l_row);
-    } else {
-      // Staged per warp so that each store instruction writes four 128-byte row segments.
-      const int64_t at = live ? head * a.o_hs + tok * a.o_ts + chunk * 64 : -1;
       __syncwarp();
-      const int c16 = lane & 7;
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int R = it * 4 + (lane >> 3);
-        const int64_t to = __shfl_sync(0xffffffffu, at, R);
-        // (to < 0: a row of no token)
-        if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + c16 * 8) = stg[R * 8 + (c16 ^ (R & 7))];
-      }
+      if (lane == 0) mbar_arrive(&sh.item_empty[n & 1]);
     }
   }
-
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -771,11 +934,15 @@ cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scal
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   a.status = reinterpret_cast<DevStatus*>(ws);
-  cudaError_t e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  a.wide_out = reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && (p.hq == 1 || out.head_stride % 16 == 0) &&
+               (p.total_q == 1 || out.tok_stride % 16 == 0);
+  const size_t smem = kSmemBytes + batch_bytes(p.batch);
+  cudaError_t e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
   if (e != cudaSuccess) return e;
-  // (a tile holds more than 64 of at most 2^24 x 4096 rows: below 2^31)
-  const unsigned grid = static_cast<unsigned>(plan.bound) * plan.chunks * p.hkv * plan.splits;
-  e = launch_dependent(packed_kernel, dim3(grid), kThreads, kSmemBytes, st, maps.q, maps.k64, maps.v, a);
+  const dim3 grid(static_cast<unsigned>(plan.bound), static_cast<unsigned>(plan.splits),
+                  static_cast<unsigned>(plan.chunks * p.hkv));
+  e = launch_dependent(packed_kernel, grid, kThreads, smem, st, maps.q, maps.k64, maps.v, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
   return launch_dependent(packed_join_kernel, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),

@@ -119,6 +119,34 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// --------------------------------------------------- taking over waiting blocks
+// Asks for a block of this grid that has not started (cluster launch control):
+// the answer, 16 bytes, lands at resp and counts as bytes on *bar. Not to be
+// asked again once an answer was no.
+__device__ __forceinline__ void take_block(void* resp, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(resp)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// Whether there was one, and its blockIdx.
+__device__ __forceinline__ bool taken_block(const void* resp, uint3& at) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::z.b32.b128 %3, r;\n\t}"
+      : "=&r"(ok), "=&r"(at.x), "=&r"(at.y), "=&r"(at.z)
+      : "r"(smem_u32(resp))
+      : "memory");
+  return ok != 0u;
+}
+
 // ------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
