@@ -7,8 +7,9 @@
 // of one kv head (128 rows at most, token by token): a kv head's keys are read
 // once for its whole group, and a short prompt fills a tile with its heads
 // where rows of one head alone would leave it empty. A block of the grid stands
-// for a tile (or a part of one, see below): kv head by kv head, the sequences of
-// most keys first, each from its last tile to its first. A block's tile follows
+// for a tile (or a part of one, see below): the sequences of most keys first, each
+// from its last tile to its first, the kv heads side by side or in turn
+// (packed_plan). A block's tile follows
 // from the lengths, so that no schedule has to be made or kept. (In the order of
 // all tiles' keys, the search for a tile took 5000 cycles, three sub-blocks.)
 //
@@ -35,8 +36,8 @@
 // Warp roles: 0-7 softmax + epilogue, 8 finds tiles and issues TMA, 9 issues the
 // products (TMEM owner).
 #include <algorithm>
+#include <cmath>
 #include <cuda_bf16.h>
-#include <type_traits>
 
 #include "attn.cuh"
 
@@ -55,10 +56,7 @@ constexpr uint32_t kHalf = kTile / 2;                     // Q: one 64-feature h
 constexpr uint32_t kSub = kTile / 2;                      // K or V: one sub-block (both feature halves)
 constexpr uint32_t kSubHalf = kSub / 2;                   // 64 keys x 64 features
 constexpr uint32_t kSmemBytes = 1024 + kTile + 4 * kSub;  // Q, K[2], V[2] (+ alignment slack)
-#ifndef ASKN
-#define ASKN 4
-#endif
-constexpr int kAskAhead = ASKN;
+constexpr int kAskAhead = 4;                              // sub-blocks before the end at which the next block is asked for
 constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,128), O [128,256)
 
 // What the CTA does with a tile: kFast; then, where its result is not finite,
@@ -71,11 +69,11 @@ enum Redo : int { kNotFinite = 1, kOverflow = 2 };
 
 struct PackedArgs {
   const int32_t *cu_q, *cu_k;
-  int batch, total_q, total_k, hq, group;
+  int batch, total_q, total_k, hq, hkv, group;
   int hp, chunks;         // heads of a tile; tiles that a group's heads take
   int tokens;             // queries of a tile
   uint32_t inv_tokens;    // ceil(2^32 / tokens), 0 for one token
-  int bound;              // no batch of these sizes has more (sequence, tokens) tiles
+  int heads_log2;         // kv heads (times chunks) that run side by side
   int splits, split_subs; // CTAs of a tile and sub-blocks of each (the last takes what is left)
   float c_log2;
   __nv_bfloat16* out;
@@ -182,8 +180,9 @@ __device__ __forceinline__ void order_sequences(const PackedArgs& a, int* keys, 
 // they see. Returns false where the block has none.
 __device__ __forceinline__ bool find_item(const PackedArgs& a, uint3 block, const uint16_t* order, const int* ranks,
                                           Item& it) {
-  const int rank = static_cast<int>(block.x), split = static_cast<int>(block.y), gc = static_cast<int>(block.z);
-  if (rank >= ranks[a.batch]) return false;
+  const int rank = static_cast<int>(block.x >> a.heads_log2), split = static_cast<int>(block.y);
+  const int gc = static_cast<int>((block.z << a.heads_log2) + (block.x & ((1u << a.heads_log2) - 1u)));
+  if (rank >= ranks[a.batch] || gc >= a.chunks * a.hkv) return false;
   int lo = 0, hi = a.batch;
 #pragma unroll 1
   while (hi - lo > 1) {
@@ -221,6 +220,15 @@ __device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, const
 }
 __device__ __noinline__ void give_up(int* abort, DevStatus* st, uint32_t where) { fail(abort, st, where); }
 
+// One lane of a converged warp (and which). Code under this condition is known to
+// run in one lane: descriptors then stay in uniform registers, where code under
+// `lane == 0` takes a loop over the lanes for each product (one QK: 360
+// instructions, 160 so).
+__device__ __forceinline__ bool elect_lane(int& lane) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync %1|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok), "=r"(lane));
+  return ok != 0u;
+}
 // Keys past the row's last one (columns above lim) -> -inf.
 __device__ __forceinline__ void mask_from32(int lim, uint32_t (&sv)[32]) {
 #pragma unroll
@@ -367,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto guard_of = [&](const Item& it) { return min(max(all_of(it) / kSubKeys - it.sub0, 0), max(it.nsub, 0)); };
 
   if (warp == kTmaWarp) {
+    int from;  // the lane that issues
+    const bool leader = elect_lane(from);
     SlotCounts kn, vn;  // loads issued per slot
     uint32_t loads = 0u, asks = 0u;
     bool asked = false, have = true, go = true;
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       take_block(&sh.answer, &sh.next);
     };
     auto ask = [&]() {
-      if (lane == 0) send();
+      if (leader) send();
       ++asks;
       asked = true;
     };
@@ -409,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int why = *reinterpret_cast<volatile int*>(&sh.redo[n & 1]);
       if (why != 0) {
         __syncwarp();
-        if (lane == 0) {
+        if (leader) {
           sh.again[again] = sh.item[n & 1];
           sh.again[again].mode = why & kOverflow ? kMaxOnly : kGuarded;
           sh.redo[n & 1] = 0;
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           found = false;
         }
       }
-      if (lane == 0) {
+      if (leader) {
         sh.item[n & 1] = it;
         sh.odd_v[n & 1] = 0;
         mbar_arrive(&sh.item_full[n & 1]);
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         return true;
       };
-      if (lane == 0 && it.nsub > 0) {
+      if (leader && it.nsub > 0) {
         if (loads > 0u) go = await(&sh.q_empty, (loads - 1u) & 1u, &sh.abort);
         if (!go) {
           give_up(&sh.abort, a.status, 0x820);
@@ -493,18 +503,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int t = 0; t <= it.nsub; ++t) {
         if (t == ask_at && ask_next) ask();
         if (t == it.nsub) {
-          go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+          go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
           if (it.mode == kFast) look_ahead();
           if (!go) break;
         }
-        if (lane == 0) {
+        if (leader) {
           if (go && t < it.nsub) go = load(true, t);
           if (go && t >= 1 && it.mode != kMaxOnly) go = load(false, t - 1);
         }
       }
-      go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+      go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
     }
-    if (lane == 0) {
+    if (leader) {
       if (!go) give_up(&sh.abort, a.status, 0x82b);
       // Everything asked for has landed before the CTA ends (after a timeout the
       // consumers may not have waited). Bounded waits that ignore the abort flag.
@@ -517,6 +527,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   } else if (warp == kMmaWarp) {
+    int from;  // the lane that issues
+    const bool leader = elect_lane(from);
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kSubKeys, false, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, 128, false, true);
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -526,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t q_items = 0u, o_items = 0u; // items with products; with second products
     bool go = true;
     for (int n = 0;; ++n) {
-      if (lane == 0) go = go && await(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort);
-      go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+      if (leader) go = go && await(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort);
+      go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
       if (!go) break;
       __syncwarp();
       const Item& it = sh.item[n & 1];
@@ -535,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (mode == kEnd) break;
       if (nsub > 0) {
         // in the fast pass V is taken as it is
-        const int guarded = mode == kFast ? nsub : guard_of(it), kv_all = all_of(it) - it.sub0 * kSubKeys, kv_end = end_of(it) - it.sub0 * kSubKeys;
+        const int kv_all = all_of(it) - it.sub0 * kSubKeys, kv_end = end_of(it) - it.sub0 * kSubKeys;
         // S_s = Q K_s^T into buffer s.
-        auto issue_qk = [&](auto s, int i) -> bool {
+        auto issue_qk = [&](int s, int i) -> bool {
           if (!await(&sh.k_full[s], kn.parity(s), &sh.abort)) return false;
           kn.inc(s);
           tc_fence_after();
@@ -546,78 +558,75 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (i == nsub - 1) umma_commit(&sh.q_empty);
           return true;
         };
-        auto await_v = [&](auto s) -> bool {
+        auto await_v = [&](int s) -> bool {
           if (!await(&sh.v_full[s], vn.parity(s), &sh.abort)) return false;
           vn.inc(s);
           return true;
         };
-        auto await_p = [&](auto s) -> bool {
+        auto await_p = [&](int s) -> bool {
           if (!await(&sh.p_full[s], pn.parity(s), &sh.abort)) return false;
           pn.inc(s);
           return true;
         };
         // O += P_s V_s.
-        auto issue_pv = [&](auto s, int i) {
+        auto issue_pv = [&](int s, int i) {
           tc_fence_after();
           umma_pv_x4(tmem + 128, tmem + s * kSubKeys + 16, dv0 + s * (kSub >> 4), idesc_pv, i == 0 ? 0u : 1u);
           umma_commit(&sh.v_empty[s]);
         };
-        if (lane == 0) go = await(&sh.q_full, q_items & 1u, &sh.abort);
+        if (leader) go = await(&sh.q_full, q_items & 1u, &sh.abort);
         ++q_items;
         // QK(0) QK(1) | PV(0) QK(2) PV(1) QK(3) | ...: the QK that writes buffer s
         // is issued right behind the PV that reads P_s from it (the products of
         // one thread execute in order).
-        for (int j = 0; j < nsub + 2; ++j) {
-          const bool products = mode != kMaxOnly;
-          if (j == 2 && products) {
+        if (mode == kFast) {
+          if (leader) {
+            go = go && issue_qk(0, 0) && (nsub < 2 || issue_qk(1, 1));
             // O is the epilogue's until it has read the last item's
-            if (lane == 0 && o_items > 0u) go = go && await(&sh.o_empty, (o_items - 1u) & 1u, &sh.abort);
-            ++o_items;
-            // Lane 0 alone, with the slots as constants: their descriptors and
-            // barriers then take no instruction between the products.
-            if (lane == 0) {
-              constexpr std::integral_constant<int, 0> s0;
-              constexpr std::integral_constant<int, 1> s1;
-              auto step = [&](auto s, int i) -> bool {
-                if (!await_v(s) || !await_p(s)) return false;
-                issue_pv(s, i);
-                return i + 2 >= nsub || issue_qk(s, i + 2);
-              };
-              for (int i = 0; go && i < guarded; i += 2) {
-                go = step(s0, i);
-                if (go && i + 1 < guarded) go = step(s1, i + 1);
+            if (o_items > 0u) go = go && await(&sh.o_empty, (o_items - 1u) & 1u, &sh.abort);
+            for (int i = 0; go && i < nsub; ++i) {
+              const int s = i & 1;
+              go = await_v(s) && await_p(s);
+              if (go) issue_pv(s, i);
+              if (go && i + 2 < nsub) go = issue_qk(s, i + 2);
+            }
+          }
+        } else {
+          // Done again: the warp looks through V where some rows do not see all of a
+          // sub-block; or scores only (a buffer is free again once they have been read).
+          const bool products = mode != kMaxOnly;
+          for (int j = 0; j < nsub + 2; ++j) {
+            const int i = j - 2;
+            if (i >= 0 && products) {
+              if (leader) {
+                if (i == 0 && o_items > 0u) go = go && await(&sh.o_empty, (o_items - 1u) & 1u, &sh.abort);
+                go = go && await_v(i & 1);
               }
+              go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
+              if (!go) break;
+              if (guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane))
+                *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) = 1;
+              fence_async_shared();
+              __syncwarp();
             }
-            j += guarded;
-            if (j >= nsub + 2) break;
-          }
-          const int i = j - 2;
-          if (i >= 0 && products) {
-            // Some rows do not see all of this one: the warp looks through its V.
-            const int s = i & 1;
-            if (lane == 0) go = go && await_v(s);
-            go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
-            if (!go) break;
-            if (guard_v(sV + s * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane))
-              *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) = 1;
-            fence_async_shared();
-            __syncwarp();
-          }
-          if (lane == 0 && go) {
-            // (scores only: a buffer is free again once its scores have been read)
-            if (i >= 0) {
-              go = await_p(i & 1);
-              if (go && products) issue_pv(i & 1, i);
+            if (leader && go) {
+              if (i >= 0) {
+                go = await_p(i & 1);
+                if (go && products) issue_pv(i & 1, i);
+              }
+              if (go && j < nsub) go = issue_qk(j & 1, j);
             }
-            if (go && j < nsub) go = issue_qk(j & 1, j);
           }
         }
-        if (lane == 0 && go && mode != kMaxOnly) umma_commit(&sh.o_full);
+        if (mode != kMaxOnly) {
+          ++o_items;
+          if (leader && go) umma_commit(&sh.o_full);
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.item_empty[n & 1]);
+      if (leader) mbar_arrive(&sh.item_empty[n & 1]);
     }
-    if (lane == 0) {
+    if (leader) {
       if (!go) give_up(&sh.abort, a.status, 0x824);
       // Every product has completed before TMEM is released (a bounded wait that ignores the abort flag).
       umma_commit(&sh.drain);
@@ -863,12 +872,17 @@ int tile_heads(int group) {
 }
 
 struct PackedPlan {
-  int hp, chunks, tokens, bound, splits, split_subs;
+  int hp, chunks, tokens, bound, heads_log2, splits, split_subs;
 };
 
-// Tiles are split over CTAs where there are not enough of them for two CTAs on
-// each SM, into parts of eight sub-blocks or more (below that the second kernel
-// and a CTA's own start and end cost more than the split saves).
+// A tile is split into parts of eight sub-blocks or more where that makes the
+// whole shorter: by the time of a sub-block (0.76 us with two CTAs on an SM), of
+// the CTAs' rounds, and of writing and joining unfinished rows (2 x 520 bytes each
+// at 6 TB/s, and 3 us for the second kernel). Chunks that go on behind many keys
+// are tiles of one size, and take whole rounds (4 x 512 tokens behind up to 48k,
+// 28/4 heads, 464 tiles: 5 rounds of a third each instead of 2); tiles of whole
+// prompts are of every size, and fill the rounds up among themselves. The lengths
+// are on the device: the sizes that the host knows stand for them.
 PackedPlan packed_plan(const crisp_packed& p) {
   PackedPlan L{};
   const int group = p.hq / p.hkv;
@@ -877,10 +891,28 @@ PackedPlan packed_plan(const crisp_packed& p) {
   L.tokens = kB / L.hp;
   const int64_t bound = (static_cast<int64_t>(p.total_q) + static_cast<int64_t>(p.batch) * (L.tokens - 1)) / L.tokens;
   L.bound = static_cast<int>(std::min<int64_t>(bound, p.total_q));
-  const int longest = p.max_k > 0 ? std::min(p.max_k, p.total_k) : p.total_k;
-  const int cost = std::max(1, div_up(std::min(longest, kMaxSeq), kSubKeys));
-  const int64_t items = static_cast<int64_t>(L.bound) * L.chunks * p.hkv;
-  L.splits = items > 0 ? static_cast<int>(std::min<int64_t>(std::max<int64_t>(kPackedCtas / items, 1), std::max(cost / 8, 1))) : 1;
+  const int longest = std::min(p.max_k > 0 ? std::min(p.max_k, p.total_k) : p.total_k, kMaxSeq);
+  // Heads side by side as long as the keys and values of a sequence fill no more
+  // than half of L2: then every head's long tiles start before any short one
+  // (16k tokens, 8/8 heads: X us, X head by head).
+  const int heads = L.chunks * p.hkv;
+  while ((2 << L.heads_log2) <= heads && (int64_t(2) << L.heads_log2) * longest * (4 * kD) <= (int64_t(64) << 20))
+    ++L.heads_log2;
+  const double batch = std::max(p.batch, 1), q = p.total_q / batch, off = std::max(p.total_k - p.total_q, 0) / batch;
+  const double mean = std::max((off + q / 2) / kSubKeys, 0.5), most = std::max(longest / double(kSubKeys), 1.0);
+  const double rounds = static_cast<double>(L.bound) * heads / kPackedCtas;
+  const double rows = static_cast<double>(p.total_q) * p.hq;
+  double best = 0.0;
+  L.splits = 1;
+  for (int s = 1; s == 1 || (s <= kPackedCtas && most / s >= 8.0); ++s) {
+    const double subs = off > q ? std::ceil(rounds * s) / s * mean : std::max(rounds * mean, most / s);
+    const double us = 0.76 * subs + (s > 1 ? 3.0 + rows * s * 1040.0 / 6e6 : 0.0);
+    if (s == 1 || us < best) {
+      best = us;
+      L.splits = s;
+    }
+  }
+  const int cost = div_up(std::max(longest, 1), kSubKeys);
   L.split_subs = div_up(cost, L.splits);
   L.splits = div_up(cost, L.split_subs);
   return L;
@@ -916,12 +948,13 @@ cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scal
   a.total_q = p.total_q;
   a.total_k = p.total_k;
   a.hq = p.hq;
+  a.hkv = p.hkv;
   a.group = p.hq / p.hkv;
   a.hp = plan.hp;
   a.chunks = plan.chunks;
   a.tokens = plan.tokens;
   a.inv_tokens = plan.tokens == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + plan.tokens - 1) / plan.tokens);
-  a.bound = plan.bound;
+  a.heads_log2 = plan.heads_log2;
   a.splits = plan.splits;
   a.split_subs = plan.split_subs;
   a.c_log2 = scale * 1.4426950408889634f;
@@ -940,8 +973,10 @@ cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scal
   cudaError_t e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(plan.bound), static_cast<unsigned>(plan.splits),
-                  static_cast<unsigned>(plan.chunks * p.hkv));
+  // (heads side by side, tiles), parts, groups of heads; a tile holds more than 64
+  // of at most 2^24 x 4096 rows
+  const dim3 grid(static_cast<unsigned>(plan.bound) << plan.heads_log2, static_cast<unsigned>(plan.splits),
+                  static_cast<unsigned>(div_up(plan.chunks * p.hkv, 1 << plan.heads_log2)));
   e = launch_dependent(packed_kernel, grid, kThreads, smem, st, maps.q, maps.k64, maps.v, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
