@@ -56,6 +56,7 @@ constexpr uint32_t kHalf = kTile / 2;                     // Q: one 64-feature h
 constexpr uint32_t kSub = kTile / 2;                      // K or V: one sub-block (both feature halves)
 constexpr uint32_t kSubHalf = kSub / 2;                   // 64 keys x 64 features
 constexpr uint32_t kSmemBytes = 1024 + kTile + 4 * kSub;  // Q, K[2], V[2] (+ alignment slack)
+constexpr int kRing = 4;                                  // items on their way through a CTA
 constexpr int kAskAhead = 4;                              // sub-blocks before the end at which the next block is asked for
 constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,128), O [128,256)
 
@@ -103,15 +104,15 @@ struct Shared {
   uint64_t k_full[2], v_full[2], v_empty[2];  // a K slot is free again once s_full of its sub-block completes
   uint64_t s_full[2], p_full[2];
   uint64_t o_full, o_empty;
-  uint64_t item_full[2], item_empty[2];
+  uint64_t item_full[kRing], item_empty[kRing];
   uint64_t next, drain;
   uint64_t xbar[4];      // per lane quarter: both warps have posted a value
   uint4 answer;          // about a block to take over
   uint32_t tmem_base;
   int abort;
-  int redo[2];           // Redo bits: a result of the slot's item is not finite, a chunk row sum passed kOverflowSum
-  int odd_v[2];          // a partly seen V element of the slot's item is not finite
-  Item item[2], again[2];
+  int redo[kRing];       // Redo bits: a result of the slot's item is not finite, a chunk row sum passed kOverflowSum
+  int odd_v[kRing];      // a partly seen V element of the slot's item is not finite
+  Item item[kRing], again[kRing];
   float xch[2][2][kB];   // [exchange & 1][chunk][row]: partial row maxima, partial row sums
 };
 
@@ -205,6 +206,9 @@ __device__ __forceinline__ bool find_item(const PackedArgs& a, uint3 block, cons
   it.hc = (gc - it.g * a.chunks) * a.hp;
   return split == 0 || it.nsub > 0;
 }
+
+// The phase of a ring slot's barrier at its n-th item.
+__device__ __forceinline__ uint32_t ring_parity(int n) { return static_cast<uint32_t>(n / kRing) & 1u; }
 
 // The waits and what follows a failed one are calls: in line, at some thirty
 // places, they made the kernel half as large again, and what a tile runs once
@@ -334,7 +338,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     sh.abort = 0;
-    for (int s = 0; s < 2; ++s) sh.redo[s] = sh.odd_v[s] = 0;
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     for (int s = 0; s < 2; ++s) {
@@ -343,6 +346,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&sh.v_empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.p_full[s], kSoftmaxWarps);
+    }
+    for (int s = 0; s < kRing; ++s) {
+      sh.redo[s] = sh.odd_v[s] = 0;
       mbar_init(&sh.item_full[s], 1);
       mbar_init(&sh.item_empty[s], kSoftmaxWarps + 1);
     }
@@ -410,19 +416,21 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!found) ask();
       }
     };
-    int again = 0;           // items that come back
+    int retired = 0;  // items known to be through
+    int again = 0;    // items that come back
     bool fixed_next = false;
     Item it;
-    // An item is through, and comes back if there is a reason.
-    auto retire = [&](int n) -> bool {
-      if (!await_warp(&sh.item_empty[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort)) return false;
-      const int why = *reinterpret_cast<volatile int*>(&sh.redo[n & 1]);
+    // The next item is through, and comes back if there is a reason.
+    auto retire = [&]() -> bool {
+      const int n = retired++;
+      if (!await_warp(&sh.item_empty[n % kRing], ring_parity(n), &sh.abort)) return false;
+      const int why = *reinterpret_cast<volatile int*>(&sh.redo[n % kRing]);
       if (why != 0) {
         __syncwarp();
         if (leader) {
-          sh.again[again] = sh.item[n & 1];
+          sh.again[again] = sh.item[n % kRing];
           sh.again[again].mode = why & kOverflow ? kMaxOnly : kGuarded;
-          sh.redo[n & 1] = 0;
+          sh.redo[n % kRing] = 0;
         }
         ++again;
         __syncwarp();
@@ -430,14 +438,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       return true;
     };
     for (int n = 0; go; ++n) {
-      if (n >= 2) go = retire(n - 2);
+      while (go && retired <= n - kRing) go = retire();
       if (!go) break;
       if (fixed_next) {
         it.mode = kFixed;
         fixed_next = false;
       } else {
         if (again == 0) look_ahead();
-        if (go && again == 0 && !found && n >= 1) go = retire(n - 1);  // the last one may come back
+        while (go && again == 0 && !found && retired < n) go = retire();  // one of the last may come back
         if (!go) break;
         if (again > 0) {
           it = sh.again[--again];
@@ -449,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (leader) {
-        sh.item[n & 1] = it;
-        sh.odd_v[n & 1] = 0;
-        mbar_arrive(&sh.item_full[n & 1]);
+        sh.item[n % kRing] = it;
+        sh.odd_v[n % kRing] = 0;
+        mbar_arrive(&sh.item_full[n % kRing]);
       }
       if (it.mode == kEnd) break;
       // The next block is asked for when this item is about to end: taken earlier, it
@@ -497,20 +505,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      // All loads but the last V; then the next item is looked for, while the
-      // products of this one's last sub-blocks run, and the last V follows.
+      // The next item is looked for before the last V is loaded (a short item's
+      // first), which is when the producer would wait for the products before.
+      const int look_at = it.nsub <= kAskAhead ? min(it.nsub, 1) : it.nsub;
 #pragma unroll 1
       for (int t = 0; t <= it.nsub; ++t) {
         if (t == ask_at && ask_next) ask();
-        if (t == it.nsub) {
+        if (leader && go && t < it.nsub) go = load(true, t);
+        if (t == look_at) {
           go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
           if (it.mode == kFast) look_ahead();
           if (!go) break;
         }
-        if (leader) {
-          if (go && t < it.nsub) go = load(true, t);
-          if (go && t >= 1 && it.mode != kMaxOnly) go = load(false, t - 1);
-        }
+        if (leader && go && t >= 1 && it.mode != kMaxOnly) go = load(false, t - 1);
       }
       go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
     }
@@ -538,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t q_items = 0u, o_items = 0u; // items with products; with second products
     bool go = true;
     for (int n = 0;; ++n) {
-      if (leader) go = go && await(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort);
+      if (leader) go = go && await(&sh.item_full[n % kRing], ring_parity(n), &sh.abort);
       go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
       if (!go) break;
       __syncwarp();
-      const Item& it = sh.item[n & 1];
+      const Item& it = sh.item[n % kRing];
       const int mode = it.mode, nsub = it.nsub;
       if (mode == kEnd) break;
       if (nsub > 0) {
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
               if (!go) break;
               if (guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane))
-                *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) = 1;
+                *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]) = 1;
               fence_async_shared();
               __syncwarp();
             }
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       __syncwarp();
-      if (leader) mbar_arrive(&sh.item_empty[n & 1]);
+      if (leader) mbar_arrive(&sh.item_empty[n % kRing]);
     }
     if (leader) {
       if (!go) give_up(&sh.abort, a.status, 0x824);
@@ -658,11 +665,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       return make_float2(at[0][r], at[1][r]);
     };
     for (int n = 0;; ++n) {
-      if (!await_warp(&sh.item_full[n & 1], static_cast<uint32_t>(n >> 1) & 1u, &sh.abort)) {
+      if (!await_warp(&sh.item_full[n % kRing], ring_parity(n), &sh.abort)) {
         if (lane == 0) give_up(&sh.abort, a.status, 0x825);
         break;
       }
-      const Item& it = sh.item[n & 1];
+      const Item& it = sh.item[n % kRing];
       const int mode = it.mode, nsub = it.nsub, sub0 = it.sub0;
       if (mode == kEnd) break;
       const bool live = r < a.hp * a.tokens && it.t0 + t_row < it.nq && it.hc + h_row < a.group;
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         p_exp32(sv, a.c_log2, -m_ref, pk, cs);
         tmem_st16(tmem + lane_addr + s * kSubKeys + s_col + 16, pk);
         l += cs;
-        if (mode == kFast && live && cs > kOverflowSum) atomicOr(&sh.redo[n & 1], kOverflow);
+        if (mode == kFast && live && cs > kOverflowSum) atomicOr(&sh.redo[n % kRing], kOverflow);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -781,8 +788,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (live) store_row32(a.out + to + c * 32 + e, w, a.wide_out != 0);
               }
           }
-          if (mode == kFast && live && (odd & 0x7fff7fffu) != 0u) atomicOr(&sh.redo[n & 1], kNotFinite);
-          if (live && mode != kFast && *reinterpret_cast<volatile int*>(&sh.odd_v[n & 1]) != 0) {
+          if (mode == kFast && live && (odd & 0x7fff7fffu) != 0u) atomicOr(&sh.redo[n % kRing], kNotFinite);
+          if (live && mode != kFast && *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]) != 0) {
             // What guard_v took out, for the rows that see it (their p is above
             // zero): infinities and NaN, whatever the finite rest is.
             add_odd(a, it, to, partial, chunk * 64, max(all_of(it), sub0 * kSubKeys),
@@ -794,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.item_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&sh.item_empty[n % kRing]);
     }
   }
   tc_fence_before();
