@@ -560,11 +560,11 @@ def _step_of(what, step, cache):
         raise ValueError(f"{what}: the step was made for another batch or device")
 
 
-def _ints(what, t, n):
+def _ints(what, t, n, dtype):
     """The address of contiguous int32 [n] (None: a null pointer)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 [{n}]")
     return t.data_ptr()
 
@@ -579,20 +579,20 @@ def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, 
     sequence has no room, the status word says so and the step takes no tokens.
     ws: kv_append_workspace_size bytes."""
     _step_of("kv_reserve", step, cache)
-    free = _ints("kv_reserve: free_pages", free_pages, cache.num_pages)
-    num = _ints("kv_reserve: num_free", num_free, 1)
-    kept = _ints("kv_reserve: keep", keep, cache.batch)
-    new = _ints("kv_reserve: new_lens", new_lens, cache.batch)
+    batch, i32 = cache.batch, cache.tensors[5].dtype
+    free = _ints("kv_reserve: free_pages", free_pages, cache.num_pages, i32)
+    num = _ints("kv_reserve: num_free", num_free, 1, i32)
+    kept = _ints("kv_reserve: keep", keep, batch, i32)
+    new = _ints("kv_reserve: new_lens", new_lens, batch, i32)
     st = _on_device(cache, stream, free_pages, num_free, ws, keep, new_lens)
     _check(lib().crisp_kv_reserve(ctypes.byref(cache), cache.table, free, num, kept, new, ctypes.byref(step),
-                                  ws.data_ptr(), _nbytes(ws), st), "crisp_kv_reserve")
+                                  ws.data_ptr(), ws.nbytes, st), "crisp_kv_reserve")
 
 
-def _packed_tokens(what, t, rows, heads):
+def _packed_tokens(what, t, rows, heads, dtype):
     """Packed [rows][heads][128] bf16."""
-    d = t.dtype
-    if t.shape != (rows, heads, D) or d.itemsize != 2 or str(d) != "torch.bfloat16":
-        raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {d} {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != (rows, heads, D):
+        raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {t.dtype} {tuple(t.shape)}")
     i, h, e = t.stride()
     if e != 1:
         raise ValueError(f"{what}: the 128 features must be contiguous")
@@ -603,11 +603,11 @@ def kv_append_packed(cache, step, k_new, v_new, ws, stream=None):
     """Writes a step's new tokens into the cache: bf16 [max_new][hkv][128], token i
     at slots[i] (rows past the step's total are not read)."""
     _step_of("kv_append_packed", step, cache)
-    kt = _packed_tokens("kv_append_packed: k_new", k_new, step.max_new, cache.hkv)
-    vt = _packed_tokens("kv_append_packed: v_new", v_new, step.max_new, cache.hkv)
+    kt = _packed_tokens("kv_append_packed: k_new", k_new, step.max_new, cache.hkv, cache.token_dtype)
+    vt = _packed_tokens("kv_append_packed: v_new", v_new, step.max_new, cache.hkv, cache.token_dtype)
     st = _on_device(cache, stream, k_new, v_new, ws)
     _check(lib().crisp_kv_append_packed(ctypes.byref(cache), ctypes.byref(step), ctypes.byref(kt), ctypes.byref(vt),
-                                        ws.data_ptr(), _nbytes(ws), st), "crisp_kv_append_packed")
+                                        ws.data_ptr(), ws.nbytes, st), "crisp_kv_append_packed")
 
 
 def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
@@ -616,13 +616,14 @@ def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
     how many of the n rows there are (e.g. step.cu_all[-1:]; None: all). Rows of
     negative slots are left alone."""
     n = slots.shape[0] if slots.dim() == 1 else -1
-    at = _ints("kv_gather: slots", slots, n)
-    num = _ints("kv_gather: count", count, 1)
-    kt = _packed_tokens("kv_gather: k_out", k_out, n, cache.hkv)
-    vt = _packed_tokens("kv_gather: v_out", v_out, n, cache.hkv)
+    i32 = cache.tensors[5].dtype
+    at = _ints("kv_gather: slots", slots, n, i32)
+    num = _ints("kv_gather: count", count, 1, i32)
+    kt = _packed_tokens("kv_gather: k_out", k_out, n, cache.hkv, cache.token_dtype)
+    vt = _packed_tokens("kv_gather: v_out", v_out, n, cache.hkv, cache.token_dtype)
     st = _on_device(cache, stream, slots, k_out, v_out, ws, count)
     _check(lib().crisp_kv_gather(ctypes.byref(cache), at, n, num, ctypes.byref(kt), ctypes.byref(vt), ws.data_ptr(),
-                                 _nbytes(ws), st), "crisp_kv_gather")
+                                 ws.nbytes, st), "crisp_kv_gather")
 
 
 def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) -> Packed:
@@ -632,13 +633,15 @@ def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) ->
     about the longest sequence's keys (None: total_k), for how work is split; no
     limit. The structure keeps the tensors alive; their contents may change
     between calls."""
+    import torch
     n = cu_q.shape[0] if cu_q.dim() == 1 else 0
     _need(n >= 1, "make_packed: cu_q must be int32 [batch + 1]")
-    q, k = _ints("make_packed: cu_q", cu_q, n), _ints("make_packed: cu_k", cu_k, n)
+    q, k = _ints("make_packed: cu_q", cu_q, n, torch.int32), _ints("make_packed: cu_k", cu_k, n, torch.int32)
     _need(cu_q.device == cu_k.device, "make_packed: the tensors must be on one device")
     _need(max_k is None or max_k >= 0, "make_packed: max_k must not be negative")
     p = Packed(n - 1, hq, hkv, D, total_q, total_k, max_k or 0, scale, q, k)
     p.tensors, p.device_index = (cu_q, cu_k), cu_q.get_device()
+    p.sizes = (total_q, total_k, hq, hkv, torch.bfloat16)
     return p
 
 
@@ -654,13 +657,14 @@ def packed_prefill(packed, q, k, v, out, ws, stream=None):
     token and head strides that are multiples of 8 elements). Query i of a
     sequence of nq queries and nk keys sees its keys j <= nk - nq + i; rows that
     see none become zeros, rows behind the last sequence are left alone."""
-    qt = _packed_tokens("packed_prefill: q", q, packed.total_q, packed.hq)
-    kt = _packed_tokens("packed_prefill: k", k, packed.total_k, packed.hkv)
-    vt = _packed_tokens("packed_prefill: v", v, packed.total_k, packed.hkv)
-    ot = _packed_tokens("packed_prefill: out", out, packed.total_q, packed.hq)
+    total_q, total_k, hq, hkv, dtype = packed.sizes
+    qt = _packed_tokens("packed_prefill: q", q, total_q, hq, dtype)
+    kt = _packed_tokens("packed_prefill: k", k, total_k, hkv, dtype)
+    vt = _packed_tokens("packed_prefill: v", v, total_k, hkv, dtype)
+    ot = _packed_tokens("packed_prefill: out", out, total_q, hq, dtype)
     st = _on_device(packed, stream, q, k, v, out, ws)
     _check(lib().crisp_packed_prefill(ctypes.byref(packed), ctypes.byref(qt), ctypes.byref(kt), ctypes.byref(vt),
-                                      ctypes.byref(ot), ws.data_ptr(), _nbytes(ws), st), "crisp_packed_prefill")
+                                      ctypes.byref(ot), ws.data_ptr(), ws.nbytes, st), "crisp_packed_prefill")
 
 
 def wait_selftest(ws, limit_ns, stream=None):

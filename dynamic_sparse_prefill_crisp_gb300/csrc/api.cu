@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/crisp.h: argument validation,
 // workspace layout, TMA descriptors and the launch sequence of each step.
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -72,15 +73,26 @@ crisp_shape normalised(const crisp_shape& s) {
   return t;
 }
 
+// The current device's answer, asked for once a device (three attributes, half a
+// microsecond): its SM count, or that it is not sm_103.
 crisp_status check_device(int* sms = nullptr) {
-  int dev = 0, major = 0, minor = 0;
+  constexpr int kKnown = 64, kOther = -1;
+  static std::atomic<int> known[kKnown];  // 0: not asked yet
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return CRISP_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return CRISP_ERR_CUDA;
-  if (sms != nullptr && cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return CRISP_ERR_CUDA;
-  return (major == 10 && minor == 3) ? CRISP_OK : CRISP_ERR_DEVICE;
+  int count = dev >= 0 && dev < kKnown ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (count == 0) {
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return CRISP_ERR_CUDA;
+    if (major != 10 || minor != 3) count = kOther;
+    if (dev >= 0 && dev < kKnown) known[dev].store(count, std::memory_order_relaxed);
+  }
+  if (count == kOther) return CRISP_ERR_DEVICE;
+  if (sms != nullptr) *sms = count;
+  return CRISP_OK;
 }
 
 crisp_status check_ws(const crisp_shape& s, const void* ws, size_t ws_bytes) {
@@ -1094,13 +1106,11 @@ crisp_status check_packed(const crisp_packed* p) {
 int64_t used_stride(int64_t stride, int size) { return size > 1 ? stride : kD; }
 
 // q of a packed batch: boxes of 64 features x a tile's heads x its tokens.
-crisp_status make_packed_q_map(CUtensorMap* m, const crisp_packed& p, const crisp_tokens& q) {
-  int heads = 0, tokens = 0;
-  packed_q_box(p, &heads, &tokens);
+crisp_status make_packed_q_map(CUtensorMap* m, const crisp_packed& p, const PackedPlan& plan, const crisp_tokens& q) {
   const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(p.hq), static_cast<cuuint64_t>(p.total_q)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(used_stride(q.head_stride, p.hq)) * 2,
                                  static_cast<cuuint64_t>(used_stride(q.tok_stride, p.total_q)) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(plan.hp), static_cast<cuuint32_t>(plan.tokens)};
   return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q.data, dims, strides, box);
 }
 
@@ -1174,7 +1184,7 @@ crisp_status crisp_packed_workspace_size(const crisp_packed* packed, size_t* byt
     crisp_status st = check_packed(packed);
     if (st != CRISP_OK) return st;
     if (!bytes) return CRISP_ERR_INVALID_ARG;
-    *bytes = packed_layout(*packed).total;
+    *bytes = packed_layout(*packed, packed_plan(*packed)).total;
     return CRISP_OK;
   });
 }
@@ -1192,10 +1202,11 @@ crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens
     const bool keys = p.total_k > 0;  // without, every row is empty and k and v are not looked at
     if (keys && (st = check_tokens(k, 1, p.hkv, p.total_k)) != CRISP_OK) return st;
     if (keys && (st = check_tokens(v, 1, p.hkv, p.total_k)) != CRISP_OK) return st;
-    if ((st = check_cache_ws(ws, ws_bytes, packed_layout(p).total)) != CRISP_OK) return st;
+    const PackedPlan plan = packed_plan(p);
+    if ((st = check_cache_ws(ws, ws_bytes, packed_layout(p, plan).total)) != CRISP_OK) return st;
     if ((st = check_device()) != CRISP_OK) return st;
     TmaMaps maps;
-    if ((st = make_packed_q_map(&maps.q, p, *q)) != CRISP_OK) return st;
+    if ((st = make_packed_q_map(&maps.q, p, plan, *q)) != CRISP_OK) return st;
     if (keys) {
       st = make_map(&maps.k64, k->data, p.hkv, p.total_k, used_stride(k->head_stride, p.hkv),
                     used_stride(k->tok_stride, p.total_k), kB / 2);
@@ -1207,7 +1218,7 @@ crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens
       maps.k64 = maps.v = maps.q;
     }
     const float c = p.scale == 0.f ? 1.0f / std::sqrt(static_cast<float>(kD)) : p.scale;
-    return from_cuda(launch_packed(p, maps, c, keys ? *v : *q, *out, static_cast<char*>(ws), stream));
+    return from_cuda(launch_packed(p, plan, maps, c, keys ? *v : *q, *out, static_cast<char*>(ws), stream));
   });
 }
 

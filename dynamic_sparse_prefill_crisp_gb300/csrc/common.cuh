@@ -153,14 +153,22 @@ EvictLayout evict_layout(const crisp_kv_cache& src, int keep);
 DecodeLayout decode_layout(const crisp_kv_cache& c, int hq, int q_len, bool with_weights);
 int decode_row_chunks(int rows);  // row chunks of a (sequence, kv head)
 
+// How the work of crisp_packed_prefill is cut.
+struct PackedPlan {
+  int hp, chunks, tokens;  // query heads of a tile, tiles of a group's heads, queries of a tile
+  int bound;               // no batch of these sizes has more (sequence, queries) tiles
+  int heads_log2;          // kv heads (times chunks) that run side by side
+  int splits, split_subs;  // parts of a tile, sub-blocks of a part
+};
+PackedPlan packed_plan(const crisp_packed& p);
+
 // Workspace of crisp_packed_prefill (the status word comes first).
 struct PackedLayout {
   size_t part;     // fp32 [splits][total_q][hq][128]    unfinished rows
   size_t part_ml;  // float2 [splits][total_q][hq]       their references and sums
   size_t total;
 };
-PackedLayout packed_layout(const crisp_packed& p);
-void packed_q_box(const crisp_packed& p, int* heads, int* tokens);  // rows of q that a tile takes
+PackedLayout packed_layout(const crisp_packed& p, const PackedPlan& plan);
 
 // Pages that max_new new tokens of a batch can touch (runs of crisp_kv_step).
 inline int64_t max_runs(int batch, int max_new) {
@@ -225,7 +233,7 @@ cudaError_t launch_kv_reserve(const crisp_kv_cache& c, int32_t* table, int32_t* 
                               DevStatus* status, cudaStream_t st);
 cudaError_t launch_kv_gather(const crisp_kv_cache& c, const int32_t* slots, int n, const int32_t* count,
                              const crisp_tokens& k_out, const crisp_tokens& v_out, DevStatus* status, cudaStream_t st);
-cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scale, const crisp_tokens& v,
+cudaError_t launch_packed(const crisp_packed& p, const PackedPlan& plan, const TmaMaps& maps, float scale, const crisp_tokens& v,
                           const crisp_tokens& out, char* ws, cudaStream_t st);
 cudaError_t launch_kv_evict(const crisp_kv_cache& src, const crisp_kv_cache& dst, const float* weights, int keep,
                             int sink, int recent, float* new_weights, int32_t* kept, char* ws, int sms,

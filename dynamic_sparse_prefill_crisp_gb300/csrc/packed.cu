@@ -36,6 +36,7 @@
 // Warp roles: 0-7 softmax + epilogue, 8 finds tiles and issues TMA, 9 issues the
 // products (TMEM owner).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -289,20 +290,6 @@ __device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end,
     }
   }
   return odd;
-}
-
-// 32 bytes of a row, eight words, past L1 (with its lines allocated, 256 short
-// prompts took 140 us, 128 without).
-__device__ __forceinline__ void store_row32(void* to, const uint32_t* w, bool wide) {
-  if (wide) {
-    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    auto* v = static_cast<uint4*>(to);
-    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
 }
 
 // out += v_j over the keys j in [from, last] and 64 columns, where v_j is not
@@ -765,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
-                  store_row32(a.part + to + c * 32 + e, v[c] + e, true);
+                  store32(a.part + to + c * 32 + e, v[c] + e, true);
 #pragma unroll
                   for (int x = 0; x < 8; ++x) none = fmaf(__uint_as_float(v[c][e + x]), 0.f, none);
                 }
@@ -786,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                   w[x] = pack_bf16x2(lo, hi);
                   note_odd(odd, w[x]);
                 }
-                if (live) store_row32(a.out + to + c * 32 + e, w, a.wide_out != 0);
+                if (live) store32(a.out + to + c * 32 + e, w, a.wide_out != 0);
               }
           }
           if (mode == kFast && live && (odd & 0x7fff7fffu) != 0u) atomicOr(&sh.redo[n % kRing], kNotFinite);
@@ -879,9 +866,7 @@ int tile_heads(int group) {
   return div_up(group, c);
 }
 
-struct PackedPlan {
-  int hp, chunks, tokens, bound, heads_log2, splits, split_subs;
-};
+}  // namespace
 
 // A tile is split into parts of eight sub-blocks or more where that makes the
 // whole shorter: by the time of a sub-block (0.76 us with two CTAs on an SM), of
@@ -926,10 +911,7 @@ PackedPlan packed_plan(const crisp_packed& p) {
   return L;
 }
 
-}  // namespace
-
-PackedLayout packed_layout(const crisp_packed& p) {
-  const PackedPlan plan = packed_plan(p);
+PackedLayout packed_layout(const crisp_packed& p, const PackedPlan& plan) {
   const size_t rows = plan.splits > 1 ? static_cast<size_t>(p.total_q) * p.hq * plan.splits : 0;
   PackedLayout L{};
   size_t o = align_up(sizeof(DevStatus));
@@ -939,16 +921,9 @@ PackedLayout packed_layout(const crisp_packed& p) {
   return L;
 }
 
-void packed_q_box(const crisp_packed& p, int* heads, int* tokens) {
-  const PackedPlan L = packed_plan(p);
-  *heads = L.hp;
-  *tokens = L.tokens;
-}
-
-cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scale, const crisp_tokens& v,
-                          const crisp_tokens& out, char* ws, cudaStream_t st) {
-  const PackedPlan plan = packed_plan(p);
-  const PackedLayout L = packed_layout(p);
+cudaError_t launch_packed(const crisp_packed& p, const PackedPlan& plan, const TmaMaps& maps, float scale,
+                          const crisp_tokens& v, const crisp_tokens& out, char* ws, cudaStream_t st) {
+  const PackedLayout L = packed_layout(p, plan);
   PackedArgs a{};
   a.cu_q = p.cu_q;
   a.cu_k = p.cu_k;
@@ -978,9 +953,18 @@ cudaError_t launch_packed(const crisp_packed& p, const TmaMaps& maps, float scal
   a.wide_out = reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && (p.hq == 1 || out.head_stride % 16 == 0) &&
                (p.total_q == 1 || out.tok_stride % 16 == 0);
   const size_t smem = kSmemBytes + batch_bytes(p.batch);
-  cudaError_t e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
+  // the most that any batch takes, once a device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   // (heads side by side, tiles), parts, groups of heads; a tile holds more than 64
   // of at most 2^24 x 4096 rows
   const dim3 grid(static_cast<unsigned>(plan.bound) << plan.heads_log2, static_cast<unsigned>(plan.splits),

@@ -22,7 +22,8 @@ namespace {
 // of a thread for every four, which spreads over the GPU.
 constexpr int kPlanThreads = 1024;
 constexpr int kSums = 5;
-constexpr int kFewTokens = 8192;
+constexpr int kHeld = 4;
+constexpr int kFewTokens = 4096;
 constexpr int kMapThreads = 256;
 constexpr int kMapTokens = 4 * kMapThreads;
 
@@ -59,9 +60,9 @@ __device__ __forceinline__ int slot_of(int id, int pos, int num_pages) {
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_constant__ ReserveArgs a) {
   __shared__ Sums sums;
   __shared__ int keeps[kMaxBatch], warp_sums[kSums][32];
-  __shared__ int problem;
+  __shared__ int problem, bad_page;
   const int b = threadIdx.x, warp = b >> 5, lane = b & 31;
-  if (b == 0) problem = 0;
+  if (b == 0) problem = bad_page = 0;
   grid_dep_launch();
   grid_dep_wait();
   const int cap = a.max_pages * kB;
@@ -111,54 +112,78 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
   const int total_new = sums.cu_new[n], total_all = sums.cu_all[n], freed = sums.freed[n], taken = sums.taken[n],
             runs = sums.runs[n];
   const int top = had_free + freed;
-  if (problem == 0) {
-    if (top > a.num_pages || total_new > a.step.max_new || (a.step.max_all > 0 && total_all > a.step.max_all)) {
-      if (b == 0) problem = CRISP_ERR_BOUNDS;
-    } else {
-      // pages to give back have to be pages
-      for (int k = b; k < freed; k += kPlanThreads) {
-        const int q = holder(sums.freed, n, k);
-        const int id = a.table[static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + k - sums.freed[q]];
-        if (id < 0 || id >= a.num_pages) problem = CRISP_ERR_BOUNDS;
-      }
+  // Page k of those given back or taken, counted over the batch: its place in the table.
+  auto place = [&](const int* before, int k) {
+    const int q = holder(before, n, k);
+    return static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + k - before[q];
+  };
+  // The pages to give back, the first kHeld of a thread's with their places in registers
+  int64_t at[kHeld];
+  int id[kHeld];
+  const bool fits = problem == 0 && top <= a.num_pages && total_new <= a.step.max_new &&
+                    (a.step.max_all == 0 || total_all <= a.step.max_all);
+  if (fits) {
+    bool none = false;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int k = b + e * kPlanThreads;
+      at[e] = k < freed ? place(sums.freed, k) : 0;
     }
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      id[e] = b + e * kPlanThreads < freed ? a.table[at[e]] : 0;
+      none = none || id[e] < 0 || id[e] >= a.num_pages;
+    }
+    for (int k = b + kHeld * kPlanThreads; k < freed; k += kPlanThreads) {
+      const int page = a.table[place(sums.freed, k)];
+      none = none || page < 0 || page >= a.num_pages;
+    }
+    if (none) bad_page = 1;  // what is given back has to be a page
   }
   __syncthreads();
-  if (problem != 0 || taken > top) {
-    if (b == 0) report_error(a.status, problem != 0 ? CRISP_ERR_BOUNDS : CRISP_ERR_PAGES, 0x901);
+  if (!fits || bad_page != 0 || taken > top) {
+    if (b == 0) report_error(a.status, fits && bad_page == 0 ? CRISP_ERR_PAGES : CRISP_ERR_BOUNDS, 0x901);
     for (int i = b; i <= n; i += kPlanThreads) a.step.cu_new[i] = a.step.cu_all[i] = 0;
     for (int i = b; i <= a.runs; i += kPlanThreads) a.step.runs[i] = 0;
     return;
   }
   // Pages go back in the order in which taking them again gives each its old place.
-  for (int k = b; k < freed; k += kPlanThreads) {
-    const int q = holder(sums.freed, n, k);
-    a.free_pages[top - 1 - k] = a.table[static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + k - sums.freed[q]];
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e)
+    if (b + e * kPlanThreads < freed) {
+      a.free_pages[top - 1 - (b + e * kPlanThreads)] = id[e];
+      a.table[at[e]] = -1;
+    }
+  for (int k = b + kHeld * kPlanThreads; k < freed; k += kPlanThreads) {
+    int32_t* entry = a.table + place(sums.freed, k);
+    a.free_pages[top - 1 - k] = *entry;
+    *entry = -1;
   }
+  if (b == 0) *a.num_free = top - taken;
   __syncthreads();
-  for (int k = b; k < freed; k += kPlanThreads) {
-    const int q = holder(sums.freed, n, k), page = k - sums.freed[q];  // counted from the first not kept
-    if (page >= sums.taken[q + 1] - sums.taken[q])
-      a.table[static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + page] = -1;
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) {
+    const int k = b + e * kPlanThreads;
+    at[e] = k < taken ? place(sums.taken, k) : 0;
+    id[e] = k < taken ? a.free_pages[top - 1 - k] : 0;
   }
-  for (int k = b; k < taken; k += kPlanThreads) {
-    const int q = holder(sums.taken, n, k);
-    a.table[static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + k - sums.taken[q]] =
-        a.free_pages[top - 1 - k];
-  }
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e)
+    if (b + e * kPlanThreads < taken) a.table[at[e]] = id[e];
+  for (int k = b + kHeld * kPlanThreads; k < taken; k += kPlanThreads)
+    a.table[place(sums.taken, k)] = a.free_pages[top - 1 - k];
   for (int i = b; i <= n; i += kPlanThreads) {
     a.step.cu_new[i] = sums.cu_new[i];
     a.step.cu_all[i] = sums.cu_all[i];
     if (i < n) a.lens[i] = sums.cu_all[i + 1] - sums.cu_all[i];
   }
-  if (b == 0) *a.num_free = top - taken;
   for (int j = b; j <= a.runs; j += kPlanThreads) {
-    int at = total_new;
+    int first = total_new;
     if (j < runs) {
       const int q = holder(sums.runs, n, j), page = keeps[q] / kB + j - sums.runs[q];
-      at = max(page * kB, keeps[q]) - keeps[q] + sums.cu_new[q];
+      first = max(page * kB, keeps[q]) - keeps[q] + sums.cu_new[q];
     }
-    a.step.runs[j] = at;
+    a.step.runs[j] = first;
   }
   if (a.write_maps == 0) return;
   __syncthreads();  // the table is written
@@ -179,8 +204,10 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
 __global__ void __launch_bounds__(kMapThreads) maps_kernel(const __grid_constant__ ReserveArgs a, int new_blocks) {
   grid_dep_launch();
   grid_dep_wait();
+  __shared__ int cu[kMaxBatch + 1];
   const bool all = static_cast<int>(blockIdx.x) >= new_blocks;
-  const int32_t* cu = all ? a.step.cu_all : a.step.cu_new;
+  for (int q = threadIdx.x; q <= a.batch; q += kMapThreads) cu[q] = (all ? a.step.cu_all : a.step.cu_new)[q];
+  __syncthreads();
   const int total = cu[a.batch];
   const int i0 = (static_cast<int>(blockIdx.x) - (all ? new_blocks : 0)) * kMapTokens + static_cast<int>(threadIdx.x) * 4;
   if (i0 >= total) return;
@@ -230,6 +257,7 @@ struct GatherArgs {
   const int32_t *slots, *count;
   int n;
   crisp_tokens k_out, v_out;
+  bool k_wide, v_wide;  // every row of a head starts at a multiple of 32 bytes
   DevStatus* status;
 };
 
@@ -257,22 +285,18 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
   const float* scale = (is_v ? a.v_scale : a.k_scale) + static_cast<int64_t>(id) * a.hkv;
   const crisp_tokens& t = is_v ? a.v_out : a.k_out;
   auto* out = static_cast<__nv_bfloat16*>(const_cast<void*>(t.data)) + i * t.tok_stride + col;
+  const bool wide = is_v ? a.v_wide : a.k_wide;
 #pragma unroll 4
   for (int g = 0; g < a.hkv; ++g) {
     const uint4 c = __ldcs(reinterpret_cast<const uint4*>(codes + g * a.head_stride));
     const float s = scale[g];
-    uint4 lo, hi;
-    lo.x = scaled_pair(c.x, s);
-    lo.y = scaled_pair(c.x >> 16, s);
-    lo.z = scaled_pair(c.y, s);
-    lo.w = scaled_pair(c.y >> 16, s);
-    hi.x = scaled_pair(c.z, s);
-    hi.y = scaled_pair(c.z >> 16, s);
-    hi.z = scaled_pair(c.w, s);
-    hi.w = scaled_pair(c.w >> 16, s);
-    auto* to = reinterpret_cast<uint4*>(out + g * t.head_stride);
-    to[0] = lo;
-    to[1] = hi;
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[2 * e] = scaled_pair((&c.x)[e], s);
+      w[2 * e + 1] = scaled_pair((&c.x)[e] >> 16, s);
+    }
+    store32(out + g * t.head_stride, w, wide);
   }
 }
 
@@ -320,6 +344,12 @@ cudaError_t launch_kv_gather(const crisp_kv_cache& c, const int32_t* slots, int 
   a.n = n;
   a.k_out = k_out;
   a.v_out = v_out;
+  auto wide = [&](const crisp_tokens& t) {
+    return reinterpret_cast<uintptr_t>(t.data) % 32 == 0 && (c.hkv == 1 || t.head_stride % 16 == 0) &&
+           (n == 1 || t.tok_stride % 16 == 0);
+  };
+  a.k_wide = wide(k_out);
+  a.v_wide = wide(v_out);
   a.status = status;
   return launch_dependent(gather_kernel, dim3(static_cast<unsigned>((n + kGatherRows - 1) / kGatherRows), 2),
                           kGatherThreads, 0, st, a);
