@@ -800,7 +800,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // The rows of split tiles: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
 // with M the largest reference m_s, in the order of the splits. A warp per row.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
+constexpr int kJoinAhead = 4;
 __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __grid_constant__ PackedArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.hq;
@@ -828,23 +829,39 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
     const float2 ml = a.part_ml[s * rows + row];
     if (ml.y != 0.f) top = fmaxf(top, ml.x);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = warp_max(top);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  const float* part = a.part + row * kD + lane * 4;
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
-    const float2 ml = a.part_ml[s * rows + row];
-    const float4 o = *reinterpret_cast<const float4*>(part + s * rows * kD);
-    if (ml.y == 0.f) continue;
-    const float w = ex2_approx(ml.x - top);
-    l = fmaf(ml.y, w, l);
-    acc.x = fmaf(o.x, w, acc.x);
-    acc.y = fmaf(o.y, w, acc.y);
-    acc.z = fmaf(o.z, w, acc.z);
-    acc.w = fmaf(o.w, w, acc.w);
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    // each lane a part's weight, then all lanes part after part, four rows in flight
+    float w = 0.f;
+    if (s0 + lane < ns) {
+      const float2 ml = a.part_ml[(s0 + lane) * rows + row];
+      w = ml.y != 0.f ? ex2_approx(ml.x - top) : 0.f;
+      l += w != 0.f ? ml.y * w : 0.f;
+    }
+    const float* part = a.part + (s0 * rows + row) * kD + lane * 4;
+    const int parts = min(32, ns - s0);
+#pragma unroll 1
+    for (int s = 0; s < parts; s += kJoinAhead) {
+      float4 o[kJoinAhead];
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e)
+        if (s + e < parts) o[e] = *reinterpret_cast<const float4*>(part + (s + e) * rows * kD);
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const float ws = __shfl_sync(0xffffffffu, w, (s + e) & 31);
+        if (s + e < parts && ws != 0.f) {
+          acc.x = fmaf(o[e].x, ws, acc.x);
+          acc.y = fmaf(o[e].y, ws, acc.y);
+          acc.z = fmaf(o[e].z, ws, acc.z);
+          acc.w = fmaf(o[e].w, ws, acc.w);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l != 0.f ? 1.f / l : 0.f;
   *reinterpret_cast<uint2*>(a.out + head * a.o_hs + tok * a.o_ts + lane * 4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
