@@ -21,7 +21,6 @@ struct SlotCounts {
   uint32_t v = 0u;
   __device__ __forceinline__ uint32_t parity(int s) const { return (v >> (16 * s)) & 1u; }
   __device__ __forceinline__ void inc(int s) { v += 1u << (16 * s); }
-  __device__ __forceinline__ bool any(int s) const { return (v >> (16 * s) & 0xffffu) != 0u; }
 };
 
 __device__ __forceinline__ void fail(int* abort, DevStatus* st, uint32_t where) {

@@ -9,15 +9,20 @@
 // where rows of one head alone would leave it empty. A block of the grid stands
 // for a tile (or a part of one, see below): the sequences of most keys first, each
 // from its last tile to its first, the kv heads side by side or in turn
-// (packed_plan). A block's tile follows
-// from the lengths, so that no schedule has to be made or kept. (In the order of
-// all tiles' keys, the search for a tile took 5000 cycles, three sub-blocks.)
+// (packed_plan). A block's tile follows from the lengths, so that no schedule has
+// to be made or kept. (In the order of all tiles' keys, the search for a tile took
+// 5000 cycles, four sub-blocks.)
 //
 // Two CTAs stay on each SM and take over blocks that have not started, one
 // ahead: the next tile's Q and first K and V are on their way while this one's
 // softmax and epilogue run. Short prompts need that (256 of up to 300 tokens,
-// 28/4 heads: XX us; a CTA per tile, whose start, loads and end came one after
-// the other, 340 us).
+// 28/4 heads: 127 us, 5.0 TB/s; a CTA per tile, whose start, loads and end came
+// one after the other, 340 us).
+//
+// Long prompts are bound by the tensor pipe at the rate of its 64-key products (a
+// product's operands come from shared memory at 128 bytes a cycle, 48 cycles where
+// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.24 ms, 1778
+// TFLOP/s, a sub-block 1225 cycles a CTA and 612 an SM.
 //
 // The products are csrc/attention.cu's: 64-key sub-blocks, two score buffers in
 // TMEM, the first sub-block's row maximum as the reference. What differs:
@@ -61,9 +66,9 @@ constexpr int kRing = 4;                                  // items on their way 
 constexpr int kAskAhead = 4;                              // sub-blocks before the end at which the next block is asked for
 constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,128), O [128,256)
 
-// What the CTA does with a tile: kFast; then, where its result is not finite,
-// kGuarded, the same but for a look through V; or, where it met an overflow,
-// kMaxOnly and kFixed (with that look too).
+// What the CTA does with a tile: kFast; then, where a result is not finite,
+// kGuarded, the same but for a look through V; and where sums left their range (or
+// kGuarded's results are not finite either), kMaxOnly and kFixed, with that look too.
 enum Mode : int { kFast, kGuarded, kMaxOnly, kFixed, kEnd };
 constexpr uint32_t batch_bytes(int batch) { return batch * 6u + 8u; }  // ranks and order
 
@@ -111,10 +116,19 @@ struct Shared {
   uint4 answer;          // about a block to take over
   uint32_t tmem_base;
   int abort;
-  int redo[kRing];       // Redo bits: a result of the slot's item is not finite, a chunk row sum passed kOverflowSum
-  int odd_v[kRing];      // a partly seen V element of the slot's item is not finite
+  int redo[kRing];       // Redo bits: the slot's item has to be done again
+  int odd_v[kRing];      // OddV bits of the slot's item, where it was looked through
   Item item[kRing], again[kRing];
   float xch[2][2][kB];   // [exchange & 1][chunk][row]: partial row maxima, partial row sums
+};
+
+// The phases of the barriers of two slots, and whether a slot was used at all. (Bits,
+// not counts: a CTA that stays passes any number of them.)
+struct SlotPhases {
+  uint32_t v = 0u;
+  __device__ __forceinline__ uint32_t parity(int s) const { return v >> s & 1u; }
+  __device__ __forceinline__ void inc(int s) { v = (v ^ 1u << s) | 4u << s; }
+  __device__ __forceinline__ bool any(int s) const { return (v >> s & 4u) != 0u; }
 };
 
 __host__ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -225,10 +239,10 @@ __device__ __forceinline__ bool await_warp(uint64_t* bar, uint32_t parity, const
 }
 __device__ __noinline__ void give_up(int* abort, DevStatus* st, uint32_t where) { fail(abort, st, where); }
 
-// One lane of a converged warp (and which). Code under this condition is known to
-// run in one lane: descriptors then stay in uniform registers, where code under
-// `lane == 0` takes a loop over the lanes for each product (one QK: 360
-// instructions, 160 so).
+// One lane of a converged warp, and which. Code under this condition is known to
+// run in one lane, and keeps descriptors in uniform registers; under `lane == 0`
+// the products took longer to issue than to run (16k tokens, 8/8 heads: 320 us,
+// 370 so).
 __device__ __forceinline__ bool elect_lane(int& lane) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync %1|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok), "=r"(lane));
@@ -251,12 +265,14 @@ __device__ __forceinline__ void note_odd(uint32_t& acc, uint32_t w) {
 // bytes in a row) safe to multiply with p = 0: rows from `seen_end` on are no
 // keys of this tile and become zeros, and in rows from `all_end` on, which some
 // of the tile's rows do not see, elements that are not finite become zero.
-// Returns whether there were such elements. One warp, eight lanes a row, eight
-// reads in flight; swizzling moves 16-byte pieces inside a row only.
-__device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end, int lane) {
-  bool odd = false;
+// Returns OddV bits. One warp, eight lanes a row, eight reads in flight; swizzling
+// moves 16-byte pieces inside a row only.
+enum OddV : int { kOddSeen = 1, kOddTaken = 2 };  // not finite: an element of the tile's keys; one that became zero
+__device__ __forceinline__ int guard_v(uint8_t* sub, int all_end, int seen_end, int lane) {
+  int odd = 0;
   uint8_t* mine = sub + (lane >> 3) * 128 + (lane & 7) * 16;
-  for (int row0 = max(all_end, 0) & ~15; row0 < kSubKeys; row0 += 16) {
+#pragma unroll 1
+  for (int row0 = 0; row0 < kSubKeys; row0 += 16) {
     uint4 x[4][2];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -266,7 +282,7 @@ __device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end,
         uint4* at = reinterpret_cast<uint4*>(mine + half * kSubHalf + (row0 + 4 * u) * 128);
         x[u][half] = make_uint4(0u, 0u, 0u, 0u);
         if (row >= seen_end) *at = x[u][half];
-        else if (row >= all_end) x[u][half] = *at;
+        else x[u][half] = *at;
       }
     }
     uint32_t acc = 0u;
@@ -277,7 +293,7 @@ __device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end,
 #pragma unroll
         for (int e = 0; e < 4; ++e) note_odd(acc, (&x[u][half].x)[e]);
     if ((acc & 0x7fff7fffu) == 0u) continue;
-    odd = true;
+    odd |= kOddSeen;
 #pragma unroll 1
     for (int e = 0; e < 4 * 2 * 4; ++e) {  // word by word
       const int u = e >> 3, half = e >> 2 & 1;
@@ -286,6 +302,7 @@ __device__ __forceinline__ bool guard_v(uint8_t* sub, int all_end, int seen_end,
       uint32_t w = *at;
       if (odd_bf16(w)) w &= 0xffff0000u;
       if (odd_bf16(w >> 16)) w &= 0x0000ffffu;
+      if (w != *at) odd |= kOddTaken;
       *at = w;
     }
   }
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kTmaWarp) {
     int from;  // the lane that issues
     const bool leader = elect_lane(from);
-    SlotCounts kn, vn;  // loads issued per slot
+    SlotPhases kn, vn;  // loads issued per slot
     uint32_t loads = 0u, asks = 0u;
     bool asked = false, have = true, go = true;
     uint3 block = blockIdx;
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int s = t & 1;
         uint64_t* empty = is_k ? &sh.s_full[s] : &sh.v_empty[s];
         uint64_t* full = is_k ? &sh.k_full[s] : &sh.v_full[s];
-        SlotCounts& cnt = is_k ? kn : vn;
+        SlotPhases& cnt = is_k ? kn : vn;
         if (!await(empty, cnt.parity(s) ^ 1u, &sh.abort)) {
           give_up(&sh.abort, a.status, is_k ? 0x821 : 0x822);
           return false;
@@ -529,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t dk0 = sdesc_sw128(smem_u32(sK), 16, 1024);       // slot 0; slot 1 behind it
     const uint64_t dv0 = sdesc_sw128(smem_u32(sV), kSubHalf, 1024);
-    SlotCounts kn, vn, pn;               // loads and p_full phases consumed per slot
-    uint32_t q_items = 0u, o_items = 0u; // items with products; with second products
+    SlotPhases kn, vn, pn;               // loads and p_full phases consumed per slot
+    uint32_t q_items = 0u, o_items = 0u;  // items with products; with second products
     bool go = true;
     for (int n = 0;; ++n) {
       if (leader) go = go && await(&sh.item_full[n % kRing], ring_parity(n), &sh.abort);
@@ -599,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
               if (!go) break;
-              if (guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane))
-                *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]) = 1;
+              const int odd = guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane);
+              if (odd != 0) atomicOr(&sh.odd_v[n % kRing], odd);
               fence_async_shared();
               __syncwarp();
             }
@@ -635,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int t_row = r / a.hp, h_row = r % a.hp;  // query of the tile, head of the tile
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_col = static_cast<uint32_t>(chunk * 32);
-    SlotCounts sn;  // s_full phases consumed per slot
+    SlotPhases sn;  // s_full phases consumed per slot
     uint32_t o_items = 0u, x_phase = 0u;
     float m_ref = 0.f;
     bool ok = true;
@@ -776,8 +793,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (live) store32(a.out + to + c * 32 + e, w, a.wide_out != 0);
               }
           }
-          if (mode == kFast && live && (odd & 0x7fff7fffu) != 0u) atomicOr(&sh.redo[n % kRing], kNotFinite);
-          if (live && mode != kFast && *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]) != 0) {
+          // Not finite: V may not be. Where it is, or a row that sees keys sums to 0, the
+          // sums may have left fp32's range.
+          const int odd_v = mode == kFast ? 0 : *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]);
+          if (live && (odd & 0x7fff7fffu) != 0u && mode <= kGuarded && (odd_v & kOddSeen) == 0)
+            atomicOr(&sh.redo[n % kRing], mode == kFast ? kNotFinite : kOverflow);
+          if (live && mode == kFast && l_row == 0.f && pos >= sub0 * kSubKeys) atomicOr(&sh.redo[n % kRing], kOverflow);
+          if (live && (odd_v & kOddTaken) != 0) {
             // What guard_v took out, for the rows that see it (their p is above
             // zero): infinities and NaN, whatever the finite rest is.
             add_odd(a, it, to, partial, chunk * 64, max(all_of(it), sub0 * kSubKeys),

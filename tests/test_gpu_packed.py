@@ -590,3 +590,147 @@ def test_two_turns_of_a_batch(captured):
                          va[:sum(x.ref.lens)].double().cpu().numpy(), [1, 1, 1], x.ref.lens)
     check(out[:3], ref, tol)
     assert (np.abs(got[:, :, 0].double().cpu().numpy() - ref) <= 2 * tol).all()
+
+
+# --------------------------------------------------------- the largest, the oddest
+def sampled_rows(q, k, v, rows, off):
+    """Attention of some rows of one sequence and head in 64 bits on the GPU, and its tolerance."""
+    out, tol = [], []
+    for i in rows:
+        n = off + i + 1
+        s = (k[:n, 0].double() @ q[i, 0].double()) * D ** -0.5
+        p = torch.softmax(s, 0)
+        ds = (D ** -0.5 * 2.0 ** -15.9 * (k[:n, 0].double().abs() @ q[i, 0].double().abs())).max()
+        o, a = p @ v[:n, 0].double(), p @ v[:n, 0].double().abs()
+        out.append(o)
+        tol.append(2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -20 + 2 * (n / 8 + 32) * 2.0 ** -23 + 2 * ds) * a)
+    return torch.stack(out), torch.stack(tol)
+
+
+def test_a_prompt_of_a_million_tokens():
+    # a CTA passes more than 2^16 sub-blocks of each of its two slots
+    n = 1 << 20
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    q, k, v = (torch.randn((n, 1, D), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(3))
+    cu = dev32([0, n])
+    p = crisp.make_packed(1, 1, cu, cu, n, n)
+    ws = workspace(crisp.packed_workspace_size(p))
+    out = torch.full_like(q, float("nan"))
+    crisp.packed_prefill(p, q, k, v, out, ws)
+    assert crisp.read_status(ws) == OK
+    assert torch.isfinite(out).all()
+    rows = [0, 1, 63, 64, 127, 128, 99_999, 500_000, n - 129, n - 128, n - 2, n - 1]
+    want, tol = sampled_rows(q, k, v, rows, 0)
+    assert ((out[rows, 0].double() - want).abs() <= tol).all()
+
+
+def test_rows_past_32_bit_offsets():
+    # rows 24 k elements apart: the last sequence starts past 2^31 elements (and 2^32 bytes)
+    stride, room = 24 * 1024, 90_000
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    flat = torch.empty(room * stride, dtype=torch.bfloat16, device="cuda")
+    rows = flat.view(room, stride // D, D)
+    q, k, v, out = rows[:, :4], rows[:, 4:6], rows[:, 6:8], rows[:, 8:12]
+    q_lens = [300, room - 700, 400]
+    cu = dev32(starts(q_lens))
+    first, last = slice(0, 300), slice(room - 400, room)
+    for t in (q, k, v, out):
+        t.fill_(float("nan"))
+        for part in (first, last):
+            t[part] = torch.randn(t[part].shape, generator=gen, device="cuda").to(torch.bfloat16)
+    out.fill_(float("nan"))
+    # the middle sequence's queries are left out (a key sequence of its length, no queries)
+    cu_q = dev32([0, 300, 300, 700])
+    qs = torch.cat([q[first], q[last]])
+    p = crisp.make_packed(4, 2, cu_q, cu, 700, room)
+    ws = workspace(crisp.packed_workspace_size(p))
+    got = torch.full_like(qs, float("nan"))
+    crisp.packed_prefill(p, qs, k, v, got, ws)
+    assert crisp.read_status(ws) == OK
+    keys, values = (torch.cat([t[first], t[last]]).double().cpu().numpy() for t in (k, v))
+    want, tol = attention(qs.double().cpu().numpy(), keys, values, [300, 400], [300, 400])
+    check(got, want, tol)
+    # and the same rows of q and out where they are
+    cu_q = dev32([room - 400, room])
+    cu_k = dev32([room - 400, room])
+    p = crisp.make_packed(4, 2, cu_q, cu_k, room, room, max_k=400)
+    ws = workspace(crisp.packed_workspace_size(p))
+    crisp.packed_prefill(p, q, k, v, out, ws)
+    assert crisp.read_status(ws) == OK
+    check(out[last], want[300:], tol[300:])
+    assert torch.isnan(out[:room - 400]).all()
+
+
+@pytest.mark.parametrize("shift", [0, 8])
+def test_rows_at_16_byte_addresses(shift):
+    # out rows that start at odd multiples of 16 bytes (and gathered rows)
+    lens = [70, 130]
+    q, k, v = inputs(4, 2, lens, lens, 53)
+    want, tol = attention(*(x.double().numpy() for x in (q, k, v)), lens, lens)
+    wide = torch.full((200, 4, D + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = wide[..., 8 + shift:8 + shift + D]
+    got = prefill(q, k, v, lens, lens, out=out)
+    check(got, want, tol)
+    assert torch.isnan(wide[..., :8 + shift]).all() and torch.isnan(wide[..., 8 + shift + D:]).all()
+    pools = Pools(2, 3)
+    codes = np.random.default_rng(1).integers(0, 127, (2, 3, B, D)).astype(np.uint8)
+    for t, s in ((pools.k, pools.ks), (pools.v, pools.vs)):
+        t.copy_(torch.from_numpy(codes))
+        s.fill_(0.5)
+    cache = pools.cache([[0]], [0])
+    ws = workspace(256)
+    outs = [torch.full((100, 3, D + 24), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    parts = [o[..., 8 + shift:8 + shift + D] for o in outs]
+    slots = np.arange(100) * 2 + 7
+    crisp.kv_gather(cache, dev32(slots), *parts, ws)
+    assert crisp.read_status(ws) == OK
+    for o, part in zip(outs, parts):
+        assert np.array_equal(part.double().cpu().numpy(), VALUES[codes[slots // B, :, slots % B]] * 0.5)
+        assert (o[..., :8 + shift] == 7.0).all() and (o[..., 8 + shift + D:] == 7.0).all()
+
+
+def test_large_values_do_not_leave_the_range_of_sums():
+    # V near 2^100 with scores that grow by up to 60 binary orders from the first keys on: the first
+    # reference would take the sums past fp32's largest number
+    n = 400
+    q, k, v = (x.double().numpy() for x in inputs(4, 1, [n], [n], 54))
+    q[:, :, 0] = 1.0
+    q[:, :, 1:] *= 0.1
+    k[:, 0, 0] = np.where(np.arange(n) < 64, 0.0, 40.0 * np.log(2.0) * np.sqrt(D))
+    v *= 2.0 ** 100
+    qb, kb, vb = bf16(q), bf16(k), bf16(v)
+    want, tol = attention(qb.double().numpy(), kb.double().numpy(), vb.double().numpy(), [n], [n])
+    check(prefill(qb, kb, vb, [n], [n]), want, tol)
+
+
+def test_many_tiles_done_again():
+    # every tile of every sequence sums past its range, or holds a NaN that some rows do not see
+    lens = [150] * 40
+    q, k, v = inputs(8, 2, lens, lens, 55)
+    k = k.clone()
+    for b in range(40):
+        k[150 * b + 100:150 * (b + 1), :, 0] = 300.0
+    q[:, :, 0] = q[:, :, 0].abs() + 2
+    want, tol = attention(*(x.double().numpy() for x in (q, k, v)), lens, lens)
+    check(prefill(q, k, v, lens, lens), want, tol)
+    v2 = v.clone()
+    for b in range(40):
+        v2[150 * b + 140:150 * b + 150] = float("nan")
+    got = prefill(q, k, v2, lens, lens).view(40, 150, 8, D)
+    seen = got[:, :140].reshape(-1, 8, D)
+    rows = [150 * b + i for b in range(40) for i in range(140)]
+    check(seen, want[rows], tol[rows])
+    assert torch.isnan(got[:, 140:].float()).all()
+
+
+def test_a_key_of_minus_infinity_is_left_out():
+    # the first sub-block's scores are all -inf for some heads: the rows go by the others
+    n = 200
+    q, k, v = inputs(2, 1, [n], [n], 56)
+    q[:, :, 0] = 1.0
+    k = k.clone()
+    k[:64, 0, 0] = float("-inf")
+    k[64:, 0, 0] = -300.0
+    want, tol = attention(q[64:].double().numpy(), k[64:].double().numpy(), v[64:].double().numpy(), [n - 64], [n - 64])
+    got = prefill(q, k, v, [n], [n])
+    check(got[64:], want, tol)
