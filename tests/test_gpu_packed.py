@@ -1,6 +1,9 @@
 """Batches of packed sequences on the GPU against their restatements on the CPU:
 causal attention, handing out pages, writing packed tokens, reading them back,
 and all of them together over two turns of a batch of requests."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +15,7 @@ from packed_helpers import B, D, Requests, attention, check, dev32, starts
 pytestmark = pytest.mark.gpu
 
 OK, BOUNDS, PAGES = 0, 8, 9
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def workspace(nbytes):
@@ -734,3 +738,88 @@ def test_a_key_of_minus_infinity_is_left_out():
     want, tol = attention(q[64:].double().numpy(), k[64:].double().numpy(), v[64:].double().numpy(), [n - 64], [n - 64])
     got = prefill(q, k, v, [n], [n])
     check(got[64:], want, tol)
+
+
+# --------------------------------------------------------------------- as documented
+def test_the_readme_example_of_a_batch():
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
+    blocks = [b for b in blocks if "make_packed" in b]
+    assert len(blocks) == 1
+    hq, hkv, max_new, max_all, pages = 8, 2, 600, 900, 20
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    rand = lambda n, h: torch.randn((n, h, D), generator=gen, device="cuda").to(torch.bfloat16)
+    pools = Pools(pages, hkv)
+    cache = pools.cache([[-1] * 6] * 3, [0] * 3)
+    names = dict(torch=torch, crisp=crisp, cache=cache, pages=pages, hq=hq, hkv=hkv, max_new=max_new, max_all=max_all,
+                 keep=dev32([0, 0, 0]), counts=dev32([300, 17, 200]), q=rand(max_new, hq), k=rand(max_new, hkv),
+                 v=rand(max_new, hkv), out=torch.zeros((max_new, hq, D), dtype=torch.bfloat16, device="cuda"),
+                 k_all=rand(max_all, hkv), v_all=rand(max_all, hkv))
+    exec(blocks[0], names)
+    assert crisp.read_status(names["ws"]) == OK
+    assert cache.tensors[5].tolist() == [300, 17, 200] and int(names["num_free"]) == pages - 3 - 1 - 2
+    n = 517
+    want, tol = attention(names["q"][:n].double().cpu().numpy(), names["k_all"][:n].double().cpu().numpy(),
+                          names["v_all"][:n].double().cpu().numpy(), [300, 17, 200], [300, 17, 200])
+    check(names["out"][:n], want, tol)
+
+
+def test_a_step_that_does_not_fit_leaves_everything():
+    x = Batch(2, 4, 5, 600, 1024, hkv=2, seed=8)
+    x.reserve(None, [300, 200])
+    k = torch.ones((600, 2, D), dtype=torch.bfloat16, device="cuda")
+    crisp.kv_append_packed(x.cache, x.step, k, k, x.ws)
+    before = x.pools.host()
+    x.reserve(None, [10, 300], PAGES)
+    q = torch.ones((600, 4, D), dtype=torch.bfloat16, device="cuda")
+    out, back = torch.full_like(q, 3.0), torch.full((1024, 2, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    crisp.workspace_init(x.ws)
+    crisp.kv_append_packed(x.cache, x.step, 2 * k, 2 * k, x.ws)
+    crisp.kv_gather(x.cache, x.step.all_slots, back, back.clone(), x.ws, count=x.step.cu_all[-1:])
+    p = crisp.make_packed(4, 2, x.step.cu_new, x.step.cu_all, 600, 1024)
+    ws = workspace(crisp.packed_workspace_size(p))
+    crisp.packed_prefill(p, q, back, back, out, ws)
+    assert crisp.read_status(x.ws) == OK and crisp.read_status(ws) == OK
+    assert (out == 3.0).all() and (back == 3.0).all()
+    for a, b in zip(before, x.pools.host()):
+        assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
+
+
+def test_many_slots_and_a_long_request():
+    # the maps of many tokens (a launch of their own), requests of no token between long ones
+    x = Batch(7, 120, 300, 40_000, 50_000, seed=9)
+    x.reserve(None, [0, 15_000, 0, 1, 9_000, 0, 127])
+    x.reserve([0, 15_000, 0, 0, 8_900, 0, 127], [1, 100, 0, 12_345, 3, 0, 1])
+    x.reserve(None, [0] * 7)
+    x.reserve([0] * 7, [5, 6, 7, 8, 9, 10, 11])
+
+
+def test_host_threads_at_once():
+    # the same structures from several host threads, each with its stream and workspace
+    import threading
+    q_lens, k_lens = [200, 30], [200, 900]
+    q, k, v = (t.cuda() for t in inputs(8, 2, q_lens, k_lens, 57))
+    cu_q, cu_k = dev32(starts(q_lens)), dev32(starts(k_lens))
+    p = crisp.make_packed(8, 2, cu_q, cu_k, len(q), len(k))
+    ws = [workspace(crisp.packed_workspace_size(p)) for _ in range(4)]
+    outs = [torch.zeros_like(q) for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            for _ in range(30):
+                crisp.packed_prefill(p, q, k, v, outs[i], ws[i], stream=streams[i])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and all(crisp.read_status(w) == OK for w in ws)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    want, tol = attention(*(t.double().cpu().numpy() for t in (q, k, v)), q_lens, k_lens)
+    check(outs[0], want, tol)
