@@ -149,11 +149,12 @@ def load_library(path):
     L.crisp_decode_attention.argtypes = [P(KVCache), i32, i32, ctypes.c_float, P(Tokens), P(Tokens), vp, vp, vp, sz,
                                          st]
     L.crisp_kv_evict.argtypes = [P(KVCache), P(KVCache), vp, i32, i32, i32, vp, vp, vp, sz, st]
+    # (crisp_tokens as untyped pointers: the binding passes places of one array)
     L.crisp_kv_reserve.argtypes = [P(KVCache), vp, vp, vp, vp, vp, P(KVStep), vp, sz, st]
-    L.crisp_kv_append_packed.argtypes = [P(KVCache), P(KVStep), P(Tokens), P(Tokens), vp, sz, st]
-    L.crisp_kv_gather.argtypes = [P(KVCache), vp, i32, vp, P(Tokens), P(Tokens), vp, sz, st]
+    L.crisp_kv_append_packed.argtypes = [P(KVCache), P(KVStep), vp, vp, vp, sz, st]
+    L.crisp_kv_gather.argtypes = [P(KVCache), vp, i32, vp, vp, vp, vp, sz, st]
     L.crisp_packed_workspace_size.argtypes = [P(Packed), P(sz)]
-    L.crisp_packed_prefill.argtypes = [P(Packed), P(Tokens), P(Tokens), P(Tokens), P(Tokens), vp, sz, st]
+    L.crisp_packed_prefill.argtypes = [P(Packed), vp, vp, vp, vp, vp, sz, st]
     L.crisp_read_status.argtypes = [vp, st, P(ctypes.c_int)]
     L.crisp_status_string.argtypes = [ctypes.c_int]
     L.crisp_status_string.restype = ctypes.c_char_p
@@ -426,6 +427,7 @@ def make_kv_cache(k, v, k_scale, v_scale, table, lens) -> KVCache:
     c = KVCache(table.shape[0], hkv, D, B, num, table.shape[1], k.stride(0), k.stride(1), k.data_ptr(), v.data_ptr(),
                 k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr())
     c.tensors, c.device_index, c.token_dtype = keep, k.get_device(), torch.bfloat16
+    c.sizes, c.ref = (table.shape[0], hkv, num, table.data_ptr(), torch.bfloat16, torch.int32), ctypes.byref(c)
     return c
 
 
@@ -537,6 +539,61 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
                                 ws.data_ptr(), _nbytes(ws), st), "crisp_kv_evict")
 
 
+# The calls on packed sequences come once a layer and step, some of them to run for
+# a few microseconds: their checks read each tensor once, and the structures they
+# hand over are kept as references (cache.ref) or built in one array.
+_ELSEWHERE = "the cache, the step or batch, and every tensor of the call must be on the current CUDA device"
+_Tokens2, _Tokens4 = ctypes.c_int64 * 8, ctypes.c_int64 * 16  # two, four crisp_tokens
+_dev = _raw = None
+
+
+def _here(owner, stream):
+    """(current device, handle of the stream to run on); the owner has to be there."""
+    global _dev, _raw
+    want = owner.device_index
+    if want >= 0:
+        if _raw is None:
+            _cuda_state()
+            import torch
+            _dev, _raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        dev = _dev()
+        if dev == want:
+            if stream is None:
+                return dev, _raw(dev)
+            return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return -1, None  # (a tensor's own fault is told first)
+
+
+def _packed_tokens(what, t, rows, heads, dtype, dev):
+    """(address, head stride, token stride) of packed [rows][heads][128] bf16."""
+    if t.dtype is not dtype or t.shape != (rows, heads, D):
+        raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {t.dtype} {tuple(t.shape)}")
+    i, h, e = t.stride()
+    if e != 1:
+        raise ValueError(f"{what}: the 128 features must be contiguous")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(_ELSEWHERE)
+    return t.data_ptr(), h, i
+
+
+def _ints(what, t, n, dtype, dev):
+    """The address of contiguous int32 [n] (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{n}]")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(_ELSEWHERE)
+    return t.data_ptr()
+
+
+def _space(ws, dev):
+    """The address of a workspace."""
+    if dev < 0 or ws.get_device() != dev:
+        raise ValueError(_ELSEWHERE)
+    return ws.data_ptr()
+
+
 def make_kv_step(cache, max_new, max_all=0) -> KVStep:
     """Room for a step's maps (kv_reserve): at most max_new new tokens of the
     cache's batch, and the slots of all its tokens where max_all is not 0 (the
@@ -551,22 +608,14 @@ def make_kv_step(cache, max_new, max_all=0) -> KVStep:
         t = torch.zeros(n, dtype=torch.int32, device=cache.tensors[5].device)
         setattr(s, name, t)
         setattr(s, "_" + name, t.data_ptr() if n else None)
-    s.batch, s.device_index = cache.batch, cache.device_index
+    s.batch, s.room, s.device_index = cache.batch, max_new, cache.device_index
+    s.ref = ctypes.byref(s)
     return s
 
 
-def _step_of(what, step, cache):
-    if step.batch != cache.batch or step.device_index != cache.device_index:
+def _step_of(what, step, sizes, cache):
+    if step.batch != sizes[0] or step.device_index != cache.device_index:
         raise ValueError(f"{what}: the step was made for another batch or device")
-
-
-def _ints(what, t, n, dtype):
-    """The address of contiguous int32 [n] (None: a null pointer)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous int32 [{n}]")
-    return t.data_ptr()
 
 
 def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, stream=None):
@@ -578,36 +627,33 @@ def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, 
     positions, runs, all_slots). If too few pages are free, or the step or a
     sequence has no room, the status word says so and the step takes no tokens.
     ws: kv_append_workspace_size bytes."""
-    _step_of("kv_reserve", step, cache)
-    batch, i32 = cache.batch, cache.tensors[5].dtype
-    free = _ints("kv_reserve: free_pages", free_pages, cache.num_pages, i32)
-    num = _ints("kv_reserve: num_free", num_free, 1, i32)
-    kept = _ints("kv_reserve: keep", keep, batch, i32)
-    new = _ints("kv_reserve: new_lens", new_lens, batch, i32)
-    st = _on_device(cache, stream, free_pages, num_free, ws, keep, new_lens)
-    _check(lib().crisp_kv_reserve(ctypes.byref(cache), cache.table, free, num, kept, new, ctypes.byref(step),
-                                  ws.data_ptr(), ws.nbytes, st), "crisp_kv_reserve")
-
-
-def _packed_tokens(what, t, rows, heads, dtype):
-    """Packed [rows][heads][128] bf16."""
-    if t.dtype is not dtype or t.shape != (rows, heads, D):
-        raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {t.dtype} {tuple(t.shape)}")
-    i, h, e = t.stride()
-    if e != 1:
-        raise ValueError(f"{what}: the 128 features must be contiguous")
-    return Tokens(t.data_ptr(), 0, h, i)
+    sizes = cache.sizes
+    batch, _, pages, table, _, i32 = sizes
+    _step_of("kv_reserve", step, sizes, cache)
+    dev, st = _here(cache, stream)
+    free = _ints("kv_reserve: free_pages", free_pages, pages, i32, dev)
+    num = _ints("kv_reserve: num_free", num_free, 1, i32, dev)
+    kept = _ints("kv_reserve: keep", keep, batch, i32, dev)
+    new = _ints("kv_reserve: new_lens", new_lens, batch, i32, dev)
+    rc = lib().crisp_kv_reserve(cache.ref, table, free, num, kept, new, step.ref, _space(ws, dev), ws.nbytes, st)
+    if rc:
+        _check(rc, "crisp_kv_reserve")
 
 
 def kv_append_packed(cache, step, k_new, v_new, ws, stream=None):
     """Writes a step's new tokens into the cache: bf16 [max_new][hkv][128], token i
     at slots[i] (rows past the step's total are not read)."""
-    _step_of("kv_append_packed", step, cache)
-    kt = _packed_tokens("kv_append_packed: k_new", k_new, step.max_new, cache.hkv, cache.token_dtype)
-    vt = _packed_tokens("kv_append_packed: v_new", v_new, step.max_new, cache.hkv, cache.token_dtype)
-    st = _on_device(cache, stream, k_new, v_new, ws)
-    _check(lib().crisp_kv_append_packed(ctypes.byref(cache), ctypes.byref(step), ctypes.byref(kt), ctypes.byref(vt),
-                                        ws.data_ptr(), ws.nbytes, st), "crisp_kv_append_packed")
+    sizes = cache.sizes
+    _, hkv, _, _, bf16, _ = sizes
+    _step_of("kv_append_packed", step, sizes, cache)
+    dev, st = _here(cache, stream)
+    k, kh, ki = _packed_tokens("kv_append_packed: k_new", k_new, step.room, hkv, bf16, dev)
+    v, vh, vi = _packed_tokens("kv_append_packed: v_new", v_new, step.room, hkv, bf16, dev)
+    both = _Tokens2(k, 0, kh, ki, v, 0, vh, vi)
+    rc = lib().crisp_kv_append_packed(cache.ref, step.ref, ctypes.byref(both), ctypes.byref(both, 32), _space(ws, dev),
+                                      ws.nbytes, st)
+    if rc:
+        _check(rc, "crisp_kv_append_packed")
 
 
 def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
@@ -615,15 +661,18 @@ def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
     slot slots[i] (int32 [n], e.g. a step's all_slots), exactly; count: int32 [1],
     how many of the n rows there are (e.g. step.cu_all[-1:]; None: all). Rows of
     negative slots are left alone."""
+    _, hkv, _, _, bf16, i32 = cache.sizes
+    dev, st = _here(cache, stream)
     n = slots.shape[0] if slots.dim() == 1 else -1
-    i32 = cache.tensors[5].dtype
-    at = _ints("kv_gather: slots", slots, n, i32)
-    num = _ints("kv_gather: count", count, 1, i32)
-    kt = _packed_tokens("kv_gather: k_out", k_out, n, cache.hkv, cache.token_dtype)
-    vt = _packed_tokens("kv_gather: v_out", v_out, n, cache.hkv, cache.token_dtype)
-    st = _on_device(cache, stream, slots, k_out, v_out, ws, count)
-    _check(lib().crisp_kv_gather(ctypes.byref(cache), at, n, num, ctypes.byref(kt), ctypes.byref(vt), ws.data_ptr(),
-                                 ws.nbytes, st), "crisp_kv_gather")
+    at = _ints("kv_gather: slots", slots, n, i32, dev)
+    num = _ints("kv_gather: count", count, 1, i32, dev)
+    k, kh, ki = _packed_tokens("kv_gather: k_out", k_out, n, hkv, bf16, dev)
+    v, vh, vi = _packed_tokens("kv_gather: v_out", v_out, n, hkv, bf16, dev)
+    both = _Tokens2(k, 0, kh, ki, v, 0, vh, vi)
+    rc = lib().crisp_kv_gather(cache.ref, at, n, num, ctypes.byref(both), ctypes.byref(both, 32), _space(ws, dev),
+                               ws.nbytes, st)
+    if rc:
+        _check(rc, "crisp_kv_gather")
 
 
 def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) -> Packed:
@@ -636,12 +685,14 @@ def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) ->
     import torch
     n = cu_q.shape[0] if cu_q.dim() == 1 else 0
     _need(n >= 1, "make_packed: cu_q must be int32 [batch + 1]")
-    q, k = _ints("make_packed: cu_q", cu_q, n, torch.int32), _ints("make_packed: cu_k", cu_k, n, torch.int32)
+    for what, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+        _need(t.dtype is torch.int32 and t.shape == (n,) and t.is_contiguous(),
+              f"make_packed: {what} must be contiguous int32 [{n}]")
     _need(cu_q.device == cu_k.device, "make_packed: the tensors must be on one device")
     _need(max_k is None or max_k >= 0, "make_packed: max_k must not be negative")
-    p = Packed(n - 1, hq, hkv, D, total_q, total_k, max_k or 0, scale, q, k)
+    p = Packed(n - 1, hq, hkv, D, total_q, total_k, max_k or 0, scale, cu_q.data_ptr(), cu_k.data_ptr())
     p.tensors, p.device_index = (cu_q, cu_k), cu_q.get_device()
-    p.sizes = (total_q, total_k, hq, hkv, torch.bfloat16)
+    p.sizes, p.ref = (total_q, total_k, hq, hkv, torch.bfloat16), ctypes.byref(p)
     return p
 
 
@@ -657,14 +708,17 @@ def packed_prefill(packed, q, k, v, out, ws, stream=None):
     token and head strides that are multiples of 8 elements). Query i of a
     sequence of nq queries and nk keys sees its keys j <= nk - nq + i; rows that
     see none become zeros, rows behind the last sequence are left alone."""
-    total_q, total_k, hq, hkv, dtype = packed.sizes
-    qt = _packed_tokens("packed_prefill: q", q, total_q, hq, dtype)
-    kt = _packed_tokens("packed_prefill: k", k, total_k, hkv, dtype)
-    vt = _packed_tokens("packed_prefill: v", v, total_k, hkv, dtype)
-    ot = _packed_tokens("packed_prefill: out", out, total_q, hq, dtype)
-    st = _on_device(packed, stream, q, k, v, out, ws)
-    _check(lib().crisp_packed_prefill(ctypes.byref(packed), ctypes.byref(qt), ctypes.byref(kt), ctypes.byref(vt),
-                                      ctypes.byref(ot), ws.data_ptr(), ws.nbytes, st), "crisp_packed_prefill")
+    total_q, total_k, hq, hkv, bf16 = packed.sizes
+    dev, st = _here(packed, stream)
+    a, ah, ai = _packed_tokens("packed_prefill: q", q, total_q, hq, bf16, dev)
+    b, bh, bi = _packed_tokens("packed_prefill: k", k, total_k, hkv, bf16, dev)
+    c, ch, ci = _packed_tokens("packed_prefill: v", v, total_k, hkv, bf16, dev)
+    d, dh, di = _packed_tokens("packed_prefill: out", out, total_q, hq, bf16, dev)
+    four, ref = _Tokens4(a, 0, ah, ai, b, 0, bh, bi, c, 0, ch, ci, d, 0, dh, di), ctypes.byref
+    rc = lib().crisp_packed_prefill(packed.ref, ref(four), ref(four, 32), ref(four, 64), ref(four, 96), _space(ws, dev),
+                                    ws.nbytes, st)
+    if rc:
+        _check(rc, "crisp_packed_prefill")
 
 
 def wait_selftest(ws, limit_ns, stream=None):
