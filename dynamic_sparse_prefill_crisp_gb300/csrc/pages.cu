@@ -12,17 +12,18 @@ namespace {
 
 // ------------------------------------------------------------------- reserve
 // One CTA, a thread per sequence: what each sequence keeps, gives back and
-// takes, as running sums over the batch, then every page moved and every run of
-// new tokens by whichever thread, which finds its sequence in the sums. Nothing
-// is written before all of it is known to fit. Integers only; the order of pages
-// on the stack depends on the arguments alone. Latency bounds it: three chains
-// of reads and the scans between them.
+// takes, as running sums over the batch, then its pages moved and its runs of new
+// tokens written. Nothing is written before all of it is known to fit. Integers
+// only; the order of pages on the stack depends on the arguments alone. Latency
+// bounds it: three chains of reads, the scans between them, and code that is run
+// once (64 sequences, a token each: 4.6 us).
 //
 // Up to kFewTokens slots are written by the same CTA; more, by a second launch
-// of a thread for every four, which spreads over the GPU.
+// of a thread for every four, which spreads over the GPU (512 requests, a third
+// replaced, 570k slots: 11.8 us together; 13 with every page looked up in the sums).
 constexpr int kPlanThreads = 1024;
 constexpr int kSums = 5;
-constexpr int kHeld = 4;
+constexpr int kOwn = 16;  // 2048 tokens
 constexpr int kFewTokens = 4096;
 constexpr int kMapThreads = 256;
 constexpr int kMapTokens = 4 * kMapThreads;
@@ -60,9 +61,9 @@ __device__ __forceinline__ int slot_of(int id, int pos, int num_pages) {
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_constant__ ReserveArgs a) {
   __shared__ Sums sums;
   __shared__ int keeps[kMaxBatch], warp_sums[kSums][32];
-  __shared__ int problem, bad_page;
+  __shared__ int problem;
   const int b = threadIdx.x, warp = b >> 5, lane = b & 31;
-  if (b == 0) problem = bad_page = 0;
+  if (b == 0) problem = 0;
   grid_dep_launch();
   grid_dep_wait();
   const int cap = a.max_pages * kB;
@@ -112,78 +113,66 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
   const int total_new = sums.cu_new[n], total_all = sums.cu_all[n], freed = sums.freed[n], taken = sums.taken[n],
             runs = sums.runs[n];
   const int top = had_free + freed;
-  // Page k of those given back or taken, counted over the batch: its place in the table.
-  auto place = [&](const int* before, int k) {
-    const int q = holder(before, n, k);
-    return static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + k - before[q];
+  // A thread moves the first kOwn pages of its own sequence; where sequences have
+  // more, those are moved by all threads, which look the sequence up in the sums.
+  int32_t* row = a.table + static_cast<int64_t>(b) * a.max_pages + kept_pages;
+  const int back = own[2], want = own[3], my_runs = own[4];                     // 0 past the batch
+  const int back0 = v[2] - back, want0 = v[3] - want, runs0 = v[4] - my_runs;  // of the sequences before
+  auto others = [&](const int* before, int total, auto&& page) {
+    for (int k = b; k < total; k += kPlanThreads) {
+      const int q = holder(before, n, k), i = k - before[q];
+      if (i >= kOwn) page(k, q, i, a.table + static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + i);
+    }
   };
-  // The pages to give back, the first kHeld of a thread's with their places in registers
-  int64_t at[kHeld];
-  int id[kHeld];
+  int id[kOwn];
   const bool fits = problem == 0 && top <= a.num_pages && total_new <= a.step.max_new &&
                     (a.step.max_all == 0 || total_all <= a.step.max_all);
+  const bool many = __syncthreads_or(back > kOwn || want > kOwn || my_runs > kOwn) != 0;
+  bool no_page = false;  // what is given back has to be a page
   if (fits) {
-    bool none = false;
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) {
-      const int k = b + e * kPlanThreads;
-      at[e] = k < freed ? place(sums.freed, k) : 0;
-    }
+    for (int e = 0; e < kOwn; ++e) id[e] = e < back ? row[e] : 0;
 #pragma unroll
-    for (int e = 0; e < kHeld; ++e) {
-      id[e] = b + e * kPlanThreads < freed ? a.table[at[e]] : 0;
-      none = none || id[e] < 0 || id[e] >= a.num_pages;
-    }
-    for (int k = b + kHeld * kPlanThreads; k < freed; k += kPlanThreads) {
-      const int page = a.table[place(sums.freed, k)];
-      none = none || page < 0 || page >= a.num_pages;
-    }
-    if (none) bad_page = 1;  // what is given back has to be a page
+    for (int e = 0; e < kOwn; ++e) no_page = no_page || id[e] < 0 || id[e] >= a.num_pages;
+    if (many)
+      others(sums.freed, freed, [&](int, int, int, const int32_t* at) { no_page = no_page || *at < 0 || *at >= a.num_pages; });
   }
-  __syncthreads();
-  if (!fits || bad_page != 0 || taken > top) {
-    if (b == 0) report_error(a.status, fits && bad_page == 0 ? CRISP_ERR_PAGES : CRISP_ERR_BOUNDS, 0x901);
+  if (__syncthreads_or(!fits || no_page || taken > top)) {
+    const bool bounds = __syncthreads_or(!fits || no_page) != 0;
+    if (b == 0) report_error(a.status, bounds ? CRISP_ERR_BOUNDS : CRISP_ERR_PAGES, 0x901);
     for (int i = b; i <= n; i += kPlanThreads) a.step.cu_new[i] = a.step.cu_all[i] = 0;
     for (int i = b; i <= a.runs; i += kPlanThreads) a.step.runs[i] = 0;
     return;
   }
   // Pages go back in the order in which taking them again gives each its old place.
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e)
-    if (b + e * kPlanThreads < freed) {
-      a.free_pages[top - 1 - (b + e * kPlanThreads)] = id[e];
-      a.table[at[e]] = -1;
+  for (int e = 0; e < kOwn; ++e)
+    if (e < back) {
+      a.free_pages[top - 1 - back0 - e] = id[e];
+      row[e] = -1;
     }
-  for (int k = b + kHeld * kPlanThreads; k < freed; k += kPlanThreads) {
-    int32_t* entry = a.table + place(sums.freed, k);
-    a.free_pages[top - 1 - k] = *entry;
-    *entry = -1;
-  }
+  if (many)
+    others(sums.freed, freed, [&](int k, int, int, int32_t* at) {
+      a.free_pages[top - 1 - k] = *at;
+      *at = -1;
+    });
   if (b == 0) *a.num_free = top - taken;
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e) {
-    const int k = b + e * kPlanThreads;
-    at[e] = k < taken ? place(sums.taken, k) : 0;
-    id[e] = k < taken ? a.free_pages[top - 1 - k] : 0;
-  }
+  for (int e = 0; e < kOwn; ++e) id[e] = e < want ? a.free_pages[top - 1 - want0 - e] : 0;
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e)
-    if (b + e * kPlanThreads < taken) a.table[at[e]] = id[e];
-  for (int k = b + kHeld * kPlanThreads; k < taken; k += kPlanThreads)
-    a.table[place(sums.taken, k)] = a.free_pages[top - 1 - k];
+  for (int e = 0; e < kOwn; ++e)
+    if (e < want) row[e] = id[e];
+  if (many) others(sums.taken, taken, [&](int k, int, int, int32_t* at) { *at = a.free_pages[top - 1 - k]; });
+  // Page i of those that the new tokens of sequence q touch: its first one.
+  auto run_at = [&](int q, int i) { return max((keeps[q] / kB + i) * kB, keeps[q]) - keeps[q] + sums.cu_new[q]; };
+  for (int e = 0; e < min(my_runs, kOwn); ++e) a.step.runs[runs0 + e] = run_at(b, e);
+  if (many) others(sums.runs, runs, [&](int k, int q, int i, const int32_t*) { a.step.runs[k] = run_at(q, i); });
+  for (int j = runs + b; j <= a.runs; j += kPlanThreads) a.step.runs[j] = total_new;
   for (int i = b; i <= n; i += kPlanThreads) {
     a.step.cu_new[i] = sums.cu_new[i];
     a.step.cu_all[i] = sums.cu_all[i];
     if (i < n) a.lens[i] = sums.cu_all[i + 1] - sums.cu_all[i];
-  }
-  for (int j = b; j <= a.runs; j += kPlanThreads) {
-    int first = total_new;
-    if (j < runs) {
-      const int q = holder(sums.runs, n, j), page = keeps[q] / kB + j - sums.runs[q];
-      first = max(page * kB, keeps[q]) - keeps[q] + sums.cu_new[q];
-    }
-    a.step.runs[j] = first;
   }
   if (a.write_maps == 0) return;
   __syncthreads();  // the table is written
