@@ -677,7 +677,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       const Item& it = sh.item[n % kRing];
       const int mode = it.mode, nsub = it.nsub, sub0 = it.sub0;
       if (mode == kEnd) break;
-      const bool live = r < a.hp * a.tokens && it.t0 + t_row < it.nq && it.hc + h_row < a.group;
+      const bool live = r < a.hp * a.tokens && it.t0 + t_row < it.nq && it.hc + h_row < a.group &&
+                        CRISP_CHECK(it.q0 + it.t0 + t_row < a.total_q && it.g * a.group + it.hc + h_row < a.hq &&
+                                        it.split < a.splits,
+                                    a.status, 0x815);
       const int pos = live ? it.nk - it.nq + it.t0 + t_row : -1;  // the row's last key
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int guarded = guard_of(it);

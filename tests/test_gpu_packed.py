@@ -740,6 +740,59 @@ def test_a_key_of_minus_infinity_is_left_out():
     check(got[64:], want, tol)
 
 
+# ------------------------------------------------------------------ checking build
+def test_the_checking_build_on_valid_batches():
+    # every call between canary regions with both libraries: no status, the same bits
+    from dynamic_sparse_prefill_crisp_gb300 import build as crisp_build
+    from test_gpu_bounds import Guarded
+
+    i32 = torch.int32
+    hq, hkv, room, room_all = 7, 1, 700, 1400
+    rng = np.random.default_rng(91)
+    values = [bf16(rng.standard_normal((room, h, D))).cuda() for h in (hq, hkv, hkv)]
+
+    def run_all(lib):
+        saved, crisp._lib = crisp._lib, lib
+        try:
+            g = Guarded()
+            k8, v8 = g((9, hkv, B, D), torch.uint8), g((9, hkv, B, D), torch.uint8)
+            ks, vs = g((9, hkv), torch.float32), g((9, hkv), torch.float32)
+            table, lens = g((3, 8), i32, 255), g((3,), i32)
+            cache = crisp.make_kv_cache(k8, v8, ks, vs, table, lens)
+            free, num = g((9,), i32), g((1,), i32)
+            free.copy_(torch.arange(9))
+            num.fill_(9)
+            step = crisp.make_kv_step(cache, room, room_all)
+            for name in ("cu_new", "cu_all", "slots", "positions", "runs", "all_slots"):
+                t = g(getattr(step, name).shape, i32)
+                setattr(step, name, t)
+                setattr(step, "_" + name, t.data_ptr())
+            q, k, v = (g(t.shape, torch.bfloat16) for t in values)
+            for a, b in zip((q, k, v), values):
+                a.copy_(b)
+            out, ka, va = g((room, hq, D), torch.bfloat16), g((room_all, hkv, D), torch.bfloat16), g((room_all, hkv, D), torch.bfloat16)
+            p = crisp.make_packed(hq, hkv, step.cu_new, step.cu_all, room, room_all)
+            ws = g((crisp.packed_workspace_size(p),), torch.uint8)
+            crisp.workspace_init(ws)
+            got = []
+            for keep, new in (([0, 0, 0], [300, 17, 200]), ([300, 0, 190], [60, 333, 1])):
+                crisp.kv_reserve(cache, free, num, step, ws, keep=dev32(keep), new_lens=dev32(new))
+                crisp.kv_append_packed(cache, step, k, v, ws)
+                crisp.kv_gather(cache, step.all_slots, ka, va, ws, count=step.cu_all[-1:])
+                crisp.packed_prefill(p, q, ka, va, out, ws)
+                got += [t.clone() for t in (out, ka, va, k8, v8, ks, vs, table, lens, free, num, step.slots, step.runs,
+                                            step.all_slots, step.positions)]
+            assert crisp.read_status(ws) == OK and g.intact()
+            return got
+        finally:
+            crisp._lib = saved
+
+    release = run_all(crisp.lib())
+    checking = run_all(crisp.load_library(crisp_build.build(debug=True)))
+    for a, b in zip(release, checking):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 # --------------------------------------------------------------------- as documented
 def test_the_readme_example_of_a_batch():
     blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(ROOT, "README.md")).read(), re.S)
