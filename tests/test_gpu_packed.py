@@ -466,6 +466,35 @@ def test_append_packed_is_append():
         assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
 
 
+@pytest.mark.parametrize("width,shift", [(D + 24, 8), (D + 24, 16), (D + 16, 16), (D + 16, 8), (D + 8, 0)])
+def test_append_at_16_byte_addresses(width, shift):
+    # rows and heads whose strides or first values are odd multiples of 16 bytes: the same pools as from dense
+    # rows, in the packed form and the padded one
+    lens, hkv, room = [200, 3, 129], 3, 340
+    rng = np.random.default_rng(width + shift)
+    k, v = (bf16(rng.standard_normal((room, hkv, D)) * 9).cuda() for _ in range(2))
+    parts = []
+    for t in (k, v):
+        wide = torch.full((room, hkv, width), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[..., shift:shift + D] = t
+        parts.append(wide[..., shift:shift + D])
+    pools = []
+    for pair in ((k, v), parts):
+        x = Batch(3, 4, 9, room, 0, hkv=hkv, seed=4)
+        x.reserve(None, lens)
+        crisp.kv_append_packed(x.cache, x.step, *pair, x.ws)
+        assert crisp.read_status(x.ws) == OK
+        pools.append(x.pools.host())
+        y = Pools(9, hkv)
+        for b, at, n in ((0, 0, 200), (2, 200, 140)):  # a sequence at a time, [1][hkv][n][128]
+            one = [t[at:at + n].transpose(0, 1)[None] for t in pair]
+            crisp.kv_append(y.cache([x.ref.table[b]], [n]), *one, x.ws)
+        assert crisp.read_status(x.ws) == OK
+        pools.append(y.host())
+    for a, b in zip(pools[0] + pools[1], pools[2] + pools[3]):
+        assert np.array_equal(a, b, equal_nan=a.dtype.kind == "f")
+
+
 def test_append_packed_refuses_bad_runs():
     x = Batch(2, 4, 8, 300, 0, hkv=1, seed=3)
     x.reserve(None, [200, 50])
