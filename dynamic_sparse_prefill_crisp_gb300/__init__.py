@@ -707,7 +707,8 @@ def packed_prefill(packed, q, k, v, out, ws, stream=None):
     [total_q][hq][128], k, v bf16 [total_k][hkv][128], features contiguous (any
     token and head strides that are multiples of 8 elements). Query i of a
     sequence of nq queries and nk keys sees its keys j <= nk - nq + i; rows that
-    see none become zeros, rows behind the last sequence are left alone."""
+    see none become zeros, rows behind the last sequence are left alone. out shares
+    no element with the inputs."""
     total_q, total_k, hq, hkv, bf16 = packed.sizes
     dev, st = _here(packed, stream)
     a, ah, ai = _packed_tokens("packed_prefill: q", q, total_q, hq, bf16, dev)

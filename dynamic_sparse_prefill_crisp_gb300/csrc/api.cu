@@ -1204,6 +1204,8 @@ crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens
     if (keys && (st = check_tokens(v, 1, p.hkv, p.total_k)) != CRISP_OK) return st;
     const PackedPlan plan = packed_plan(p);
     if ((st = check_cache_ws(ws, ws_bytes, packed_layout(p, plan).total)) != CRISP_OK) return st;
+    if (out->data == q->data || (keys && (out->data == k->data || out->data == v->data)))
+      return CRISP_ERR_INVALID_ARG;  // a tile may be read again after it was written
     if ((st = check_device()) != CRISP_OK) return st;
     TmaMaps maps;
     if ((st = make_packed_q_map(&maps.q, p, plan, *q)) != CRISP_OK) return st;

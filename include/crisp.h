@@ -26,6 +26,10 @@
  *   crisp_kv_append             new K and V tokens into a paged 8-bit cache
  *   crisp_decode_attention      attention of 1..16 new tokens per sequence over that cache
  *   crisp_kv_evict              keeps a cache's sink, recent and heaviest tokens
+ *   crisp_kv_reserve            a batch's pages, slots and positions from its requests' lengths
+ *   crisp_kv_append_packed      crisp_kv_append for a batch's tokens in one packed array
+ *   crisp_kv_gather             cached tokens back as packed bf16 rows
+ *   crisp_packed_prefill        dense causal attention over packed sequences
  *   crisp_wait_selftest         failure detection: a bounded wait that must time out
  *
  * Conventions (every function):
@@ -40,10 +44,10 @@
  *    out) are recorded in the workspace status word; read it with
  *    crisp_read_status. No C++ exception crosses this boundary.
  *  - Fixed sizes: head_dim = 128, block = 128 tokens, batch 1 (a batch is a
- *    loop over calls; the cache calls take one). seq_len = n <= 2^20, any n:
- *    blocks are aligned at token 0, nb = ceil(n/128), and when 128 does not
- *    divide n the last block is short (n - 128*(nb-1) tokens). The method's
- *    steps (A1..A7) need
+ *    loop over calls; the cache and the packed calls take one). seq_len = n
+ *    <= 2^20, any n: blocks are aligned at token 0, nb = ceil(n/128), and when
+ *    128 does not divide n the last block is short (n - 128*(nb-1) tokens).
+ *    The method's steps (A1..A7) need
  *    n >= 256 (the sink block and at least one more); attention, the whole
  *    layer and the workspace sizes take any n >= 0, and n = 0 (an empty
  *    input) launches nothing and returns CRISP_OK.
@@ -602,9 +606,9 @@ typedef struct crisp_kv_step {
  *
  * Where the step cannot be, the status word says so, cu_new, cu_all and runs become
  * zeros (the calls that follow do nothing), and nothing else changes:
- * CRISP_ERR_PAGES if too few pages are free; CRISP_ERR_BOUNDS for a length, keep
- * or new_lens outside [0, 128 * max_pages], more than 128 * max_pages tokens in a
- * sequence, max_new or (where it is not 0) max_all exceeded, num_free outside [0,
+ * CRISP_ERR_PAGES if too few pages are free; CRISP_ERR_BOUNDS for a length or
+ * new_lens outside [0, 128 * max_pages], a negative keep, more than 128 * max_pages
+ * tokens in a sequence, max_new or (where it is not 0) max_all exceeded, num_free outside [0,
  * num_pages], or a page to be given back that is none. A page id on the stack or
  * in the table that is none gives slots of -1. Workspace: as for crisp_kv_append.
  * keep, new_lens: int32 [batch], neither of them cache->lens. */
@@ -653,7 +657,8 @@ CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, s
  * not), and
  *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j,    zeros where no key is seen,
  * kv head h / (hq / hkv). q bf16 [hq][total_q][128], k, v [hkv][total_k][128], out
- * as q. What a row does not see does not reach it, infinities and NaN in v
+ * as q, and none of the inputs (equal pointers are CRISP_ERR_INVALID_ARG; no element
+ * may be shared). What a row does not see does not reach it, infinities and NaN in v
  * included. A sequence whose running sums descend, leave [0, total_q] or [0,
  * total_k], or are more than 2^20 rows apart is CRISP_ERR_BOUNDS and counts as
  * empty: its rows are left as they were. Precision: products of bf16 in fp32, p

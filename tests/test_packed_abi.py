@@ -138,6 +138,10 @@ def test_packed_prefill_refusals(L):
         assert prefill(L, **{name: tokens(t=64)}) == SHAPE
     assert prefill(L, nbytes=n.value - 1) == WORKSPACE and prefill(L, ws=None) == WORKSPACE
     assert prefill(L, ws=128) == ALIGN
+    # out is none of the inputs
+    for name in ("q", "k", "v"):
+        others = {x: tokens(data=512 * i) for i, x in enumerate(("q", "k", "v"), 1)}
+        assert prefill(L, **others, out=tokens(data=others[name].data)) == INVALID
     # no queries: nothing is looked at; no keys: k and v are not
     assert prefill(L, packed(total_q=0, cu_q=None), q=tokens(data=None), ws=None) == OK
     assert prefill(L, packed(batch=0, cu_k=None), q=tokens(data=None), ws=None) == OK
