@@ -299,7 +299,8 @@ class Batch:
 
 
 @pytest.mark.parametrize("batch,max_pages,num_pages,most,seed", [
-    (1, 9, 9, 900, 0), (5, 12, 40, 500, 1), (33, 8, 150, 700, 2), (64, 3, 192, 300, 3), (1024, 2, 1500, 150, 4)])
+    (1, 9, 9, 900, 0), (5, 12, 40, 500, 1), (33, 8, 150, 700, 2), (64, 3, 192, 300, 3), (1024, 2, 1500, 150, 4),
+    (6, 70, 260, 4000, 5), (3, 40, 100, 5120, 6)])
 def test_reserve_follows_the_lists(batch, max_pages, num_pages, most, seed):
     rng = np.random.default_rng(100 + seed)
     x = Batch(batch, max_pages, num_pages, max_new=batch * most, max_all=batch * max_pages * B, seed=seed)
