@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcrisp.so")
@@ -149,12 +150,12 @@ def load_library(path):
     L.crisp_decode_attention.argtypes = [P(KVCache), i32, i32, ctypes.c_float, P(Tokens), P(Tokens), vp, vp, vp, sz,
                                          st]
     L.crisp_kv_evict.argtypes = [P(KVCache), P(KVCache), vp, i32, i32, i32, vp, vp, vp, sz, st]
-    # (crisp_tokens as untyped pointers: the binding passes places of one array)
-    L.crisp_kv_reserve.argtypes = [P(KVCache), vp, vp, vp, vp, vp, P(KVStep), vp, sz, st]
-    L.crisp_kv_append_packed.argtypes = [P(KVCache), P(KVStep), vp, vp, vp, sz, st]
-    L.crisp_kv_gather.argtypes = [P(KVCache), vp, i32, vp, vp, vp, vp, sz, st]
+    # (structures as untyped pointers: addresses, and crisp_tokens as packed bytes)
+    L.crisp_kv_reserve.argtypes = [vp] * 8 + [sz, st]
+    L.crisp_kv_append_packed.argtypes = [vp, vp, vp, vp, vp, sz, st]
+    L.crisp_kv_gather.argtypes = [vp, vp, i32, vp, vp, vp, vp, sz, st]
     L.crisp_packed_workspace_size.argtypes = [P(Packed), P(sz)]
-    L.crisp_packed_prefill.argtypes = [P(Packed), vp, vp, vp, vp, vp, sz, st]
+    L.crisp_packed_prefill.argtypes = [vp, vp, vp, vp, vp, vp, sz, st]
     L.crisp_read_status.argtypes = [vp, st, P(ctypes.c_int)]
     L.crisp_status_string.argtypes = [ctypes.c_int]
     L.crisp_status_string.restype = ctypes.c_char_p
@@ -427,7 +428,7 @@ def make_kv_cache(k, v, k_scale, v_scale, table, lens) -> KVCache:
     c = KVCache(table.shape[0], hkv, D, B, num, table.shape[1], k.stride(0), k.stride(1), k.data_ptr(), v.data_ptr(),
                 k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(), lens.data_ptr())
     c.tensors, c.device_index, c.token_dtype = keep, k.get_device(), torch.bfloat16
-    c.sizes, c.ref = (table.shape[0], hkv, num, table.data_ptr(), torch.bfloat16, torch.int32), ctypes.byref(c)
+    c.sizes = table.shape[0], hkv, num, table.data_ptr(), torch.bfloat16, torch.int32
     return c
 
 
@@ -540,10 +541,10 @@ def kv_evict(cache, new_cache, weights, ws, keep, sink=0, recent=0, new_weights=
 
 
 # The calls on packed sequences come once a layer and step, some of them to run for
-# a few microseconds: their checks read each tensor once, and the structures they
-# hand over are kept as references (cache.ref) or built in one array.
+# a few microseconds: their checks read each tensor once, and crisp_tokens is packed
+# (a quarter of the time of a ctypes structure).
 _ELSEWHERE = "the cache, the step or batch, and every tensor of the call must be on the current CUDA device"
-_Tokens2, _Tokens4 = ctypes.c_int64 * 8, ctypes.c_int64 * 16  # two, four crisp_tokens
+_pack, _at = struct.Struct("=4q").pack, ctypes.addressof
 _dev = _raw = None
 
 
@@ -565,7 +566,7 @@ def _here(owner, stream):
 
 
 def _packed_tokens(what, t, rows, heads, dtype, dev):
-    """(address, head stride, token stride) of packed [rows][heads][128] bf16."""
+    """The crisp_tokens of packed [rows][heads][128] bf16."""
     if t.dtype is not dtype or t.shape != (rows, heads, D):
         raise ValueError(f"{what} must be bf16 [tokens][heads][128] = {(rows, heads, D)}: {t.dtype} {tuple(t.shape)}")
     i, h, e = t.stride()
@@ -573,7 +574,7 @@ def _packed_tokens(what, t, rows, heads, dtype, dev):
         raise ValueError(f"{what}: the 128 features must be contiguous")
     if dev < 0 or t.get_device() != dev:
         raise ValueError(_ELSEWHERE)
-    return t.data_ptr(), h, i
+    return _pack(t.data_ptr(), 0, h, i)
 
 
 def _ints(what, t, n, dtype, dev):
@@ -609,7 +610,6 @@ def make_kv_step(cache, max_new, max_all=0) -> KVStep:
         setattr(s, name, t)
         setattr(s, "_" + name, t.data_ptr() if n else None)
     s.batch, s.room, s.device_index = cache.batch, max_new, cache.device_index
-    s.ref = ctypes.byref(s)
     return s
 
 
@@ -635,7 +635,7 @@ def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, 
     num = _ints("kv_reserve: num_free", num_free, 1, i32, dev)
     kept = _ints("kv_reserve: keep", keep, batch, i32, dev)
     new = _ints("kv_reserve: new_lens", new_lens, batch, i32, dev)
-    rc = lib().crisp_kv_reserve(cache.ref, table, free, num, kept, new, step.ref, _space(ws, dev), ws.nbytes, st)
+    rc = lib().crisp_kv_reserve(_at(cache), table, free, num, kept, new, _at(step), _space(ws, dev), ws.nbytes, st)
     if rc:
         _check(rc, "crisp_kv_reserve")
 
@@ -647,11 +647,9 @@ def kv_append_packed(cache, step, k_new, v_new, ws, stream=None):
     _, hkv, _, _, bf16, _ = sizes
     _step_of("kv_append_packed", step, sizes, cache)
     dev, st = _here(cache, stream)
-    k, kh, ki = _packed_tokens("kv_append_packed: k_new", k_new, step.room, hkv, bf16, dev)
-    v, vh, vi = _packed_tokens("kv_append_packed: v_new", v_new, step.room, hkv, bf16, dev)
-    both = _Tokens2(k, 0, kh, ki, v, 0, vh, vi)
-    rc = lib().crisp_kv_append_packed(cache.ref, step.ref, ctypes.byref(both), ctypes.byref(both, 32), _space(ws, dev),
-                                      ws.nbytes, st)
+    k = _packed_tokens("kv_append_packed: k_new", k_new, step.room, hkv, bf16, dev)
+    v = _packed_tokens("kv_append_packed: v_new", v_new, step.room, hkv, bf16, dev)
+    rc = lib().crisp_kv_append_packed(_at(cache), _at(step), k, v, _space(ws, dev), ws.nbytes, st)
     if rc:
         _check(rc, "crisp_kv_append_packed")
 
@@ -666,11 +664,9 @@ def kv_gather(cache, slots, k_out, v_out, ws, count=None, stream=None):
     n = slots.shape[0] if slots.dim() == 1 else -1
     at = _ints("kv_gather: slots", slots, n, i32, dev)
     num = _ints("kv_gather: count", count, 1, i32, dev)
-    k, kh, ki = _packed_tokens("kv_gather: k_out", k_out, n, hkv, bf16, dev)
-    v, vh, vi = _packed_tokens("kv_gather: v_out", v_out, n, hkv, bf16, dev)
-    both = _Tokens2(k, 0, kh, ki, v, 0, vh, vi)
-    rc = lib().crisp_kv_gather(cache.ref, at, n, num, ctypes.byref(both), ctypes.byref(both, 32), _space(ws, dev),
-                               ws.nbytes, st)
+    k = _packed_tokens("kv_gather: k_out", k_out, n, hkv, bf16, dev)
+    v = _packed_tokens("kv_gather: v_out", v_out, n, hkv, bf16, dev)
+    rc = lib().crisp_kv_gather(_at(cache), at, n, num, k, v, _space(ws, dev), ws.nbytes, st)
     if rc:
         _check(rc, "crisp_kv_gather")
 
@@ -692,7 +688,7 @@ def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) ->
     _need(max_k is None or max_k >= 0, "make_packed: max_k must not be negative")
     p = Packed(n - 1, hq, hkv, D, total_q, total_k, max_k or 0, scale, cu_q.data_ptr(), cu_k.data_ptr())
     p.tensors, p.device_index = (cu_q, cu_k), cu_q.get_device()
-    p.sizes, p.ref = (total_q, total_k, hq, hkv, torch.bfloat16), ctypes.byref(p)
+    p.sizes = total_q, total_k, hq, hkv, torch.bfloat16
     return p
 
 
@@ -711,13 +707,11 @@ def packed_prefill(packed, q, k, v, out, ws, stream=None):
     no element with the inputs."""
     total_q, total_k, hq, hkv, bf16 = packed.sizes
     dev, st = _here(packed, stream)
-    a, ah, ai = _packed_tokens("packed_prefill: q", q, total_q, hq, bf16, dev)
-    b, bh, bi = _packed_tokens("packed_prefill: k", k, total_k, hkv, bf16, dev)
-    c, ch, ci = _packed_tokens("packed_prefill: v", v, total_k, hkv, bf16, dev)
-    d, dh, di = _packed_tokens("packed_prefill: out", out, total_q, hq, bf16, dev)
-    four, ref = _Tokens4(a, 0, ah, ai, b, 0, bh, bi, c, 0, ch, ci, d, 0, dh, di), ctypes.byref
-    rc = lib().crisp_packed_prefill(packed.ref, ref(four), ref(four, 32), ref(four, 64), ref(four, 96), _space(ws, dev),
-                                    ws.nbytes, st)
+    a = _packed_tokens("packed_prefill: q", q, total_q, hq, bf16, dev)
+    b = _packed_tokens("packed_prefill: k", k, total_k, hkv, bf16, dev)
+    c = _packed_tokens("packed_prefill: v", v, total_k, hkv, bf16, dev)
+    d = _packed_tokens("packed_prefill: out", out, total_q, hq, bf16, dev)
+    rc = lib().crisp_packed_prefill(_at(packed), a, b, c, d, _space(ws, dev), ws.nbytes, st)
     if rc:
         _check(rc, "crisp_packed_prefill")
 
