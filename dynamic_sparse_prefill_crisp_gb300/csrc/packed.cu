@@ -369,9 +369,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   grid_dep_wait();
   order_sequences(a, reinterpret_cast<int*>(sK), order, ranks);
+  Item ahead;
+  bool found = false;  // ahead is the next item
+  // (side by side, and with no waits behind an item that is through: 7.9 us for a
+  // prompt of 300 tokens, 8.5 without)
   if (warp == kMmaWarp) {
     tmem_alloc(&sh.tmem_base, kTmemCols);
     tmem_relinquish();
+  } else if (warp == kTmaWarp) {
+    found = find_item(a, blockIdx, order, ranks, ahead);
   }
   fence_async_shared();  // the K slots' use above comes before the copies into them
   tc_fence_before();
@@ -390,8 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool leader = elect_lane(from);
     SlotPhases kn, vn;  // loads issued per slot
     uint32_t loads = 0u, asks = 0u;
-    bool asked = false, have = true, go = true;
-    uint3 block = blockIdx;
+    bool asked = false, go = true;
     bool more = true;  // no answer was no yet
     auto send = [&]() {
       mbar_arrive_expect_tx(&sh.next, 16);
@@ -403,24 +408,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       asked = true;
     };
     // The next item, passing over blocks that have none.
-    Item ahead;
-    bool found = false;  // ahead is one
     auto look_ahead = [&]() {
-      while (go && !found && (have || asked)) {
-        if (!have) {
-          go = await_warp(&sh.next, (asks - 1u) & 1u, &sh.abort);
-          asked = false;
-          if (!go) return;
-          have = more = taken_block(&sh.answer, block);
-          fence_async_shared();  // read before the next answer is written
-          __syncwarp();
-          if (!have) return;
-        }
-        have = false;
+      while (go && !found && asked) {
+        go = await_warp(&sh.next, (asks - 1u) & 1u, &sh.abort);
+        asked = false;
+        if (!go) return;
+        uint3 block;
+        more = taken_block(&sh.answer, block);
+        fence_async_shared();  // read before the next answer is written
+        __syncwarp();
+        if (!more) return;
         found = find_item(a, block, order, ranks, ahead);
         if (!found) ask();
       }
     };
+    if (!found) ask();
     int retired = 0;  // items known to be through
     int again = 0;    // items that come back
     bool fixed_next = false;
@@ -526,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
     }
-    if (leader) {
-      if (!go) give_up(&sh.abort, a.status, 0x82b);
-      // Everything asked for has landed before the CTA ends (after a timeout the
-      // consumers may not have waited). Bounded waits that ignore the abort flag.
+    if (leader && !go) {
+      give_up(&sh.abort, a.status, 0x82b);
+      // Everything asked for has landed before the CTA ends (where no wait ran out, all
+      // items are through). Bounded waits that ignore the abort flag.
       const int never = 0;
       if (asked) await(&sh.next, (asks - 1u) & 1u, &never);
       if (loads > 0u) await(&sh.q_full, (loads - 1u) & 1u, &never);
@@ -638,9 +640,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (leader) mbar_arrive(&sh.item_empty[n % kRing]);
     }
-    if (leader) {
-      if (!go) give_up(&sh.abort, a.status, 0x824);
-      // Every product has completed before TMEM is released (a bounded wait that ignores the abort flag).
+    if (leader && !go) {
+      give_up(&sh.abort, a.status, 0x824);
+      // Every product has completed before TMEM is released (where no wait ran out, all
+      // items are through). A bounded wait that ignores the abort flag.
       umma_commit(&sh.drain);
       const int never = 0;
       if (!await(&sh.drain, 0u, &never)) give_up(&sh.abort, a.status, 0x826);
