@@ -16,12 +16,12 @@
 // Two CTAs stay on each SM and take over blocks that have not started, one
 // ahead: the next tile's Q and first K and V are on their way while this one's
 // softmax and epilogue run. Short prompts need that (256 of up to 300 tokens,
-// 28/4 heads: 127 us, 5.0 TB/s; a CTA per tile, whose start, loads and end came
+// 28/4 heads: 128 us, 5.0 TB/s; a CTA per tile, whose start, loads and end came
 // one after the other, 340 us).
 //
 // Long prompts are bound by the tensor pipe at the rate of its 64-key products (a
 // product's operands come from shared memory at 128 bytes a cycle, 48 cycles where
-// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.24 ms, 1778
+// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.22 ms, 1807
 // TFLOP/s, a sub-block 1225 cycles a CTA and 612 an SM.
 //
 // The products are csrc/attention.cu's: 64-key sub-blocks, two score buffers in
