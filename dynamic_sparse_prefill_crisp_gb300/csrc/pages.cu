@@ -16,14 +16,16 @@ namespace {
 // tokens written. Nothing is written before all of it is known to fit. Integers
 // only; the order of pages on the stack depends on the arguments alone. Latency
 // bounds it: three chains of reads, the scans between them, and code that is run
-// once (64 sequences, a token each: 4.6 us).
+// once and fetched as it is run (64 sequences, a token each: 3.8 us; 4.7 with a
+// thread's 16 pages in line instead of twice 8).
 //
 // Up to kFewTokens slots are written by the same CTA; more, by a second launch
 // of a thread for every four, which spreads over the GPU (512 requests, a third
-// replaced, 570k slots: 11.8 us together; 13 with every page looked up in the sums).
+// replaced, 570k slots: 11.2 us together; 13 with every page looked up in the sums).
 constexpr int kPlanThreads = 1024;
 constexpr int kSums = 5;
-constexpr int kOwn = 16;  // 2048 tokens
+constexpr int kOwn = 16;    // pages of its sequence that a thread moves itself,
+constexpr int kAtOnce = 8;  // so many at a time
 constexpr int kFewTokens = 4096;
 constexpr int kMapThreads = 256;
 constexpr int kMapTokens = 4 * kMapThreads;
@@ -124,16 +126,19 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
       if (i >= kOwn) page(k, q, i, a.table + static_cast<int64_t>(q) * a.max_pages + (keeps[q] + kB - 1) / kB + i);
     }
   };
-  int id[kOwn];
   const bool fits = problem == 0 && top <= a.num_pages && total_new <= a.step.max_new &&
                     (a.step.max_all == 0 || total_all <= a.step.max_all);
   const bool many = __syncthreads_or(back > kOwn || want > kOwn || my_runs > kOwn) != 0;
   bool no_page = false;  // what is given back has to be a page
   if (fits) {
+#pragma unroll 1
+    for (int e0 = 0; e0 < min(back, kOwn); e0 += kAtOnce) {
+      int id[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kOwn; ++e) id[e] = e < back ? row[e] : 0;
+      for (int e = 0; e < kAtOnce; ++e) id[e] = e0 + e < back ? row[e0 + e] : 0;
 #pragma unroll
-    for (int e = 0; e < kOwn; ++e) no_page = no_page || id[e] < 0 || id[e] >= a.num_pages;
+      for (int e = 0; e < kAtOnce; ++e) no_page = no_page || id[e] < 0 || id[e] >= a.num_pages;
+    }
     if (many)
       others(sums.freed, freed, [&](int, int, int, const int32_t* at) { no_page = no_page || *at < 0 || *at >= a.num_pages; });
   }
@@ -145,12 +150,18 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
     return;
   }
   // Pages go back in the order in which taking them again gives each its old place.
+#pragma unroll 1
+  for (int e0 = 0; e0 < min(back, kOwn); e0 += kAtOnce) {
+    int id[kAtOnce];
 #pragma unroll
-  for (int e = 0; e < kOwn; ++e)
-    if (e < back) {
-      a.free_pages[top - 1 - back0 - e] = id[e];
-      row[e] = -1;
-    }
+    for (int e = 0; e < kAtOnce; ++e) id[e] = e0 + e < back ? row[e0 + e] : 0;
+#pragma unroll
+    for (int e = 0; e < kAtOnce; ++e)
+      if (e0 + e < back) {
+        a.free_pages[top - 1 - back0 - e0 - e] = id[e];
+        row[e0 + e] = -1;
+      }
+  }
   if (many)
     others(sums.freed, freed, [&](int k, int, int, int32_t* at) {
       a.free_pages[top - 1 - k] = *at;
@@ -158,11 +169,15 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
     });
   if (b == 0) *a.num_free = top - taken;
   __syncthreads();
+#pragma unroll 1
+  for (int e0 = 0; e0 < min(want, kOwn); e0 += kAtOnce) {
+    int id[kAtOnce];
 #pragma unroll
-  for (int e = 0; e < kOwn; ++e) id[e] = e < want ? a.free_pages[top - 1 - want0 - e] : 0;
+    for (int e = 0; e < kAtOnce; ++e) id[e] = e0 + e < want ? a.free_pages[top - 1 - want0 - e0 - e] : 0;
 #pragma unroll
-  for (int e = 0; e < kOwn; ++e)
-    if (e < want) row[e] = id[e];
+    for (int e = 0; e < kAtOnce; ++e)
+      if (e0 + e < want) row[e0 + e] = id[e];
+  }
   if (many) others(sums.taken, taken, [&](int k, int, int, int32_t* at) { *at = a.free_pages[top - 1 - k]; });
   // Page i of those that the new tokens of sequence q touch: its first one.
   auto run_at = [&](int q, int i) { return max((keeps[q] / kB + i) * kB, keeps[q]) - keeps[q] + sums.cu_new[q]; };
