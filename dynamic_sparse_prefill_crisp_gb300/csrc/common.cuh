@@ -127,7 +127,7 @@ struct KvMaps {
 };
 
 // Attention over packed sequences.
-constexpr int kPackedCtas = 304;      // 152 SMs x 2: from that many tiles on none is split
+constexpr int kPackedCtas = 304;      // 152 SMs x 2
 constexpr int kMaxPacked = 1 << 24;   // rows of a packed tensor
 
 inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }

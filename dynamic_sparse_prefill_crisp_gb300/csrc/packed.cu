@@ -827,17 +827,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // The rows of split tiles: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
-// with M the largest reference m_s, in the order of the splits. A warp per row.
+// with M the largest reference m_s, in the order of the splits. A warp takes kJoinRows
+// rows of a token, kJoinAhead parts of each in flight: one row, or two where a warp a
+// row would be more than the GPU holds at once (32k rows of whole prompts in halves: 8
+// us, 11 with one).
 constexpr int kJoinWarps = 4;
-constexpr int kJoinAhead = 4;
+template <int kJoinRows, int kJoinAhead>
 __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __grid_constant__ PackedArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.total_q) * a.hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int groups = div_up(a.hq, kJoinRows);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   grid_dep_launch();
   grid_dep_wait();
-  if (row >= rows) return;
-  const int tok = static_cast<int>(row / a.hq), head = static_cast<int>(row % a.hq);
+  const int tok = static_cast<int>(unit / groups), head0 = static_cast<int>(unit % groups) * kJoinRows;
+  if (tok >= a.total_q) return;
   // the last sequence that starts at or before the token
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
@@ -852,47 +856,70 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
   const int cost = tile_cost(n.x, n.y, t / a.tokens * a.tokens, a.tokens);
   const int ns = min(a.splits, div_up(cost, a.split_subs));
   if (ns <= 1) return;  // written by the tile's only CTA
-  float top = -INFINITY;
-  for (int s = lane; s < ns; s += 32) {
-    const float2 ml = a.part_ml[s * rows + row];
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  const int64_t row0 = static_cast<int64_t>(tok) * a.hq + head0;
+  const int live = min(kJoinRows, a.hq - head0);
+  float top[kJoinRows], l[kJoinRows];
+  float4 acc[kJoinRows];
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) {
+    top[r] = -INFINITY;
+    l[r] = 0.f;
+    acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  top = warp_max(top);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  for (int s = lane; s < ns; s += 32)
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r)
+      if (r < live) {
+        const float2 ml = a.part_ml[s * rows + row0 + r];
+        if (ml.y != 0.f) top[r] = fmaxf(top[r], ml.x);
+      }
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) top[r] = warp_max(top[r]);
   for (int s0 = 0; s0 < ns; s0 += 32) {
-    // each lane a part's weight, then all lanes part after part, four rows in flight
-    float w = 0.f;
-    if (s0 + lane < ns) {
-      const float2 ml = a.part_ml[(s0 + lane) * rows + row];
-      w = ml.y != 0.f ? ex2_approx(ml.x - top) : 0.f;
-      l += w != 0.f ? ml.y * w : 0.f;
+    // each lane a part's weights, then all lanes part after part
+    float w[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+      w[r] = 0.f;
+      if (s0 + lane < ns && r < live) {
+        const float2 ml = a.part_ml[(s0 + lane) * rows + row0 + r];
+        w[r] = ml.y != 0.f ? ex2_approx(ml.x - top[r]) : 0.f;
+        l[r] += w[r] != 0.f ? ml.y * w[r] : 0.f;
+      }
     }
-    const float* part = a.part + (s0 * rows + row) * kD + lane * 4;
+    const float* part = a.part + (s0 * rows + row0) * kD + lane * 4;
     const int parts = min(32, ns - s0);
 #pragma unroll 1
     for (int s = 0; s < parts; s += kJoinAhead) {
-      float4 o[kJoinAhead];
+      float4 o[kJoinAhead][kJoinRows];
 #pragma unroll
       for (int e = 0; e < kJoinAhead; ++e)
-        if (s + e < parts) o[e] = *reinterpret_cast<const float4*>(part + (s + e) * rows * kD);
 #pragma unroll
-      for (int e = 0; e < kJoinAhead; ++e) {
-        const float ws = __shfl_sync(0xffffffffu, w, (s + e) & 31);
-        if (s + e < parts && ws != 0.f) {
-          acc.x = fmaf(o[e].x, ws, acc.x);
-          acc.y = fmaf(o[e].y, ws, acc.y);
-          acc.z = fmaf(o[e].z, ws, acc.z);
-          acc.w = fmaf(o[e].w, ws, acc.w);
+        for (int r = 0; r < kJoinRows; ++r)
+          if (s + e < parts && r < live) o[e][r] = *reinterpret_cast<const float4*>(part + ((s + e) * rows + r) * kD);
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e)
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+          const float ws = __shfl_sync(0xffffffffu, w[r], (s + e) & 31);
+          if (s + e < parts && r < live && ws != 0.f) {
+            acc[r].x = fmaf(o[e][r].x, ws, acc[r].x);
+            acc[r].y = fmaf(o[e][r].y, ws, acc[r].y);
+            acc[r].z = fmaf(o[e][r].z, ws, acc[r].z);
+            acc[r].w = fmaf(o[e][r].w, ws, acc[r].w);
+          }
         }
-      }
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(a.out + head * a.o_hs + tok * a.o_ts + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  for (int r = 0; r < kJoinRows; ++r) {
+    if (r >= live) break;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+    const float inv = l[r] != 0.f ? 1.f / l[r] : 0.f;
+    *reinterpret_cast<uint2*>(a.out + (head0 + r) * a.o_hs + tok * a.o_ts + lane * 4) =
+        make_uint2(pack_bf16x2(acc[r].x * inv, acc[r].y * inv), pack_bf16x2(acc[r].z * inv, acc[r].w * inv));
+  }
 }
 
 // Heads of a tile: all of a group where they fill 128 rows well, else the
@@ -913,14 +940,16 @@ int tile_heads(int group) {
 
 }  // namespace
 
-// A tile is split into parts of eight sub-blocks or more where that makes the
-// whole shorter: by the time of a sub-block (0.76 us with two CTAs on an SM), of
-// the CTAs' rounds, and of writing and joining unfinished rows (2 x 520 bytes each
-// at 6 TB/s, and 3 us for the second kernel). Chunks that go on behind many keys
-// are tiles of one size, and take whole rounds (4 x 512 tokens behind up to 48k,
-// 28/4 heads, 464 tiles: 5 rounds of a third each instead of 2); tiles of whole
-// prompts are of every size, and fill the rounds up among themselves. The lengths
-// are on the device: the sizes that the host knows stand for them.
+// A tile is split into parts of two sub-blocks or more where that makes the whole
+// shorter by this estimate in us, fitted to 115 batches of 1 to 16k queries behind up
+// to 130k keys, each with up to 38 parts (its choice is 0.8 % slower than the best of
+// them, 50 % at worst and 7 % on average with a plainer one):
+//   a sub-block          0.45 with a CTA an SM, 0.6 with two, 0.72 with CTAs that go on
+//   the CTAs' chains     their longest part; with more blocks than CTAs the mean too
+//   the join             0.7, 0.04 a part, 1e-4 a row and 2e-4 a part of a row
+// Whole prompts have tiles of every size, of which the long ones are split: half as
+// many parts. The lengths are on the device: the sizes that the host knows stand for
+// them.
 PackedPlan packed_plan(const crisp_packed& p) {
   PackedPlan L{};
   const int group = p.hq / p.hkv;
@@ -938,13 +967,14 @@ PackedPlan packed_plan(const crisp_packed& p) {
     ++L.heads_log2;
   const double batch = std::max(p.batch, 1), q = p.total_q / batch, off = std::max(p.total_k - p.total_q, 0) / batch;
   const double mean = std::max((off + q / 2) / kSubKeys, 0.5), most = std::max(longest / double(kSubKeys), 1.0);
-  const double rounds = static_cast<double>(L.bound) * heads / kPackedCtas;
-  const double rows = static_cast<double>(p.total_q) * p.hq;
+  const double tiles = static_cast<double>(L.bound) * heads, rows = static_cast<double>(p.total_q) * p.hq;
   double best = 0.0;
   L.splits = 1;
-  for (int s = 1; s == 1 || (s <= kPackedCtas && most / s >= 8.0); ++s) {
-    const double subs = off > q ? std::ceil(rounds * s) / s * mean : std::max(rounds * mean, most / s);
-    const double us = 0.76 * subs + (s > 1 ? 3.0 + rows * s * 1040.0 / 6e6 : 0.0);
+  for (int s = 1; s == 1 || (s <= kPackedCtas && most / s >= 2.0); s += 1 + s / 32) {
+    const double parts = off > q ? s : (s + 1) / 2.0, part = most / s, blocks = tiles * parts;
+    double us = 2 * blocks <= kPackedCtas ? 0.45 * part : 0.6 * part;
+    if (blocks > kPackedCtas) us = std::max(us, 0.72 * mean * tiles / kPackedCtas);
+    if (s > 1) us += 0.7 + 0.04 * s + rows * (1e-4 + 2e-4 * parts);
     if (s == 1 || us < best) {
       best = us;
       L.splits = s;
@@ -1016,9 +1046,13 @@ cudaError_t launch_packed(const crisp_packed& p, const PackedPlan& plan, const T
                   static_cast<unsigned>(div_up(plan.chunks * p.hkv, 1 << plan.heads_log2)));
   e = launch_dependent(packed_kernel, grid, kThreads, smem, st, maps.q, maps.k64, maps.v, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
+  // two rows a warp where a row each would be more warps than the GPU holds at once
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
-  return launch_dependent(packed_join_kernel, dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
-                          kJoinWarps * 32, 0, st, a);
+  const bool two = rows > kPackedCtas * 32;
+  const int64_t units = two ? static_cast<int64_t>(p.total_q) * div_up(p.hq, 2) : rows;
+  const dim3 blocks(static_cast<unsigned>((units + kJoinWarps - 1) / kJoinWarps));
+  return two ? launch_dependent(packed_join_kernel<2, 2>, blocks, kJoinWarps * 32, 0, st, a)
+             : launch_dependent(packed_join_kernel<1, 4>, blocks, kJoinWarps * 32, 0, st, a);
 }
 
 }  // namespace crisp
