@@ -16,7 +16,7 @@
 // Two CTAs stay on each SM and take over blocks that have not started, one
 // ahead: the next tile's Q and first K and V are on their way while this one's
 // softmax and epilogue run. Short prompts need that (256 of up to 300 tokens,
-// 28/4 heads: 128 us, 5.0 TB/s; a CTA per tile, whose start, loads and end came
+// 28/4 heads: 121 us, 5.3 TB/s; a CTA per tile, whose start, loads and end came
 // one after the other, 340 us).
 //
 // Long prompts are bound by the tensor pipe at the rate of its 64-key products (a
@@ -85,7 +85,6 @@ struct PackedArgs {
   float c_log2;
   __nv_bfloat16* out;
   int64_t o_hs, o_ts;
-  int wide_out;           // out's rows allow 32-byte stores
   const __nv_bfloat16* v;
   int64_t v_hs, v_ts;
   float* part;            // [splits][total_q][hq][128]  unfinished rows (splits > 1)
@@ -328,6 +327,8 @@ __device__ __noinline__ void add_odd(const PackedArgs& a, const Item& it, int64_
   }
 }
 
+// kWide: the rows of out allow 32-byte stores.
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 2)
     packed_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ PackedArgs a) {
@@ -754,21 +755,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (!ok) break;
         if (warp_live) {
-          uint32_t v[2][32];
-          if (nsub > 0) {
-            tmem_ld32_async(tmem + lane_addr + 128 + chunk * 64, v[0]);
-            tmem_ld32_async(tmem + lane_addr + 160 + chunk * 64, v[1]);
-            tmem_ld_wait32(v[0]);
-            tmem_ld_wait32(v[1]);
+          uint32_t odd = 0u;  // no longer zero: the result is no finite number
+          auto o_read = [&]() {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.o_empty);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[0][e] = v[1][e] = 0u;
-          }
-          uint32_t odd = 0u;  // no longer zero: the result is no finite number
+          };
+          const uint32_t o_addr = tmem + lane_addr + 128 + chunk * 64;
           if (partial) {
+            uint32_t v[2][32];
+            tmem_ld32_async(o_addr, v[0]);
+            tmem_ld32_async(o_addr + 32, v[1]);
+            tmem_ld_wait32(v[0]);
+            tmem_ld_wait32(v[1]);
+            o_read();
             if (live) {
               float none = 0.f;
 #pragma unroll
@@ -783,21 +783,30 @@ __global__ void __launch_bounds__(kThreads, 2)
               if (chunk == 0) a.part_ml[row_index] = make_float2(l_row != 0.f ? m_ref : -INFINITY, l_row);
             }
           } else {
+            // (half a row after the other: both in line are code of every tile that has to
+            // be fetched again, 128 us for the short prompts above)
             const float inv_l = l_row != 0.f ? 1.0f / l_row : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              uint32_t v[32], w[16];
+              if (nsub > 0) {
+                tmem_ld32(o_addr + c, v);
+                if (c != 0) o_read();
+              } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; e += 16) {
-                uint32_t w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                  float lo, hi;
-                  fmul2(lo, hi, __uint_as_float(v[c][e + 2 * x]), __uint_as_float(v[c][e + 2 * x + 1]), inv_l, inv_l);
-                  w[x] = pack_bf16x2(lo, hi);
-                  note_odd(odd, w[x]);
-                }
-                if (live) store32(a.out + to + c * 32 + e, w, a.wide_out != 0);
+                for (int e = 0; e < 32; ++e) v[e] = 0u;
               }
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                float lo, hi;
+                fmul2(lo, hi, __uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]), inv_l, inv_l);
+                w[x] = pack_bf16x2(lo, hi);
+                note_odd(odd, w[x]);
+              }
+              if (live)
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) store32(a.out + to + c + 2 * e, w + e, kWide);
+            }
           }
           // Not finite: V may not be. Where it is, or a row that sees keys sums to 0, the
           // sums may have left fp32's range.
@@ -1025,8 +1034,8 @@ cudaError_t launch_packed(const crisp_packed& p, const PackedPlan& plan, const T
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   a.status = reinterpret_cast<DevStatus*>(ws);
-  a.wide_out = reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && (p.hq == 1 || out.head_stride % 16 == 0) &&
-               (p.total_q == 1 || out.tok_stride % 16 == 0);
+  const bool wide = reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && (p.hq == 1 || out.head_stride % 16 == 0) &&
+                    (p.total_q == 1 || out.tok_stride % 16 == 0);
   const size_t smem = kSmemBytes + batch_bytes(p.batch);
   // the most that any batch takes, once a device
   static std::atomic<uint64_t> allowed{0};
@@ -1035,16 +1044,18 @@ cudaError_t launch_packed(const crisp_packed& p, const PackedPlan& plan, const T
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
-    e = cudaFuncSetAttribute(packed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
-    if (e != cudaSuccess) return e;
+    for (auto* kernel : {packed_kernel<false>, packed_kernel<true>}) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmemBytes + batch_bytes(kMaxBatch)));
+      if (e != cudaSuccess) return e;
+    }
     allowed.fetch_or(bit, std::memory_order_relaxed);
   }
   // (heads side by side, tiles), parts, groups of heads; a tile holds more than 64
   // of at most 2^24 x 4096 rows
   const dim3 grid(static_cast<unsigned>(plan.bound) << plan.heads_log2, static_cast<unsigned>(plan.splits),
                   static_cast<unsigned>(div_up(plan.chunks * p.hkv, 1 << plan.heads_log2)));
-  e = launch_dependent(packed_kernel, grid, kThreads, smem, st, maps.q, maps.k64, maps.v, a);
+  e = launch_dependent(wide ? packed_kernel<true> : packed_kernel<false>, grid, kThreads, smem, st, maps.q, maps.k64, maps.v, a);
   if (e != cudaSuccess || plan.splits == 1) return e;
   // two rows a warp where a row each would be more warps than the GPU holds at once
   const int64_t rows = static_cast<int64_t>(p.total_q) * p.hq;
