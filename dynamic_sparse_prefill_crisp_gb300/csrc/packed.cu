@@ -21,7 +21,7 @@
 //
 // Long prompts are bound by the tensor pipe at the rate of its 64-key products (a
 // product's operands come from shared memory at 128 bytes a cycle, 48 cycles where
-// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.21 ms, 1822
+// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.20 ms, 1840
 // TFLOP/s, a sub-block 1225 cycles a CTA and 612 an SM.
 //
 // The products are csrc/attention.cu's: 64-key sub-blocks, two score buffers in
