@@ -85,6 +85,9 @@ ATTEND = [
     ("split-chunk-gqa7", 7, 1, [40], [3001]),
     ("split-ragged", 4, 1, [9, 33, 1, 0, 3], [9000, 40, 2222, 100, 1]),
     ("split-short-and-long", 2, 1, [60, 60, 60], [60, 513, 4097]),
+    ("split-in-twos", 4, 1, [1], [1001]),
+    ("split-many-rows", 7, 1, [1500, 40], [4400, 3001]),
+    ("split-whole-prompts", 5, 1, [2100, 130], None),
     ("batch-limit", 2, 1, [i % 3 for i in range(1024)], [i % 3 + i % 7 for i in range(1024)]),
     ("many-short", 4, 1, [(37 * i) % 200 for i in range(300)], None),
 ]
