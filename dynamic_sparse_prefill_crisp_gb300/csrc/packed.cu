@@ -34,7 +34,10 @@
 //    see them (to look through V first took 5000 cycles of a tile's 60000 in a 4k
 //    prompt).
 //  - a tile is done again, as two more items of the CTA, too where a row's sum
-//    passes 2^64: the exact row maxima first, then the sums at those.
+//    passes 2^64 or stays under 2^-64: the exact row maxima first, then the sums at
+//    those. (A sum is small where the first sub-block's scores are all -inf, and the
+//    reference 0 is none of the row's scores: exponentials below 2^-126 are zeros, of
+//    a sum of 2^-64 at most 2^-42 over 2^20 keys, of a smaller one up to all of it.)
 //  - when there are too few tiles for the GPU, a tile's keys are split over
 //    several blocks, whose unfinished rows a second kernel joins in a fixed order.
 //
@@ -71,6 +74,8 @@ constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,
 // kGuarded's results are not finite either), kMaxOnly and kFixed, with that look too.
 enum Mode : int { kFast, kGuarded, kMaxOnly, kFixed, kEnd };
 constexpr uint32_t batch_bytes(int batch) { return batch * 6u + 8u; }  // ranks and order
+
+constexpr float kSmallSum = 0x1p-64f;  // sum of a row that sees keys, below which the row is done again
 
 enum Redo : int { kNotFinite = 1, kOverflow = 2 };
 
@@ -808,12 +813,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int e = 0; e < 16; e += 8) store32(a.out + to + c + 2 * e, w + e, kWide);
             }
           }
-          // Not finite: V may not be. Where it is, or a row that sees keys sums to 0, the
-          // sums may have left fp32's range.
+          // Not finite: V may not be. Where it is, or the sum over keys is small, the sums
+          // may have left fp32's range.
           const int odd_v = mode == kFast ? 0 : *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]);
           if (live && (odd & 0x7fff7fffu) != 0u && mode <= kGuarded && (odd_v & kOddSeen) == 0)
             atomicOr(&sh.redo[n % kRing], mode == kFast ? kNotFinite : kOverflow);
-          if (live && mode == kFast && l_row == 0.f && pos >= sub0 * kSubKeys) atomicOr(&sh.redo[n % kRing], kOverflow);
+          if (live && mode == kFast && l_row < kSmallSum && pos >= sub0 * kSubKeys) atomicOr(&sh.redo[n % kRing], kOverflow);
           if (live && (odd_v & kOddTaken) != 0) {
             // What guard_v took out, for the rows that see it (their p is above
             // zero): infinities and NaN, whatever the finite rest is.
