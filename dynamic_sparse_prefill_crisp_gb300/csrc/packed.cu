@@ -856,17 +856,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
   grid_dep_wait();
   const int tok = static_cast<int>(unit / groups), head0 = static_cast<int>(unit % groups) * kJoinRows;
   if (tok >= a.total_q) return;
-  // the last sequence that starts at or before the token
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= tok) lo = mid;
-    else hi = mid;
+  // The sequence that holds the token, looked for among all, 32 at a time: where some
+  // are not well-formed, the sums need not ascend over the others either.
+  int t = -1;
+  int2 n = make_int2(0, 0);
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    bool holds = b < a.batch && a.cu_q[b] <= tok && tok < a.cu_q[b + 1];
+    if (holds) n = seq_lens(a, b, holds);
+    const uint32_t which = __ballot_sync(0xffffffffu, holds);
+    if (which == 0u) continue;
+    const int at = __ffs(which) - 1;
+    n = make_int2(__shfl_sync(0xffffffffu, n.x, at), __shfl_sync(0xffffffffu, n.y, at));
+    t = tok - a.cu_q[b0 + at];
+    break;
   }
-  bool ok;
-  const int2 n = seq_lens(a, lo, ok);
-  const int t = tok - a.cu_q[lo];
-  if (t < 0 || t >= n.x) return;
+  if (t < 0) return;
   const int cost = tile_cost(n.x, n.y, t / a.tokens * a.tokens, a.tokens);
   const int ns = min(a.splits, div_up(cost, a.split_subs));
   if (ns <= 1) return;  // written by the tile's only CTA

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import dynamic_sparse_prefill_crisp_gb300 as crisp
-from packed_helpers import D, attention, check, dev32
+from packed_helpers import D, attention, check, dev32, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,52 @@ def test_low_scores_behind_keys_of_minus_infinity_in_parts(level, tail):
     got = call(q, k, v, [0, nq], [0, nk], split=True)
     want, tol = attention(q.double().numpy(), *(t[nk - tail:].double().numpy() for t in (k, v)), [nq], [tail])
     check(got, want, tol)
+
+
+# ------------------------------------------------------------------- running sums
+def rows_of(cu_q, cu_k, total_q, total_k):
+    """Which sequences of any sums count, by the documented rule, on plain numbers."""
+    n = len(cu_q) - 1
+    return [0 <= cu_q[b] <= cu_q[b + 1] <= total_q and 0 <= cu_k[b] <= cu_k[b + 1] <= total_k and
+            cu_q[b + 1] - cu_q[b] <= 1 << 20 and cu_k[b + 1] - cu_k[b] <= 1 << 20 for b in range(n)]
+
+
+def against_the_rule(q, k, v, cu_q, cu_k, split):
+    good = rows_of(cu_q, cu_k, q.shape[0], k.shape[0])
+    got = call(q, k, v, cu_q, cu_k, status=OK if all(good) else BOUNDS, split=split)
+    left = np.ones(q.shape[0], dtype=bool)
+    for b, ok in enumerate(good):
+        if not ok or cu_q[b] == cu_q[b + 1]:
+            continue
+        at, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        want, tol = attention(*(t.double().numpy() for t in (q[at], k[keys], v[keys])), [at.stop - at.start],
+                              [keys.stop - keys.start])
+        check(got[at], want, tol)
+        left[at] = False
+    assert torch.isnan(got[torch.from_numpy(left).cuda()]).all()
+
+
+@pytest.mark.parametrize("cu_q", [[0, 2 ** 30, 40, 120], [0, 2 ** 30, 90, 120], [-5, 30, 40, 120],
+                                  [100, 30, 40, 120], [0, 2 ** 31 - 1, 40, 120], [0, 30, 121, 120]])
+def test_bad_sums_between_split_sequences(cu_q):
+    q, k, v = inputs(4, 1, 120, 6000, 87)
+    against_the_rule(q, k, v, cu_q, [0, 2000, 4000, 6000], split=True)
+
+
+@pytest.mark.parametrize("cu_k", [[0, 2 ** 30, 2000, 6000], [0, 4000, 2000, 6000], [-1, 2000, 4000, 6001],
+                                  [0, 3000, 0, 3000]])
+def test_bad_key_sums_between_split_sequences(cu_k):
+    q, k, v = inputs(4, 1, 120, 6000, 88)
+    against_the_rule(q, k, v, [0, 40, 80, 120], cu_k, split=True)
+
+
+def test_bad_sums_among_many_split_sequences():
+    # 75 sequences of 3 queries, each behind 200 keys but two; sums in the middle that are none
+    k_lens = [200] * 75
+    k_lens[5], k_lens[50] = 9000, 7000
+    cu_q, cu_k = starts([3] * 75), starts(k_lens)
+    q, k, v = inputs(4, 1, int(cu_q[-1]), int(cu_k[-1]), 89)
+    for at, value in ((10, 2 ** 30), (33, -1), (70, 2 ** 31 - 1)):
+        sums = cu_q.copy()
+        sums[at] = value
+        against_the_rule(q, k, v, sums.tolist(), cu_k.tolist(), split=True)
