@@ -846,6 +846,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // row would be more than the GPU holds at once (32k rows of whole prompts in halves: 8
 // us, 11 with one).
 constexpr int kJoinWarps = 4;
+
 template <int kJoinRows, int kJoinAhead>
 __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __grid_constant__ PackedArgs a) {
   const int lane = threadIdx.x & 31;
@@ -856,26 +857,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
   grid_dep_wait();
   const int tok = static_cast<int>(unit / groups), head0 = static_cast<int>(unit % groups) * kJoinRows;
   if (tok >= a.total_q) return;
-  // The sequence that holds the token, looked for among all, 32 at a time: where some
-  // are not well-formed, the sums need not ascend over the others either.
-  int t = -1;
-  int2 n = make_int2(0, 0);
+  // The parts of the token's tile, by the lane that finds the sequence that holds it:
+  // all are looked at, 32 at a time, because the sums need not ascend where some are not
+  // well-formed.
+  int ns = -1;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    bool holds = b < a.batch && a.cu_q[b] <= tok && tok < a.cu_q[b + 1];
-    if (holds) n = seq_lens(a, b, holds);
-    const uint32_t which = __ballot_sync(0xffffffffu, holds);
-    if (which == 0u) continue;
-    const int at = __ffs(which) - 1;
-    n = make_int2(__shfl_sync(0xffffffffu, n.x, at), __shfl_sync(0xffffffffu, n.y, at));
-    t = tok - a.cu_q[b0 + at];
-    break;
+  for (int b0 = 0; ns < 0 && b0 < a.batch; b0 += 32) {
+    const int b = min(b0 + lane, a.batch - 1);  // (the last one, more than once)
+    bool ok;
+    const int2 n = seq_lens(a, b, ok);
+    const int t = ok ? tok - a.cu_q[b] : -1;
+    const bool holds = t >= 0 && t < n.x;
+    const int cost = tile_cost(n.x, n.y, t / a.tokens * a.tokens, a.tokens);
+    ns = __reduce_max_sync(0xffffffffu, holds ? min(a.splits, div_up(cost, a.split_subs)) : -1);
   }
-  if (t < 0) return;
-  const int cost = tile_cost(n.x, n.y, t / a.tokens * a.tokens, a.tokens);
-  const int ns = min(a.splits, div_up(cost, a.split_subs));
-  if (ns <= 1) return;  // written by the tile's only CTA
+  if (ns <= 1) return;  // written by the tile's only CTA, or no sequence's
   const int64_t row0 = static_cast<int64_t>(tok) * a.hq + head0;
   const int live = min(kJoinRows, a.hq - head0);
   float top[kJoinRows], l[kJoinRows];
