@@ -154,6 +154,27 @@ __device__ __forceinline__ int2 seq_lens(const PackedArgs& a, int b, bool& ok) {
   return ok ? make_int2(q1 - q0, k1 - k0) : make_int2(0, 0);
 }
 
+// Whether sequence b begins before the end of an earlier one that is well-formed; then
+// it counts as empty, and no row belongs to two. (Only where some are not: else all sums
+// ascend.)
+__device__ __noinline__ bool begins_early(const PackedArgs& a, int b) {
+  for (int c = 0; c < b; ++c) {
+    bool ok;
+    seq_lens(a, c, ok);
+    if (ok && a.cu_q[c + 1] > a.cu_q[b]) return true;
+  }
+  return false;
+}
+
+// Reports sums that are not well-formed, and leaves sequences out that begin early.
+// All threads.
+__device__ __noinline__ void drop_early(const PackedArgs& a, int* keys, int* tiles) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x801);
+  for (int b = threadIdx.x; b < a.batch; b += kThreads)
+    if (tiles[b] > 0 && begins_early(a, b)) keys[b] = tiles[b] = 0;
+  __syncthreads();
+}
+
 // The order in which the CTAs take the sequences, most keys first (equal ones: in
 // the batch's order): order[i] the i-th one's place in the batch, ranks[i] the
 // tiles of those before it, ranks[batch] all tiles. All threads; keys: room for
@@ -161,18 +182,19 @@ __device__ __forceinline__ int2 seq_lens(const PackedArgs& a, int b, bool& ok) {
 __device__ __forceinline__ void order_sequences(const PackedArgs& a, int* keys, uint16_t* order, int* ranks) {
   const int padded = div_up(a.batch, 4) * 4;
   int* tiles = keys + padded;
+  bool all_ok = true;
 #pragma unroll 1
   for (int b = threadIdx.x; b < padded; b += kThreads) {
     int2 n = make_int2(0, -1);
     if (b < a.batch) {
       bool ok;
       n = seq_lens(a, b, ok);
-      if (!ok && blockIdx.x == 0) report_error(a.status, CRISP_ERR_BOUNDS, 0x801);
+      all_ok = all_ok && ok;
     }
     keys[b] = n.y;
     tiles[b] = over_tokens(a, n.x + a.tokens - 1);
   }
-  __syncthreads();
+  if (__syncthreads_or(!all_ok)) drop_early(a, keys, tiles);
 #pragma unroll 1
   for (int b = threadIdx.x; b < a.batch; b += kThreads) {
     const int mine = keys[b];
@@ -861,13 +883,15 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
   // all are looked at, 32 at a time, because the sums need not ascend where some are not
   // well-formed.
   int ns = -1;
+  bool all_ok = true;
 #pragma unroll 1
   for (int b0 = 0; ns < 0 && b0 < a.batch; b0 += 32) {
     const int b = min(b0 + lane, a.batch - 1);  // (the last one, more than once)
     bool ok;
     const int2 n = seq_lens(a, b, ok);
     const int t = ok ? tok - a.cu_q[b] : -1;
-    const bool holds = t >= 0 && t < n.x;
+    all_ok = __all_sync(0xffffffffu, ok) && all_ok;
+    const bool holds = t >= 0 && t < n.x && (all_ok || !begins_early(a, b));
     const int cost = tile_cost(n.x, n.y, t / a.tokens * a.tokens, a.tokens);
     ns = __reduce_max_sync(0xffffffffu, holds ? min(a.splits, div_up(cost, a.split_subs)) : -1);
   }

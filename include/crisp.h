@@ -661,7 +661,8 @@ CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, s
  * may be shared). What a row does not see does not reach it, infinities and NaN in v
  * included. A sequence whose running sums descend, leave [0, total_q] or [0,
  * total_k], or are more than 2^20 rows apart is CRISP_ERR_BOUNDS and counts as
- * empty: its rows are left as they were. Precision: products of bf16 in fp32, p
+ * empty, and so does one that begins in cu_q before the end of an earlier one
+ * whose sums do none of that: their rows are left as they were. Precision: products of bf16 in fp32, p
  * rounded to bf16 (2^-8 of itself) for the product with v, sums in fp32. The
  * result does not depend on timing. */
 CRISP_API crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,

@@ -72,8 +72,9 @@ def test_low_scores_behind_keys_of_minus_infinity_in_parts(level, tail):
 def rows_of(cu_q, cu_k, total_q, total_k):
     """Which sequences of any sums count, by the documented rule, on plain numbers."""
     n = len(cu_q) - 1
-    return [0 <= cu_q[b] <= cu_q[b + 1] <= total_q and 0 <= cu_k[b] <= cu_k[b + 1] <= total_k and
+    fine = [0 <= cu_q[b] <= cu_q[b + 1] <= total_q and 0 <= cu_k[b] <= cu_k[b + 1] <= total_k and
             cu_q[b + 1] - cu_q[b] <= 1 << 20 and cu_k[b + 1] - cu_k[b] <= 1 << 20 for b in range(n)]
+    return [fine[b] and not any(fine[c] and cu_q[c + 1] > cu_q[b] for c in range(b)) for b in range(n)]
 
 
 def against_the_rule(q, k, v, cu_q, cu_k, split):
@@ -112,6 +113,31 @@ def test_bad_sums_among_many_split_sequences():
     cu_q, cu_k = starts([3] * 75), starts(k_lens)
     q, k, v = inputs(4, 1, int(cu_q[-1]), int(cu_k[-1]), 89)
     for at, value in ((10, 2 ** 30), (33, -1), (70, 2 ** 31 - 1)):
+        sums = cu_q.copy()
+        sums[at] = value
+        against_the_rule(q, k, v, sums.tolist(), cu_k.tolist(), split=True)
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [
+    ([0, 100, 0, 100], [0, 2000, 4000, 6000]),           # the same rows twice
+    ([0, 100, 0, 100, 0, 100, 0, 100], [0, 900, 900, 1800, 1800, 2700, 2700, 6000]),  # more tiles than rows have
+    ([0, 40, 20, 120], [0, 2000, 4000, 6000]),           # rows 20 to 39 twice
+    ([0, 120, 40, 80], [0, 2000, 4000, 6000]),           # inside an earlier one's
+    ([0, 40, 20, 30, 60, 120], [0, 1000, 2000, 3000, 4000, 6000]),  # after one that counts as empty itself
+    ([50, 120, 0, 50], [0, 2000, 4000, 6000])])          # apart, the later rows first
+def test_sequences_that_share_rows(cu_q, cu_k):
+    q, k, v = inputs(4, 1, 120, 6000, 90)
+    against_the_rule(q, k, v, cu_q, cu_k, split=True)
+    # and where tiles are whole
+    against_the_rule(q, k[:120], v[:120], cu_q, [x // 50 for x in cu_k], split=False)
+
+
+def test_sequences_that_share_rows_among_many():
+    k_lens = [200] * 75
+    k_lens[5], k_lens[50] = 9000, 7000
+    cu_q, cu_k = starts([3] * 75), starts(k_lens)
+    q, k, v = inputs(4, 1, int(cu_q[-1]), int(cu_k[-1]), 91)
+    for at, value in ((33, 0), (40, 7), (70, 140), (20, 80)):
         sums = cu_q.copy()
         sums[at] = value
         against_the_rule(q, k, v, sums.tolist(), cu_k.tolist(), split=True)
