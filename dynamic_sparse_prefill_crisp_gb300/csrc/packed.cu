@@ -646,6 +646,11 @@ __global__ void __launch_bounds__(kThreads, 2)
               }
               go = __shfl_sync(0xffffffffu, go ? 1 : 0, from) != 0;
               if (!go) break;
+              // every lane that reads V sees its barrier's phase for itself (its next one comes
+              // no earlier than the product below)
+              const uint32_t phase = __shfl_sync(0xffffffffu, vn.parity(i & 1) ^ 1u, from);
+              go = await_warp(&sh.v_full[i & 1], phase, &sh.abort);
+              if (!go) break;
               const int odd = guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane);
               if (odd != 0) atomicOr(&sh.odd_v[n % kRing], odd);
               fence_async_shared();

@@ -141,3 +141,29 @@ def test_sequences_that_share_rows_among_many():
         sums = cu_q.copy()
         sums[at] = value
         against_the_rule(q, k, v, sums.tolist(), cu_k.tolist(), split=True)
+
+
+# ------------------------------------------------------------- tiles done again
+@pytest.mark.parametrize("q_lens,k_lens", [([900, 300], [900, 300]), ([40, 30], [7000, 3001])])
+def test_tiles_done_again_read_what_was_copied(q_lens, k_lens):
+    # every tile holds values that are not finite in its last keys and behind them: both slots of V are looked
+    # through again and again, and each time the same bits come out
+    cu_q, cu_k = starts(q_lens), starts(k_lens)
+    q, k, v = inputs(14, 2, int(cu_q[-1]), int(cu_k[-1]), 92)
+    clean = call(q, k, v, cu_q, cu_k)
+    w = v.clone()
+    odd = torch.zeros(v.shape[0], dtype=torch.bool)
+    for b, (nq, nk) in enumerate(zip(q_lens, k_lens)):
+        odd[cu_k[b] + nk - nq + 5:cu_k[b + 1]:9] = True
+    w[odd, :, 5], w[odd, :, 90] = float("inf"), float("nan")
+    got = call(q, k, w, cu_q, cu_k)
+    rest = [f for f in range(D) if f not in (5, 90)]
+    seen = torch.zeros(q.shape[0], dtype=torch.bool)
+    for b in range(2):
+        first = int(cu_q[b]) + 5
+        seen[first:cu_q[b + 1]] = True
+    assert torch.equal(got[~seen], clean[~seen]) and torch.equal(got[..., rest], clean[..., rest])
+    assert torch.isnan(got[seen][..., 90]).all() and (got[seen][..., 5] == float("inf")).all()
+    for _ in range(20):
+        again = call(q, k, w, cu_q, cu_k)
+        assert torch.equal(again.view(torch.int16), got.view(torch.int16))
