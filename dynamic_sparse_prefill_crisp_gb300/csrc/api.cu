@@ -933,6 +933,13 @@ crisp_status check_cache(const crisp_kv_cache* c) {
   return CRISP_OK;
 }
 
+// What crisp_kv_gather reads of a cache, also of one without sequences.
+crisp_status check_pages(const crisp_kv_cache* c) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return CRISP_ERR_INVALID_ARG;
+  return aligned16(c->k) && aligned16(c->v) && aligned(c->k_scale, 4) && aligned(c->v_scale, 4) ? CRISP_OK
+                                                                                               : CRISP_ERR_ALIGN;
+}
+
 // [batch][heads][tokens][128]; the stride of an axis of one entry is not used.
 crisp_status check_tokens(const crisp_tokens* t, int batch, int heads, int tokens) {
   if (!t || !t->data) return CRISP_ERR_INVALID_ARG;
@@ -1168,7 +1175,8 @@ crisp_status crisp_kv_gather(const crisp_kv_cache* cache, const int32_t* slots, 
     crisp_status st = check_cache(cache);
     if (st != CRISP_OK) return st;
     if (n < 0 || n > kMaxPacked) return CRISP_ERR_SHAPE;
-    if (n == 0 || cache->batch == 0) return CRISP_OK;  // no rows
+    if (n == 0) return CRISP_OK;  // no rows
+    if ((st = check_pages(cache)) != CRISP_OK) return st;
     if (!slots) return CRISP_ERR_INVALID_ARG;
     if (!aligned(slots, 4) || !aligned(count, 4)) return CRISP_ERR_ALIGN;
     if ((st = check_tokens(k_out, 1, cache->hkv, n)) != CRISP_OK) return st;

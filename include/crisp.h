@@ -631,7 +631,7 @@ CRISP_API crisp_status crisp_kv_append_packed(const crisp_kv_cache* cache, const
  * the device, NULL: n; after crisp_kv_reserve, all_slots and cu_all + batch). A
  * negative slot leaves its row as it was; one outside the pool is
  * CRISP_ERR_BOUNDS and does too. 0 <= n <= 2^24. The cache's table and lens are
- * not read. Workspace: as for crisp_kv_append. */
+ * not read, and its batch may be 0. Workspace: as for crisp_kv_append. */
 CRISP_API crisp_status crisp_kv_gather(const crisp_kv_cache* cache, const int32_t* slots, int32_t n,
                                        const int32_t* count, const crisp_tokens* k_out, const crisp_tokens* v_out,
                                        void* ws, size_t ws_bytes, crisp_stream_t stream);

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import dynamic_sparse_prefill_crisp_gb300 as crisp
-from packed_helpers import D, attention, check, dev32, starts
+from kv_helpers import VALUES, Pools
+from packed_helpers import B, D, attention, check, dev32, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +168,21 @@ def test_tiles_done_again_read_what_was_copied(q_lens, k_lens):
     for _ in range(20):
         again = call(q, k, w, cu_q, cu_k)
         assert torch.equal(again.view(torch.int16), got.view(torch.int16))
+
+
+# --------------------------------------------------------------------- the cache
+def test_rows_of_a_cache_without_sequences():
+    pools = Pools(3, 2)
+    codes = np.random.default_rng(93).integers(0, 127, (3, 2, B, D)).astype(np.uint8)
+    for t, s in ((pools.k, pools.ks), (pools.v, pools.vs)):
+        t.copy_(torch.from_numpy(codes))
+        s.fill_(2.0)
+    cache = crisp.make_kv_cache(pools.k, pools.v, pools.ks, pools.vs, torch.empty((0, 4), dtype=torch.int32, device="cuda"),
+                                torch.empty(0, dtype=torch.int32, device="cuda"))
+    ws = workspace(crisp.kv_append_workspace_size(cache))
+    slots = np.arange(0, 3 * B, 5)
+    outs = [torch.full((len(slots), 2, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    crisp.kv_gather(cache, dev32(slots), *outs, ws)
+    assert crisp.read_status(ws) == OK
+    for out in outs:
+        assert np.array_equal(out.double().cpu().numpy(), VALUES[codes[slots // B, :, slots % B]] * 2.0)

@@ -120,6 +120,15 @@ def test_gather_refusals(L):
     assert gather(L, n=0, slots=None, ws=None) == OK
 
 
+def test_gather_goes_by_the_pages_alone(L):
+    # a cache without sequences has rows to read all the same
+    none = dict(batch=0, table=None, lens=None)
+    assert gather(L, cache(**none), ws=None) == WORKSPACE and gather(L, cache(**none), slots=None) == INVALID
+    for field in ("k", "v", "k_scale", "v_scale"):
+        assert gather(L, cache(**none, **{field: None})) == INVALID and gather(L, cache(**none, **{field: 258})) == ALIGN
+    assert gather(L, cache(**none, k=None), n=0, slots=None) == OK
+
+
 def test_packed_prefill_refusals(L):
     n = ctypes.c_size_t()
     for field, value, code in (("head_dim", 64, SHAPE), ("hq", 0, SHAPE), ("hq", 4098, SHAPE), ("hq", 7, SHAPE),
