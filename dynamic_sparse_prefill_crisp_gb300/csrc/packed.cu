@@ -77,6 +77,12 @@ constexpr uint32_t batch_bytes(int batch) { return batch * 6u + 8u; }  // ranks 
 
 constexpr float kSmallSum = 0x1p-64f;  // sum of a row that sees keys, below which the row is done again
 
+// Room below fp32's largest number: p of a tile that is done again at its row maxima is
+// at most 2^-24 (and the parts' weights of a join too), so that sums of p v over 2^20
+// keys stay finite whatever finite v is. (What that takes below 2^-126 is a 2^-102 of the
+// largest.)
+constexpr float kHeadroom = 24.f;
+
 enum Redo : int { kNotFinite = 1, kOverflow = 2 };
 
 struct PackedArgs {
@@ -856,6 +862,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else if (nsub > 0) {
           if (lane == 0) mbar_arrive(&sh.o_empty);
         }
+      } else {
+        m_ref += kHeadroom;  // (here: added where the maximum is taken, it made long prompts 1 to 4 % slower)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.item_empty[n % kRing]);
@@ -867,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// The rows of split tiles: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
+// The rows of split tiles: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, both times 2^-24,
 // with M the largest reference m_s, in the order of the splits. A warp takes kJoinRows
 // rows of a token, kJoinAhead parts of each in flight: one row, or two where a warp a
 // row would be more than the GPU holds at once (32k rows of whole prompts in halves: 8
@@ -928,7 +936,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) packed_join_kernel(const __gr
       w[r] = 0.f;
       if (s0 + lane < ns && r < live) {
         const float2 ml = a.part_ml[(s0 + lane) * rows + row0 + r];
-        w[r] = ml.y != 0.f ? ex2_approx(ml.x - top[r]) : 0.f;
+        w[r] = ml.y != 0.f ? ex2_approx(ml.x - top[r]) * 0x1p-24f : 0.f;  // kHeadroom
         l[r] += w[r] != 0.f ? ml.y * w[r] : 0.f;
       }
     }

@@ -69,6 +69,18 @@ def test_low_scores_behind_keys_of_minus_infinity_in_parts(level, tail):
     check(got, want, tol)
 
 
+@pytest.mark.parametrize("nq,nk", [(300, 300), (5, 5000)])
+@pytest.mark.parametrize("top", [2.0 ** 104, 2.0 ** 120, 2.0 ** 127])
+def test_values_up_to_the_largest(nq, nk, top):
+    # sums of p v pass fp32's largest number before they are divided, results do not
+    q, k, v = inputs(4, 1, nq, nk, 83)
+    v = bf16(torch.sign(v.float()) * (1.0 + 0.9 * torch.frac(v.float().abs())) * top)
+    assert torch.isfinite(v).all()
+    got = call(q, k, v, [0, nq], [0, nk], split=nk > 1000)
+    want, tol = attention(*(t.double().numpy() for t in (q, k, v)), [nq], [nk])
+    check(got, want, tol)
+
+
 # ------------------------------------------------------------------- running sums
 def rows_of(cu_q, cu_k, total_q, total_k):
     """Which sequences of any sums count, by the documented rule, on plain numbers."""
