@@ -71,7 +71,7 @@ constexpr uint32_t kTmemCols = 256;                       // S/P [0,64) and [64,
 
 // What the CTA does with a tile: kFast; then, where a result is not finite,
 // kGuarded, the same but for a look through V; and where sums left their range (or
-// kGuarded's results are not finite either), kMaxOnly and kFixed, with that look too.
+// kGuarded's results are not finite where V is), kMaxOnly and kFixed, with that look too.
 enum Mode : int { kFast, kGuarded, kMaxOnly, kFixed, kEnd };
 constexpr uint32_t batch_bytes(int batch) { return batch * 6u + 8u; }  // ranks and order
 
@@ -127,7 +127,7 @@ struct Shared {
   uint32_t tmem_base;
   int abort;
   int redo[kRing];       // Redo bits: the slot's item has to be done again
-  int odd_v[kRing];      // OddV bits of the slot's item, where it was looked through
+  uint32_t odd_v[kRing][5];  // of the slot's item, where V was looked through: see guard_v
   Item item[kRing], again[kRing];
   float xch[2][2][kB];   // [exchange & 1][chunk][row]: partial row maxima, partial row sums
 };
@@ -296,12 +296,12 @@ __device__ __forceinline__ void note_odd(uint32_t& acc, uint32_t w) {
 // Makes a sub-block of V (two halves of 64 keys x 64 features, each key's 128
 // bytes in a row) safe to multiply with p = 0: rows from `seen_end` on are no
 // keys of this tile and become zeros, and in rows from `all_end` on, which some
-// of the tile's rows do not see, elements that are not finite become zero.
-// Returns OddV bits. One warp, eight lanes a row, eight reads in flight; swizzling
-// moves 16-byte pieces inside a row only.
-enum OddV : int { kOddSeen = 1, kOddTaken = 2 };  // not finite: an element of the tile's keys; one that became zero
-__device__ __forceinline__ int guard_v(uint8_t* sub, int all_end, int seen_end, int lane) {
-  int odd = 0;
+// of the tile's rows do not see, elements that are not finite become zero (then
+// odd[kTaken] = 1). odd[c / 32], bit c % 32: a key that all rows see has an element
+// of feature c that is not finite. One warp, eight lanes a row, eight reads in
+// flight; swizzling moves 16-byte pieces inside a row only.
+constexpr int kTaken = kD / 32;
+__device__ __noinline__ void guard_v(uint8_t* sub, int all_end, int seen_end, int lane, uint32_t* odd) {
   uint8_t* mine = sub + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll 1
   for (int row0 = 0; row0 < kSubKeys; row0 += 16) {
@@ -325,20 +325,24 @@ __device__ __forceinline__ int guard_v(uint8_t* sub, int all_end, int seen_end, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) note_odd(acc, (&x[u][half].x)[e]);
     if ((acc & 0x7fff7fffu) == 0u) continue;
-    odd |= kOddSeen;
 #pragma unroll 1
     for (int e = 0; e < 4 * 2 * 4; ++e) {  // word by word
-      const int u = e >> 3, half = e >> 2 & 1;
-      if (row0 + 4 * u + (lane >> 3) < all_end) continue;
+      const int u = e >> 3, half = e >> 2 & 1, row = row0 + 4 * u + (lane >> 3);
       uint32_t* at = reinterpret_cast<uint32_t*>(mine + half * kSubHalf + (row0 + 4 * u) * 128) + (e & 3);
       uint32_t w = *at;
-      if (odd_bf16(w)) w &= 0xffff0000u;
-      if (odd_bf16(w >> 16)) w &= 0x0000ffffu;
-      if (w != *at) odd |= kOddTaken;
+      const uint32_t which = (odd_bf16(w) ? 1u : 0u) | (odd_bf16(w >> 16) ? 2u : 0u);
+      if (which == 0u) continue;
+      if (row < all_end) {
+        const int feature = half * 64 + ((lane & 7) ^ (row & 7)) * 8 + (e & 3) * 2;
+        atomicOr(&odd[feature / 32], which << feature % 32);
+        continue;
+      }
+      if (which & 1u) w &= 0xffff0000u;
+      if (which & 2u) w &= 0x0000ffffu;
       *at = w;
+      odd[kTaken] = 1u;
     }
   }
-  return odd;
 }
 
 // out += v_j over the keys j in [from, last] and 64 columns, where v_j is not
@@ -358,6 +362,31 @@ __device__ __noinline__ void add_odd(const PackedArgs& a, const Item& it, int64_
         a.out[to + e] = __float2bfloat16(__bfloat162float(a.out[to + e]) + x);
     }
   }
+}
+
+// What is left of a row's 64 columns from col0 on, where its results are not all finite or
+// its tile is done again. V may not be finite: the tile is looked through. Where it was,
+// and a result is not finite although what all rows see of its feature is, the sums
+// have left fp32's range. And what guard_v took out is added for the rows that see it
+// (their p is above zero): infinities and NaN, whatever the finite rest is.
+__device__ __noinline__ void settle(const PackedArgs& a, const Item& it, int64_t to, int col0, int last, bool odd,
+                                    Shared& sh, int slot) {
+  const uint32_t* odd_v = sh.odd_v[slot];
+  int* redo = &sh.redo[slot];
+  const bool partial = it.partial != 0;
+  if (odd && it.mode == kFast) atomicOr(redo, kNotFinite);
+  if (odd && it.mode == kGuarded) {
+    bool found = false;
+#pragma unroll 1
+    for (int e = 0; e < 64; ++e) {
+      const float x = partial ? a.part[to + e] : __bfloat162float(a.out[to + e]);
+      found = found || (!(fabsf(x) < INFINITY) && (odd_v[(col0 + e) / 32] >> e % 32 & 1u) == 0u);
+    }
+    if (found) atomicOr(redo, kOverflow);
+  }
+  if (it.mode != kFast && odd_v[kTaken] != 0u)
+    add_odd(a, it, to, partial, col0, max(it.nk - it.nq + it.t0 + 1, it.sub0 * kSubKeys),
+            min(last, (it.sub0 + it.nsub) * kSubKeys - 1));
 }
 
 // kWide: the rows of out allow 32-byte stores.
@@ -387,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&sh.p_full[s], kSoftmaxWarps);
     }
     for (int s = 0; s < kRing; ++s) {
-      sh.redo[s] = sh.odd_v[s] = 0;
+      sh.redo[s] = 0;
       mbar_init(&sh.item_full[s], 1);
       mbar_init(&sh.item_empty[s], kSoftmaxWarps + 1);
     }
@@ -499,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (leader) {
         sh.item[n % kRing] = it;
-        sh.odd_v[n % kRing] = 0;
+        if (it.mode != kFast)
+          for (uint32_t& w : sh.odd_v[n % kRing]) w = 0u;
         mbar_arrive(&sh.item_full[n % kRing]);
       }
       if (it.mode == kEnd) break;
@@ -657,8 +687,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               const uint32_t phase = __shfl_sync(0xffffffffu, vn.parity(i & 1) ^ 1u, from);
               go = await_warp(&sh.v_full[i & 1], phase, &sh.abort);
               if (!go) break;
-              const int odd = guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane);
-              if (odd != 0) atomicOr(&sh.odd_v[n % kRing], odd);
+              guard_v(sV + (i & 1) * kSub, kv_all - i * kSubKeys, kv_end - i * kSubKeys, lane, sh.odd_v[n % kRing]);
               fence_async_shared();
               __syncwarp();
             }
@@ -846,18 +875,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int e = 0; e < 16; e += 8) store32(a.out + to + c + 2 * e, w + e, kWide);
             }
           }
-          // Not finite: V may not be. Where it is, or the sum over keys is small, the sums
-          // may have left fp32's range.
-          const int odd_v = mode == kFast ? 0 : *reinterpret_cast<volatile int*>(&sh.odd_v[n % kRing]);
-          if (live && (odd & 0x7fff7fffu) != 0u && mode <= kGuarded && (odd_v & kOddSeen) == 0)
-            atomicOr(&sh.redo[n % kRing], mode == kFast ? kNotFinite : kOverflow);
           if (live && mode == kFast && l_row < kSmallSum && pos >= sub0 * kSubKeys) atomicOr(&sh.redo[n % kRing], kOverflow);
-          if (live && (odd_v & kOddTaken) != 0) {
-            // What guard_v took out, for the rows that see it (their p is above
-            // zero): infinities and NaN, whatever the finite rest is.
-            add_odd(a, it, to, partial, chunk * 64, max(all_of(it), sub0 * kSubKeys),
-                    min(pos, (sub0 + nsub) * kSubKeys - 1));
-          }
+          const bool not_finite = (odd & 0x7fff7fffu) != 0u;
+          if (live && (not_finite || mode != kFast))
+            settle(a, it, to, chunk * 64, pos, not_finite, sh, n % kRing);
           __syncwarp();
         } else if (nsub > 0) {
           if (lane == 0) mbar_arrive(&sh.o_empty);

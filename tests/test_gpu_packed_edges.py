@@ -81,6 +81,29 @@ def test_values_up_to_the_largest(nq, nk, top):
     check(got, want, tol)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_values_that_are_not_finite_beside_sums_out_of_range(value):
+    # one feature of one value that every row sees is not finite; the other features' sums leave fp32's range
+    # at the first reference: scores grow by 40 binary orders, V is near 2^100
+    n = 400
+    q, k, v = (x.double().numpy() for x in inputs(4, 1, n, n, 84))
+    q[:, :, 0] = 1.0
+    q[:, :, 1:] *= 0.1
+    k[:, 0, 0] = np.where(np.arange(n) < 64, 0.0, 40.0 * np.log(2.0) * np.sqrt(D))
+    v *= 2.0 ** 100
+    q, k, v = bf16(q), bf16(k), bf16(v)
+    want, tol = attention(*(t.double().numpy() for t in (q, k, v)), [n], [n])
+    for key, feature in ((0, 77), (0, 3), (130, 40)):
+        w = v.clone()
+        w[key, 0, feature] = value
+        got = call(q, k, w, [0, n], [0, n])
+        rest = [f for f in range(D) if f != feature]
+        check(got[..., rest], want[..., rest], tol[..., rest])
+        check(got[:key, :, feature], want[:key, :, feature], tol[:key, :, feature])
+        hit = got[key:, :, feature].float()
+        assert torch.isnan(hit).all() if value != value else (hit == value).all()
+
+
 # ------------------------------------------------------------------- running sums
 def rows_of(cu_q, cu_k, total_q, total_k):
     """Which sequences of any sums count, by the documented rule, on plain numbers."""
