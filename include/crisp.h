@@ -663,8 +663,11 @@ CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, s
  * total_k], or are more than 2^20 rows apart is CRISP_ERR_BOUNDS and counts as
  * empty, and so does one that begins in cu_q before the end of an earlier one
  * whose sums do none of that: their rows are left as they were. Precision: products of bf16 in fp32, p
- * rounded to bf16 (2^-8 of itself) for the product with v, sums in fp32. The
- * result does not depend on timing. */
+ * rounded to bf16 (2^-8 of itself) for the product with v, sums in fp32. Scores
+ * scale * q_i . k_j that are finite stay below 2^30 in magnitude (beyond, fp32 no
+ * longer tells a row's scores from its largest one's by an exponent). A row that
+ * sees keys, all of them with a score of -inf, becomes zeros. The result does not
+ * depend on timing. */
 CRISP_API crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,
                                             const crisp_tokens* v, const crisp_tokens* out, void* ws, size_t ws_bytes,
                                             crisp_stream_t stream);

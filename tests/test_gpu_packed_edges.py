@@ -104,6 +104,49 @@ def test_values_that_are_not_finite_beside_sums_out_of_range(value):
         assert torch.isnan(hit).all() if value != value else (hit == value).all()
 
 
+@pytest.mark.parametrize("nq,nk", [(200, 200), (5, 5000)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power", [10, 18, 24, 28, 32])
+def test_scores_up_to_the_largest(nq, nk, sign, power):
+    # scores of one product each, exact, up to the documented 2^30 (2^(power - 2.4)): neighbouring values lie
+    # further apart than an exponential reaches, and a row is the mean of its largest score's values
+    rng = np.random.default_rng(85 + power)
+    q, k, v = inputs(4, 1, nq, nk, 86)
+    q[:], k[:] = 0.0, 0.0
+    # bf16 keys of 128 magnitudes, each a 2^-8 of the next apart at least
+    keys = sign * (128 + rng.integers(0, 128, nk)) / 256.0
+    q[:, :, 0] = bf16(2.0 ** (power - power // 2) * (1.0 + rng.integers(0, 128, (nq, 4)) / 128.0))
+    k[:, 0, 0] = bf16(keys * 2.0 ** (power // 2))
+    got = call(q, k, v, [0, nq], [0, nk], split=nk > 1000)
+    x, y, z = (t.double().numpy() for t in (q[:, :, 0], k[:, 0, 0], v[:, 0]))
+    want = np.zeros((nq, 4, D))
+    tol = np.zeros((nq, 4, D))
+    for i in range(nq):
+        n = nk - nq + i + 1
+        s = x[i][:, None] * y[None, :n] * D ** -0.5
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        want[i] = p @ z[:n]
+        # as in attention(), without an error of the scores: a product of 16 bits is exact, and the factor
+        # scale * log2 e, off by 2^-23 of itself, changes differences of scores by as much
+        tol[i] = 2.0 ** -8 * np.abs(want[i]) + (2.0 ** -8 + 2.0 ** -20 + 2 * (n / 8 + 32) * 2.0 ** -23) * (p @ np.abs(z[:n]))
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("nq,nk,masked", [(200, 200, 70), (5, 5000, 4998)])
+def test_rows_of_minus_infinity_only_become_zeros(nq, nk, masked):
+    # the first keys' scores are -inf: rows that see no others are zeros, and the others go by what they see
+    q, k, v = inputs(4, 1, nq, nk, 94)
+    q[:, :, 0] = 1.0
+    k[:masked, 0, 0] = float("-inf")
+    got = call(q, k, v, [0, nq], [0, nk], split=nk > 1000)
+    zeros = masked - (nk - nq)
+    assert not got[:zeros].any()
+    want, tol = attention(q[zeros:].double().numpy(), *(t[masked:].double().numpy() for t in (k, v)), [nq - zeros],
+                          [nk - masked])
+    check(got[zeros:], want, tol)
+
+
 # ------------------------------------------------------------------- running sums
 def rows_of(cu_q, cu_k, total_q, total_k):
     """Which sequences of any sums count, by the documented rule, on plain numbers."""
