@@ -625,8 +625,9 @@ def kv_reserve(cache, free_pages, num_free, step, ws, keep=None, new_lens=None, 
     [num_pages], num_free int32 [1]), missing ones come from it; the cache's table
     and lens are brought up to date and `step` is filled (cu_new, cu_all, slots,
     positions, runs, all_slots). If too few pages are free, or the step or a
-    sequence has no room, the status word says so and the step takes no tokens.
-    ws: kv_append_workspace_size bytes."""
+    sequence has no room, the status word says so and the step takes no tokens:
+    the packed calls behind it do nothing, but decode_attention goes by lens, which
+    stay as they were. ws: kv_append_workspace_size bytes."""
     sizes = cache.sizes
     batch, _, pages, table, _, i32 = sizes
     _step_of("kv_reserve", step, sizes, cache)

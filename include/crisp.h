@@ -605,7 +605,10 @@ typedef struct crisp_kv_step {
  * stands in several tables must not be given back.
  *
  * Where the step cannot be, the status word says so, cu_new, cu_all and runs become
- * zeros (the calls that follow do nothing), and nothing else changes:
+ * zeros (crisp_kv_append_packed, crisp_kv_gather over cu_all and crisp_packed_prefill,
+ * which go by them, do nothing), and nothing else changes. crisp_decode_attention goes
+ * by cache->lens, which stay: it would attend over the tokens from before the step, so
+ * read the status word before it. The reasons:
  * CRISP_ERR_PAGES if too few pages are free; CRISP_ERR_BOUNDS for a length or
  * new_lens outside [0, 128 * max_pages], a negative keep, more than 128 * max_pages
  * tokens in a sequence, max_new or (where it is not 0) max_all exceeded, num_free outside [0,

@@ -10,7 +10,7 @@ from packed_helpers import B, D, attention, check, dev32, starts
 
 pytestmark = pytest.mark.gpu
 
-OK, BOUNDS = 0, 8
+OK, BOUNDS, PAGES = 0, 8, 9
 
 
 def workspace(nbytes):
@@ -264,3 +264,25 @@ def test_rows_of_a_cache_without_sequences():
     assert crisp.read_status(ws) == OK
     for out in outs:
         assert np.array_equal(out.double().cpu().numpy(), VALUES[codes[slots // B, :, slots % B]] * 2.0)
+
+
+def test_decode_behind_a_refused_step_goes_by_the_lengths_from_before():
+    hq, hkv = 4, 2
+    pools = Pools(5, hkv)
+    cache = pools.cache([[-1] * 4] * 2, [0, 0])
+    free, num = dev32(range(5)), dev32([5])
+    step = crisp.make_kv_step(cache, 600, 1024)
+    ws = workspace(crisp.kv_append_workspace_size(cache))
+    q, k, v = (t.cuda() for t in inputs(hq, hkv, 2, 600, 95))
+    crisp.kv_reserve(cache, free, num, step, ws, new_lens=dev32([300, 200]))
+    crisp.kv_append_packed(cache, step, k, v, ws)
+    dws = workspace(crisp.decode_workspace_size(cache, hq))
+    one = q.unsqueeze(2)
+    before, after = torch.empty_like(one), torch.empty_like(one)
+    crisp.decode_attention(cache, one, before, dws)
+    assert crisp.read_status(ws) == OK
+    crisp.kv_reserve(cache, free, num, step, ws, new_lens=dev32([10, 300]))
+    assert crisp.read_status(ws) == PAGES and pools.lens.tolist() == [300, 200]
+    crisp.kv_append_packed(cache, step, 2 * k, 2 * v, ws)
+    crisp.decode_attention(cache, one, after, dws)
+    assert crisp.read_status(dws) == OK and torch.equal(before, after)
