@@ -676,8 +676,9 @@ def make_packed(hq, hkv, cu_q, cu_k, total_q, total_k, max_k=None, scale=0.0) ->
     """A batch of packed sequences: sequence b has the query rows [cu_q[b], cu_q[b +
     1]) of total_q and the key rows [cu_k[b], cu_k[b + 1]) of total_k (int32 CUDA
     tensors of batch + 1 running sums; the same tensor for whole prompts). max_k:
-    about the longest sequence's keys (None: total_k), for how work is split; no
-    limit. The structure keeps the tensors alive; their contents may change
+    about the longest sequence's keys (None: total_k), for how work is split, no
+    limit; leaving it out where total_k is the room of many sequences costs
+    workspace (packed_workspace_size) and time. The structure keeps the tensors alive; their contents may change
     between calls."""
     import torch
     n = cu_q.shape[0] if cu_q.dim() == 1 else 0

@@ -646,12 +646,19 @@ typedef struct crisp_packed {
   int32_t head_dim;     /* must be 128 */
   int32_t total_q;      /* rows of q and out, at most 2^24 */
   int32_t total_k;      /* rows of k and v, at most 2^24 */
-  int32_t max_k;        /* about the most keys of a sequence (0: total_k): decides how work is split, is no limit */
+  int32_t max_k;        /* about the most keys of a sequence (0: total_k): decides how work is split, and with it
+                           the workspace; no limit */
   float scale;          /* 0: 1/sqrt(128) */
   const int32_t* cu_q;  /* int32 [batch + 1] */
   const int32_t* cu_k;  /* int32 [batch + 1]; may be cu_q */
 } crisp_packed;
 
+/* The status word, and room for the unfinished rows of tiles whose keys are split over
+ * several parts: parts x total_q x hq rows of 520 bytes. The number of parts goes by
+ * total_q, total_k and max_k, not by the lengths on the device. Without max_k a step
+ * with room for many tokens counts as one long sequence: 64 requests of 32/8 heads with
+ * room for 8192 new tokens and 400000 in all take 818 MB, and 256 bytes with a max_k of
+ * 16384. */
 CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, size_t* bytes /* host */);
 
 /* Exact causal softmax attention of every sequence of a batch: with nq and nk its
@@ -665,12 +672,13 @@ CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, s
  * included. A sequence whose running sums descend, leave [0, total_q] or [0,
  * total_k], or are more than 2^20 rows apart is CRISP_ERR_BOUNDS and counts as
  * empty, and so does one that begins in cu_q before the end of an earlier one
- * whose sums do none of that: their rows are left as they were. Precision: products of bf16 in fp32, p
- * rounded to bf16 (2^-8 of itself) for the product with v, sums in fp32. Scores
- * scale * q_i . k_j that are finite stay below 2^30 in magnitude (beyond, fp32 no
- * longer tells a row's scores from its largest one's by an exponent). A row that
- * sees keys, all of them with a score of -inf, becomes zeros. The result does not
- * depend on timing. */
+ * whose sums do none of that: their rows are left as they were. Precision:
+ * products of bf16 in fp32, p rounded to bf16 (2^-8 of itself) for the product
+ * with v, sums in fp32. Scores scale * q_i . k_j that are finite stay below 2^30
+ * in magnitude (beyond, fp32 no longer tells a row's scores from its largest
+ * one's by an exponent). A row that sees keys, all of them with a score of -inf,
+ * becomes zeros. The result does not depend on timing. Calls that may run at the
+ * same time (on two streams, in two captured graphs) take a workspace each. */
 CRISP_API crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,
                                             const crisp_tokens* v, const crisp_tokens* out, void* ws, size_t ws_bytes,
                                             crisp_stream_t stream);

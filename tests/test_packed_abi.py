@@ -173,6 +173,13 @@ def test_workspaces_hold_unfinished_rows_of_split_tiles_only(L):
     assert size(batch=1, hq=32, hkv=8, total_q=40, total_k=131072, max_k=256) == 256
 
 
+def test_the_longest_sequence_bounds_the_workspace(L):
+    # the room of a step is no sequence's length: told the longest one, no tile is split and no rows are held
+    n = ctypes.c_size_t()
+    p = packed(batch=64, hq=32, hkv=8, total_q=8192, total_k=400_000, max_k=16384)
+    assert L.crisp_packed_workspace_size(ref(p), ref(n)) == OK and n.value == 256
+
+
 def make_cache():
     t = lambda *s, **k: torch.zeros(s, **k)  # noqa: E731
     u8, i32 = torch.uint8, torch.int32
