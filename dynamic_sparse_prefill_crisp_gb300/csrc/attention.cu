@@ -62,6 +62,19 @@ struct Bars {
   float xsum[2][kB];     // [chunk][row]: partial row sums (epilogue)
 };
 
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
+  const bool ok = mbar_wait(bar, parity, abort);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Two 16-bit counters (one per slot s = 0, 1) in one register, so that a
+// slot picked at run time costs shifts, not a local-memory array.
+struct SlotCounts {
+  uint32_t v = 0u;
+  __device__ __forceinline__ uint32_t parity(int s) const { return (v >> (16 * s)) & 1u; }
+  __device__ __forceinline__ void inc(int s) { v += 1u << (16 * s); }
+};
+
 // Keys above the row on the diagonal block (key index col0 + e > r) -> -inf.
 __device__ __forceinline__ void mask_diag32(int col0, int r, uint32_t (&sv)[32]) {
 #pragma unroll

@@ -1,5 +1,5 @@
 // Device building blocks of the prefill attention kernels (csrc/attention.cu,
-// csrc/packed.cu): bounded waits of a whole warp, the products of a 64-key
+// csrc/packed.cu): what follows a wait that ran out, the products of a 64-key
 // sub-block, and the softmax arithmetic of 32 scores of a row.
 #pragma once
 
@@ -9,19 +9,6 @@
 namespace crisp {
 
 constexpr float kOverflowSum = 0x1p64f;  // chunk row sum past which a row is redone
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort) {
-  const bool ok = ptx::mbar_wait(bar, parity, abort);
-  return __all_sync(0xffffffffu, ok);
-}
-
-// Two 16-bit counters (one per slot s = 0, 1) in one register, so that a
-// slot picked at run time costs shifts, not a local-memory array.
-struct SlotCounts {
-  uint32_t v = 0u;
-  __device__ __forceinline__ uint32_t parity(int s) const { return (v >> (16 * s)) & 1u; }
-  __device__ __forceinline__ void inc(int s) { v += 1u << (16 * s); }
-};
 
 __device__ __forceinline__ void fail(int* abort, DevStatus* st, uint32_t where) {
   *reinterpret_cast<volatile int*>(abort) = 1;
