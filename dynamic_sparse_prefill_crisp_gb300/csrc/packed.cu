@@ -115,6 +115,8 @@ struct Item {
   int partial;       // other splits hold the rest
 };
 
+constexpr int kTaken = 3 * kD / 32, kOddWords = kTaken + 1;
+
 struct Shared {
   uint64_t q_full, q_empty;
   uint64_t k_full[2], v_full[2], v_empty[2];  // a K slot is free again once s_full of its sub-block completes
@@ -127,7 +129,7 @@ struct Shared {
   uint32_t tmem_base;
   int abort;
   int redo[kRing];       // Redo bits: the slot's item has to be done again
-  uint32_t odd_v[kRing][5];  // of the slot's item, where V was looked through: see guard_v
+  uint32_t odd_v[kRing][kOddWords];  // of the slot's item, where V was looked through: see guard_v
   Item item[kRing], again[kRing];
   float xch[2][2][kB];   // [exchange & 1][chunk][row]: partial row maxima, partial row sums
 };
@@ -297,10 +299,10 @@ __device__ __forceinline__ void note_odd(uint32_t& acc, uint32_t w) {
 // bytes in a row) safe to multiply with p = 0: rows from `seen_end` on are no
 // keys of this tile and become zeros, and in rows from `all_end` on, which some
 // of the tile's rows do not see, elements that are not finite become zero (then
-// odd[kTaken] = 1). odd[c / 32], bit c % 32: a key that all rows see has an element
-// of feature c that is not finite. One warp, eight lanes a row, eight reads in
-// flight; swizzling moves 16-byte pieces inside a row only.
-constexpr int kTaken = kD / 32;
+// odd[kTaken] = 1). Bit f % 32 of odd[kind * 4 + f / 32]: a key that all rows see has an
+// element of feature f that is infinity, minus infinity or NaN (kind 0, 1, 2). One warp,
+// eight lanes a row, eight reads in flight; swizzling moves 16-byte pieces inside a row
+// only.
 __device__ __noinline__ void guard_v(uint8_t* sub, int all_end, int seen_end, int lane, uint32_t* odd) {
   uint8_t* mine = sub + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll 1
@@ -334,7 +336,11 @@ __device__ __noinline__ void guard_v(uint8_t* sub, int all_end, int seen_end, in
       if (which == 0u) continue;
       if (row < all_end) {
         const int feature = half * 64 + ((lane & 7) ^ (row & 7)) * 8 + (e & 3) * 2;
-        atomicOr(&odd[feature / 32], which << feature % 32);
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t h = w >> 16 * x & 0xffffu;
+          const int kind = (h & 0x7fu) != 0u ? 2 : static_cast<int>(h >> 15);
+          if (which >> x & 1u) atomicOr(&odd[kind * 4 + feature / 32], 1u << (feature + x) % 32);
+        }
         continue;
       }
       if (which & 1u) w &= 0xffff0000u;
@@ -366,9 +372,10 @@ __device__ __noinline__ void add_odd(const PackedArgs& a, const Item& it, int64_
 
 // What is left of a row's 64 columns from col0 on, where its results are not all finite or
 // its tile is done again. V may not be finite: the tile is looked through. Where it was,
-// and a result is not finite although what all rows see of its feature is, the sums
-// have left fp32's range. And what guard_v took out is added for the rows that see it
-// (their p is above zero): infinities and NaN, whatever the finite rest is.
+// and a result that is not finite is not what the keys that all rows see make it
+// (infinity, minus infinity, or NaN for NaN and for both), the sums have left fp32's
+// range. And what guard_v took out is added for the rows that see it (their p is above
+// zero): infinities and NaN, whatever the finite rest is.
 __device__ __noinline__ void settle(const PackedArgs& a, const Item& it, int64_t to, int col0, int last, bool odd,
                                     Shared& sh, int slot) {
   const uint32_t* odd_v = sh.odd_v[slot];
@@ -380,7 +387,10 @@ __device__ __noinline__ void settle(const PackedArgs& a, const Item& it, int64_t
 #pragma unroll 1
     for (int e = 0; e < 64; ++e) {
       const float x = partial ? a.part[to + e] : __bfloat162float(a.out[to + e]);
-      found = found || (!(fabsf(x) < INFINITY) && (odd_v[(col0 + e) / 32] >> e % 32 & 1u) == 0u);
+      if (fabsf(x) < INFINITY) continue;
+      auto seen = [&](int kind) { return (odd_v[kind * 4 + (col0 + e) / 32] >> e % 32 & 1u) != 0u; };
+      const bool nan = seen(2) || (seen(0) && seen(1));
+      found = found || (x != x ? !nan : nan || !seen(x > 0.f ? 0 : 1));
     }
     if (found) atomicOr(redo, kOverflow);
   }

@@ -677,8 +677,9 @@ CRISP_API crisp_status crisp_packed_workspace_size(const crisp_packed* packed, s
  * with v, sums in fp32. Scores scale * q_i . k_j that are finite stay below 2^30
  * in magnitude (beyond, fp32 no longer tells a row's scores from its largest
  * one's by an exponent). A row that sees keys, all of them with a score of -inf,
- * becomes zeros. The result does not depend on timing. Calls that may run at the
- * same time (on two streams, in two captured graphs) take a workspace each. */
+ * becomes zeros; v that is not finite may or may not reach a row through a score
+ * of -inf. The result does not depend on timing. Calls that may run at the same
+ * time (on two streams, in two captured graphs) take a workspace each. */
 CRISP_API crisp_status crisp_packed_prefill(const crisp_packed* packed, const crisp_tokens* q, const crisp_tokens* k,
                                             const crisp_tokens* v, const crisp_tokens* out, void* ws, size_t ws_bytes,
                                             crisp_stream_t stream);

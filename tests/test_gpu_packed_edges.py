@@ -104,6 +104,21 @@ def test_values_that_are_not_finite_beside_sums_out_of_range(value):
         assert torch.isnan(hit).all() if value != value else (hit == value).all()
 
 
+@pytest.mark.parametrize("nq,nk", [(300, 300), (5, 5000)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_infinities_beside_sums_out_of_range_of_the_other_sign(nq, nk, value):
+    # all of key 130's value is infinite, behind products of p and the values before it, of scores 40 binary
+    # orders above the first ones, that pass the largest number with the other sign: not NaN
+    q, k, v = inputs(4, 1, nq, nk, 96)
+    q[:, :, 0], q[:, :, 1:] = 1.0, 0.1 * q[:, :, 1:]
+    k[64:, 0, 0] += 40.0 * np.log(2.0) * np.sqrt(D)
+    v = bf16(-np.sign(value) * (1.0 + 0.9 * torch.frac(v.float().abs())) * 2.0 ** 126)
+    v[130] = value
+    got = call(q, k, v, [0, nq], [0, nk], split=nk > 1000).float()
+    first = max(130 - (nk - nq), 0)
+    assert (got[first:] == value).all() and torch.isfinite(got[:first]).all()
+
+
 @pytest.mark.parametrize("nq,nk", [(200, 200), (5, 5000)])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("power", [10, 18, 24, 28, 32])
