@@ -21,8 +21,9 @@
 //
 // Long prompts are bound by the tensor pipe at the rate of its 64-key products (a
 // product's operands come from shared memory at 128 bytes a cycle, 48 cycles where
-// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.20 ms, 1840
-// TFLOP/s, a sub-block 1225 cycles a CTA and 612 an SM.
+// 64 keys' arithmetic takes 32): 16k tokens of 32/8 heads take 1.22 ms, 1800
+// TFLOP/s, a sub-block 1225 cycles a CTA and 612 an SM (1.42 ms in calls back to
+// back, which the power cap holds at 1.5 GHz).
 //
 // The products are csrc/attention.cu's: 64-key sub-blocks, two score buffers in
 // TMEM, the first sub-block's row maximum as the reference. What differs:
@@ -186,7 +187,9 @@ __device__ __noinline__ void drop_early(const PackedArgs& a, int* keys, int* til
 // The order in which the CTAs take the sequences, most keys first (equal ones: in
 // the batch's order): order[i] the i-th one's place in the batch, ranks[i] the
 // tiles of those before it, ranks[batch] all tiles. All threads; keys: room for
-// the batch's key counts, tiles of each beside them (2 ints a sequence).
+// the batch's key counts, tiles of each beside them (2 ints a sequence). Each is compared
+// with each, full or empty: 4 tokens behind 500 take 9.6 us in a batch of 4, 14 among 256
+// slots, 40 among 512, 141 among 1024.
 __device__ __forceinline__ void order_sequences(const PackedArgs& a, int* keys, uint16_t* order, int* ranks) {
   const int padded = div_up(a.batch, 4) * 4;
   int* tiles = keys + padded;

@@ -640,7 +640,8 @@ CRISP_API crisp_status crisp_kv_gather(const crisp_kv_cache* cache, const int32_
                                        void* ws, size_t ws_bytes, crisp_stream_t stream);
 
 typedef struct crisp_packed {
-  int32_t batch;        /* sequences, at most 1024 */
+  int32_t batch;        /* sequences, at most 1024; an empty one costs as much of a call's start as others (5 us of
+                           it with 256, 30 with 512, 131 with 1024) */
   int32_t hq;           /* query heads, at most 4096 */
   int32_t hkv;          /* key/value heads; hq % hkv == 0 */
   int32_t head_dim;     /* must be 128 */
